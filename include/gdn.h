@@ -386,6 +386,156 @@ gdn_status gqa_repeat_tiled(const void *src, void *dst,
                             gdn_dtype dtype, size_t src_bytes, size_t dst_bytes,
                             gdn_stream_t stream);
 
+/*
+ * The operators around the recurrence.  A recurrent layer takes its
+ * projections through gdn_causal_conv, runs a recurrence (gdn_step_record, or
+ * gdn_selective_scan for layers of the state space family), normalises the
+ * result with gdn_gated_norm; gdn_sample draws the tokens whose matches with
+ * a draft are the `accepted` counts of the replay calls.  The conventions
+ * above hold, and:
+ *   - Inputs that a layer has as slices of a wider projection may have
+ *     strides (in elements) on their outer dimensions; the inner dimensions
+ *     are dense.  A stride below the inner size is
+ *     GDN_ERR_INVALID_ARGUMENT.
+ *   - `lengths` ([B] int32, DEVICE memory, or NULL for T) is the number of
+ *     steps that a sequence has; an entry < 0 acts as 0, an entry > T as T.
+ *     Steps at or past it change nothing: y is not written there, and their
+ *     inputs are not used.  To roll a sequence back to an accepted prefix,
+ *     repeat the call from the state before it with lengths = accepted (y may
+ *     be NULL).
+ *   - Pointers need the alignment of their element type unless 16 bytes are
+ *     asked for; 16-byte aligned rows take the vector paths.
+ *   - An output must not overlap an input, except where a call says so.
+ */
+typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+
+/*
+ * gdn_causal_conv -- depthwise causal convolution of W taps with its state.
+ *     y[b,t,c] = act(bias[c] + sum_j weight[c,j] * in[b, t-W+1+j, c])
+ * where in[b,t] is x[b,t] for t >= 0 and state_in[b, W-1+t] for t < 0.
+ *
+ *   x          [B,T,C] dtype, strides x_stride_b, x_stride_t, 1
+ *   weight     [C,W] dtype, tap W-1 on the current step; W from 2 to 8 (else
+ *              GDN_ERR_UNSUPPORTED)
+ *   bias       [C] dtype or NULL
+ *   state_in   [B,W-1,C] dtype, the last W-1 inputs, oldest first, or NULL
+ *              (zeros: the start of a sequence)
+ *   lengths    [B] int32 or NULL
+ *   y          [B,T,C] dtype or NULL (only the state is wanted)
+ *   state_out  [B,W-1,C] dtype or NULL: the last W-1 inputs after the call, a
+ *              bit-exact copy; may be state_in's own buffer
+ * Sums are float32, rounded once.  One kernel.
+ */
+gdn_status gdn_causal_conv(const void *x, const void *weight, const void *bias,
+                           const void *state_in, const int32_t *lengths,
+                           void *y, void *state_out,
+                           int64_t B, int64_t T, int64_t C, int64_t W,
+                           int64_t x_stride_b, int64_t x_stride_t,
+                           gdn_activation activation, gdn_dtype dtype,
+                           gdn_stream_t stream);
+
+/*
+ * gdn_selective_scan -- the selective state space scan with one decay per
+ * head and step.  For every state row s = state[b,h,p,:] (N entries), with
+ * g = h / (H/G) and every step t < lengths[b]:
+ *     dl  = softplus(dt[b,t,h] + dt_bias[h])      (softplus = 0: without it)
+ *     s   <- exp(dl * A[h]) * s + (dl * x[b,t,h,p]) * B[b,t,g,:]
+ *     y[b,t,h,p] = s . C[b,t,g,:] + D[h] * x[b,t,h,p]
+ * and state_out[b,h,p,:] = s after the last step.
+ *
+ *   x          [B,T,H,P] dtype      dt       [B,T,H] dtype
+ *   B, C       [B,T,G,N] dtype      A        [H] float32 (negative: a decay)
+ *   D, dt_bias [H] float32 or NULL  lengths  [B] int32 or NULL
+ *   state_in   [B,H,P,N] float32, 16-byte aligned, or NULL (zeros)
+ *   y          [B,T,H,P] dtype or NULL (only the state is wanted)
+ *   state_out  [B,H,P,N] float32, 16-byte aligned, or NULL; may be
+ *              state_in's own buffer
+ *   N          16, 32, 64, 128 or 256 (else GDN_ERR_UNSUPPORTED); P any > 0
+ *   strides    batch and step strides of x, dt, B and C, or NULL (dense)
+ *   workspace  at least gdn_selective_scan_workspace_size bytes, 16-byte
+ *              aligned; not looked at when that call gives 16
+ * The state and all sums are float32 and results do not change from run to
+ * run.  One to three kernels.
+ */
+typedef struct gdn_scan_strides {
+    int64_t x_b, x_t, dt_b, dt_t, B_b, B_t, C_b, C_t;
+} gdn_scan_strides;
+
+size_t gdn_selective_scan_workspace_size(int64_t B, int64_t T, int64_t H, int64_t P,
+                                         int64_t N);
+
+gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A,
+                              const void *Bm, const void *Cm, const float *D,
+                              const float *dt_bias, const float *state_in,
+                              const int32_t *lengths, void *y, float *state_out,
+                              int64_t B, int64_t T, int64_t H, int64_t P,
+                              int64_t G, int64_t N,
+                              const gdn_scan_strides *strides, int softplus,
+                              void *workspace, size_t workspace_bytes,
+                              gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * gdn_gated_norm -- root-mean-square norm with a gate and a residual sum.
+ * For every token m and head k, over D entries:
+ *     u = x                       (gate_first: u = x * silu(gate))
+ *     u = residual + residual_scale * u      (with a residual)
+ *     residual_out = u
+ *     y = u / sqrt(mean(u^2) + eps) * weight (gate, not first: * silu(gate))
+ * The norm takes u in float32, before it is rounded to residual_out.
+ *
+ *   x             [M,K,D] dtype, token stride x_stride_m
+ *   gate          [M,K,D] dtype, token stride gate_stride_m, or NULL
+ *   weight        [weight_rows,D] dtype; weight_rows is 1 (shared by the
+ *                 heads) or K
+ *   residual      [M,K,D] dtype or NULL; residual_out with it, else NULL
+ *   y             [M,K,D] dtype
+ * y and residual_out may each be the dense buffer of x, gate or residual.
+ * One kernel.
+ */
+gdn_status gdn_gated_norm(const void *x, const void *weight, const void *gate,
+                          const void *residual, void *y, void *residual_out,
+                          int64_t M, int64_t K, int64_t D, int64_t x_stride_m,
+                          int64_t gate_stride_m, int64_t weight_rows,
+                          int gate_first, float residual_scale, float eps,
+                          gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * gdn_sample -- one token per row of logits, from given noise.
+ *
+ * With max the row's largest logit and e_i = exp((l_i - max) / temperature),
+ * the tokens in the order (l descending, index ascending) are cut three
+ * times, each time to a prefix that holds the first token at least:
+ *     top_k  the first top_k tokens (<= 0 or >= V: all)
+ *     top_p  a token stays while the mass of those before it is below top_p
+ *            times the mass of the top_k tokens (>= 1: all)
+ *     min_p  tokens with e_i >= min_p (<= 0: all)
+ * token[r] is then the largest e_i / noise[r,i], ties to the lowest index:
+ * with independent standard exponential noise, token i comes out with
+ * probability e_i over the mass of the tokens that are left.  A temperature
+ * of 0 or less takes the largest logit (lowest index), whatever the noise,
+ * and 1 stands in its place for logprob.
+ * logprob[r] = (l - max)/temperature - log(sum of e_i over the whole row).
+ *
+ *   logits   [R,V] dtype, row stride logits_stride; V at most 2^22.  A NaN
+ *            counts as -inf (a masked token), +inf as the largest float.
+ *   noise    [R,V] float32, row stride noise_stride; > 0 (anything else
+ *            counts as the smallest normal float)
+ *   temperature, top_k, top_p, min_p  [R] DEVICE memory, or NULL: then the
+ *            *_all value holds for every row
+ *   token    [R] int32; -1 in a row whose logits are all -inf
+ *   logprob  [R] float32 or NULL; -inf in such a row
+ * Masses are summed as integers and ties are broken by index, so results do
+ * not change from run to run.  One kernel.
+ */
+gdn_status gdn_sample(const void *logits, const float *noise,
+                      const float *temperature, const int32_t *top_k,
+                      const float *top_p, const float *min_p,
+                      float temperature_all, int32_t top_k_all,
+                      float top_p_all, float min_p_all,
+                      int32_t *token, float *logprob, int64_t R, int64_t V,
+                      int64_t logits_stride, int64_t noise_stride,
+                      gdn_dtype dtype, gdn_stream_t stream);
+
 /* Static name of a status code ("GDN_OK", ...); never NULL. */
 const char *gdn_status_string(gdn_status status);
 

@@ -30,6 +30,16 @@ Entry points (same names as the C ABI):
   sequence (an int32 device tensor).
 * ``gqa_repeat_tiled`` -- ``dst[t,h,k] = src[t,h%hg,k]``, "mlx-native
   repeat_tiled.rs".
+
+The operators around the recurrence (``layer.py``, re-exported here):
+
+* ``gdn_causal_conv`` -- the short causal convolution in front of a
+  recurrence, with its state, for prompts, draft tokens and single tokens.
+* ``gdn_selective_scan`` -- the selective state space scan (one decay per head
+  and step) over prompts, draft tokens and single tokens.
+* ``gdn_gated_norm`` -- root-mean-square norm with gate and residual sum.
+* ``gdn_sample`` -- temperature, top-k, top-p and min-p sampling from given
+  noise.
 """
 from __future__ import annotations
 
@@ -48,6 +58,8 @@ __all__ = ["GdnError", "build", "load", "lib_path", "gdn_step_record", "gdn_step
            "gdn_chunk_replay", "gdn_chunk_replay_workspace_size",
            "gdn_step_record_tstate", "gdn_state_replay_tstate",
            "gdn_state_replay", "gdn_state_replay_per_seq", "gqa_repeat_tiled", "RecordOutputs",
+           "gdn_causal_conv", "gdn_selective_scan", "gdn_selective_scan_workspace_size",
+           "gdn_gated_norm", "gdn_sample", "ConvOutputs", "ScanOutputs", "NormOutputs", "SampleOutputs",
            "STATUS_NAMES", "DTYPE_CODES", "GQA_MAPPINGS"]
 
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -58,7 +70,9 @@ EXPORTED = ("gdn_step_record", "gdn_step_record_mapped", "gdn_chunk_prefill",
             "gdn_chunk_prefill_workspace_size", "gdn_chunk_prefill_noalloc", "gdn_chunk_replay",
             "gdn_chunk_replay_workspace_size", "gdn_step_record_tstate",
             "gdn_state_replay_tstate", "gdn_state_replay",
-            "gdn_state_replay_per_seq", "gqa_repeat_tiled", "gdn_status_string",
+            "gdn_state_replay_per_seq", "gqa_repeat_tiled", "gdn_causal_conv",
+            "gdn_selective_scan_workspace_size", "gdn_selective_scan", "gdn_gated_norm",
+            "gdn_sample", "gdn_status_string",
             "gdn_last_error", "gdn_abi_version", "gdn_wait_status", "gdn_set_wait_bound",
             "gdn_inject_wait_expiry", "gdn_force_launch_failures")
 
@@ -114,6 +128,19 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.gqa_repeat_tiled.argtypes = [_P, _P] + [_I] * 4 + [ctypes.c_int, ctypes.c_size_t,
                                                             ctypes.c_size_t, _P]
     lib.gqa_repeat_tiled.restype = ctypes.c_int
+    lib.gdn_causal_conv.argtypes = [_P] * 7 + [_I] * 6 + [ctypes.c_int] * 2 + [_P]
+    lib.gdn_causal_conv.restype = ctypes.c_int
+    lib.gdn_selective_scan_workspace_size.argtypes = [_I] * 5
+    lib.gdn_selective_scan_workspace_size.restype = ctypes.c_size_t
+    lib.gdn_selective_scan.argtypes = [_P] * 11 + [_I] * 6 + [_P, ctypes.c_int, _P, ctypes.c_size_t,
+                                                            ctypes.c_int, _P]
+    lib.gdn_selective_scan.restype = ctypes.c_int
+    lib.gdn_gated_norm.argtypes = [_P] * 6 + [_I] * 6 + [ctypes.c_int, ctypes.c_float, ctypes.c_float,
+                                                       ctypes.c_int, _P]
+    lib.gdn_gated_norm.restype = ctypes.c_int
+    lib.gdn_sample.argtypes = [_P] * 6 + [ctypes.c_float, ctypes.c_int32, ctypes.c_float, ctypes.c_float] + \
+        [_P] * 2 + [_I] * 4 + [ctypes.c_int, _P]
+    lib.gdn_sample.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -462,3 +489,7 @@ def force_launch_failures(n: int) -> None:
     with GDN_ERR_CUDA before touching the device (C entry point
     gdn_force_launch_failures)."""
     _check(load().gdn_force_launch_failures(int(n)), "gdn_force_launch_failures")
+
+
+from .layer import (ConvOutputs, NormOutputs, SampleOutputs, ScanOutputs, gdn_causal_conv,  # noqa: E402
+                    gdn_gated_norm, gdn_sample, gdn_selective_scan, gdn_selective_scan_workspace_size)

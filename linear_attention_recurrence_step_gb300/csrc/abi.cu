@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <string>
 
+#include "abi_util.h"
 #include "gdn.h"
 #include "launch.h"
 #include "record.cuh"
@@ -19,6 +20,17 @@
 namespace {
 
 thread_local std::string g_last_error;
+
+// Testing hooks (gdn_force_launch_failures, gdn_set_wait_bound).
+constexpr long long kDefaultWaitBound = 2000000000ll;  // clock cycles, about a second
+std::atomic<int> g_forced_failures{0};
+std::atomic<long long> g_wait_bound{kDefaultWaitBound};
+std::atomic<int> g_inject_expiry{0};
+
+}  // namespace
+
+namespace gdn {
+namespace abi {
 
 gdn_status fail(gdn_status st, const char *fmt, ...) {
     char buf[512];
@@ -35,37 +47,10 @@ gdn_status ok() {
     return GDN_OK;
 }
 
-bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
-
-// Product of dims (all > 0) times elem_bytes, or -1 on overflow.
-int64_t nbytes(std::initializer_list<int64_t> dims, int64_t elem_bytes) {
-    int64_t acc = elem_bytes;
-    for (int64_t d : dims)
-        if (!mul_ok(acc, d, &acc)) return -1;
-    return acc;
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
-int elem_bytes(gdn_dtype dt) {
-    switch (dt) {
-    case GDN_DTYPE_F32: return 4;
-    case GDN_DTYPE_BF16: return 2;
-    case GDN_DTYPE_F16: return 2;
-    }
-    return 0;
-}
-
 gdn_status cuda_fail(const char *fn, const char *what, cudaError_t e) {
     return fail(GDN_ERR_CUDA, "%s: %s: %s (%s)", fn, what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-// SM count of the current device (0 if it cannot be read).
 int current_sm_count(cudaError_t *err) {
     int dev = 0, sms = 0;
     *err = cudaGetDevice(&dev);
@@ -74,15 +59,6 @@ int current_sm_count(cudaError_t *err) {
     return sms;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Testing hooks (gdn_force_launch_failures, gdn_set_wait_bound).
-constexpr long long kDefaultWaitBound = 2000000000ll;  // clock cycles, about a second
-std::atomic<int> g_forced_failures{0};
-std::atomic<long long> g_wait_bound{kDefaultWaitBound};
-std::atomic<int> g_inject_expiry{0};
-
-// Consume one forced failure, if any is pending.
 bool take_forced_failure() {
     int n = g_forced_failures.load();
     while (n > 0)
@@ -94,7 +70,10 @@ gdn_status forced_failure(const char *fn) {
     return cuda_fail(fn, "launch (forced by gdn_force_launch_failures)", cudaErrorLaunchFailure);
 }
 
-}  // namespace
+}  // namespace abi
+}  // namespace gdn
+
+using namespace gdn::abi;
 
 namespace gdn {
 

@@ -1,0 +1,162 @@
+// causal_conv.cu -- the short depthwise causal convolution in front of a
+// recurrence, with the last W-1 inputs of a sequence as its state:
+//     y[b,t,c] = act(bias[c] + sum_j weight[c,j] in[b, t-W+1+j, c])
+// where in[b,t] is x[b,t] for t >= 0 and state_in[b, W-1+t] before it.
+//
+// Bound by memory: every input is read once and every output written once
+// (2 W + 4 operations per element).  A thread owns one 16-byte piece of
+// channels and a run of consecutive steps; the window of W-1 earlier inputs
+// stays in its registers, so a run re-reads only the W-1 steps before it.
+// Sums are f32 and rounded once.
+#include "pieces.cuh"
+#include "layer.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kConvBatch = 4;   // steps whose loads are issued together
+
+// blockIdx.x: (sequence, run of steps, block of channel pieces), channels
+// innermost.
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, int run, int64_t runs,
+                                                            int64_t cblocks) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t blk = blockIdx.x;
+    const int64_t cb = blk % cblocks, rb = blk / cblocks;
+    const int64_t r = rb % runs, b = rb / runs;
+    const int64_t c = (cb * kConvThreads + threadIdx.x) * VEC;
+    if (c >= a.C) return;
+    const T *x = static_cast<const T *>(a.x) + b * a.x_sb + c;
+    const T *sin = a.state_in ? static_cast<const T *>(a.state_in) + b * (W - 1) * a.C + c : nullptr;
+    int64_t len = a.T;
+    if (a.lengths) {
+        const int64_t n = a.lengths[b];
+        len = n < 0 ? 0 : (n < a.T ? n : a.T);
+    }
+    const int64_t t0 = r * run;
+    const int64_t t1 = t0 + run < len ? t0 + run : len;
+
+    float w[W][VEC], bias[VEC];
+    {
+        const T *wp = static_cast<const T *>(a.weight) + c * W;
+#pragma unroll
+        for (int p = 0; p < W; ++p) {  // VEC * W consecutive taps, VEC at a time
+            float piece[VEC];
+            load_piece<T, VEC>(piece, wp + p * VEC);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[(p * VEC + i) % W][(p * VEC + i) / W] = piece[i];
+        }
+        if (a.bias) load_piece<T, VEC>(bias, static_cast<const T *>(a.bias) + c);
+        else
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) bias[i] = 0.f;
+    }
+
+    // win[j]: the input W-1-j steps before the current one
+    float win[W - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t t = t0 - (W - 1) + j;
+        if (t >= 0) load_piece<T, VEC>(win[j], x + t * a.x_st);
+        else if (sin) load_piece<T, VEC>(win[j], sin + (W - 1 + t) * a.C);
+        else
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+    }
+    // the first run's thread also writes the new state, a copy of inputs: it
+    // alone reads state_in at its channels and has done so before it writes,
+    // so state_out may be state_in
+    if (a.state_out && r == 0) {
+        T *so = static_cast<T *>(a.state_out) + b * (W - 1) * a.C + c;
+        RawPiece<T, VEC> next[W - 1];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            const int64_t t = len - (W - 1) + j;
+            if (t >= 0) next[j] = load_raw<T, VEC>(x + t * a.x_st);
+            else if (sin) next[j] = load_raw<T, VEC>(sin + (W - 1 + t) * a.C);
+            else next[j] = RawPiece<T, VEC>{};
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) store_raw<T, VEC>(so + j * a.C, next[j]);
+    }
+    if (!a.y) return;
+    T *y = static_cast<T *>(a.y) + (b * a.T) * a.C + c;
+    for (int64_t t = t0; t < t1; t += kConvBatch) {
+        RawPiece<T, VEC> raw[kConvBatch];
+#pragma unroll
+        for (int k = 0; k < kConvBatch; ++k)
+            if (t + k < t1) raw[k] = load_raw<T, VEC>(x + (t + k) * a.x_st);
+#pragma unroll
+        for (int k = 0; k < kConvBatch; ++k) {
+            if (t + k < t1) {
+                float in[VEC], out[VEC];
+                widen<T, VEC>(in, raw[k]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    float s = bias[i];
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
+                    s = fmaf(w[W - 1][i], in[i], s);
+                    out[i] = a.silu ? silu(s) : s;
+                }
+                store_piece<T, VEC>(y + (t + k) * a.C, out);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+                    for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+                    win[W - 2][i] = in[i];
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int VEC, int W>
+cudaError_t launch_w(const ConvArgs &a, int sm_count, cudaStream_t s) {
+    const int64_t cblocks = (a.C + (int64_t)kConvThreads * VEC - 1) / ((int64_t)kConvThreads * VEC);
+    // steps per thread: up to 32, fewer while there are not four blocks per SM
+    int run = 32;
+    const int64_t want = 4 * (int64_t)(sm_count > 0 ? sm_count : 152);
+    if (!a.y || a.T <= 8) run = 8;
+    while (run > 8 && a.B * cblocks * ((a.T + run - 1) / run) < want) run /= 2;
+    const int64_t runs = a.y ? (a.T + run - 1) / run : 1;
+    const int64_t blocks = a.B * runs * cblocks;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_dependent(conv_kernel<T, VEC, W>, (unsigned)blocks, kConvThreads, 0, s, a, run, runs, cblocks);
+}
+
+template <typename T, int VEC>
+cudaError_t launch_v(const ConvArgs &a, int sm_count, cudaStream_t s) {
+    switch (a.W) {
+    case 2: return launch_w<T, VEC, 2>(a, sm_count, s);
+    case 3: return launch_w<T, VEC, 3>(a, sm_count, s);
+    case 4: return launch_w<T, VEC, 4>(a, sm_count, s);
+    case 5: return launch_w<T, VEC, 5>(a, sm_count, s);
+    case 6: return launch_w<T, VEC, 6>(a, sm_count, s);
+    case 7: return launch_w<T, VEC, 7>(a, sm_count, s);
+    case 8: return launch_w<T, VEC, 8>(a, sm_count, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t launch_t(const ConvArgs &a, int sm_count, cudaStream_t s) {
+    return a.vec ? launch_v<T, 16 / sizeof(T)>(a, sm_count, s) : launch_v<T, 1>(a, sm_count, s);
+}
+
+}  // namespace
+
+cudaError_t launch_causal_conv(DType dt, const ConvArgs &a, int sm_count, cudaStream_t s) {
+    switch (dt) {
+    case DType::F32: return launch_t<float>(a, sm_count, s);
+    case DType::BF16: return launch_t<__nv_bfloat16>(a, sm_count, s);
+    case DType::F16: return launch_t<__half>(a, sm_count, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -1,0 +1,98 @@
+// pieces.cuh -- loads and stores of VEC neighbouring elements as f32, and the
+// gate function, shared by the operators around the recurrence.  A piece of
+// 16 bytes is one vector access (its address is 16-byte aligned); others go
+// element by element.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn {
+
+// Two neighbouring elements from one 32-bit word, and back.
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    // bf16 -> f32 is exact: the bf16 bits are the top half of the f32 bits
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The raw bits of a piece, so that loads can be issued ahead of their use.
+template <typename T, int VEC> struct RawPiece;
+template <> struct RawPiece<float, 4> { uint4 w; };
+template <> struct RawPiece<__nv_bfloat16, 8> { uint4 w; };
+template <> struct RawPiece<__half, 8> { uint4 w; };
+template <> struct RawPiece<float, 1> { float w; };
+template <> struct RawPiece<__nv_bfloat16, 1> { __nv_bfloat16 w; };
+template <> struct RawPiece<__half, 1> { __half w; };
+
+template <typename T, int VEC>
+__device__ __forceinline__ RawPiece<T, VEC> load_raw(const T *p) {
+    RawPiece<T, VEC> r;
+    if constexpr (VEC == 1) r.w = *p;
+    else r.w = *reinterpret_cast<const uint4 *>(p);
+    return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(T *p, const RawPiece<T, VEC> &r) {
+    if constexpr (VEC == 1) *p = r.w;
+    else *reinterpret_cast<uint4 *>(p) = r.w;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(float (&v)[VEC], const RawPiece<T, VEC> &r) {
+    if constexpr (VEC == 1) {
+        v[0] = Elem<T>::to_f32(r.w);
+    } else if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(r.w.x);
+        v[1] = __uint_as_float(r.w.y);
+        v[2] = __uint_as_float(r.w.z);
+        v[3] = __uint_as_float(r.w.w);
+    } else {
+        const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2<T>(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_piece(float (&v)[VEC], const T *p) {
+    widen<T, VEC>(v, load_raw<T, VEC>(p));
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_piece(T *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        st_from_f32(p, v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint4 w;
+        w.x = pack2<T>(v[0], v[1]);
+        w.y = pack2<T>(v[2], v[3]);
+        w.z = pack2<T>(v[4], v[5]);
+        w.w = pack2<T>(v[6], v[7]);
+        *reinterpret_cast<uint4 *>(p) = w;
+    }
+}
+
+// x * sigmoid(x).  __expf and __fdividef are within a few units in the last
+// place here; exp overflowing to infinity gives the limit, -0.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+}  // namespace gdn

@@ -1,0 +1,304 @@
+// selective_scan.cu -- the selective state space scan, one scalar decay per
+// head and step:
+//     dl    = softplus(dt[b,t,h] + dt_bias[h])      (or dt + dt_bias)
+//     s    <- exp(dl * A[h]) * s + (dl * x[b,t,h,p]) * B[b,t,g,:]
+//     y     = s . C[b,t,g,:] + D[h] * x[b,t,h,p]
+// for every state row s = state[b,h,p,:] (f32, N entries), g = h / (H/G).
+//
+// Step form (this file): a row's N entries lie in the registers of LR lanes,
+// a lane holds VPL of them for each of RPL rows.  One call reads and writes
+// the state once; the rows of up to kStage steps wait in shared memory.  A
+// call of few steps is bound by the state's bytes.  A long call with few
+// heads is split along the steps: a first kernel folds every segment (the
+// first from state_in, the others from zero) into its end state and its total
+// decay, a second one starts each segment from the fold of those before it.
+#include "layer.h"
+#include "pieces.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kStage = 16;      // steps staged in shared memory at a time
+constexpr int kScanWarps = 4;   // most warps per CTA
+
+template <int N> struct ScanShape {
+    static constexpr int LR = N >= 32 ? 8 : 4;        // lanes per row
+    static constexpr int VPL = N / LR;                // entries per lane and row
+    static constexpr int RPL = N >= 256 ? 2 : 4;      // rows per lane
+    static constexpr int RW = 32 / LR;                // rows side by side in a warp
+    static constexpr int kWarpRows = RW * RPL;
+};
+
+enum ScanPhase { kScanWhole = 0, kScanFold = 1, kScanOutput = 2 };
+
+// workspace: end states [segments][B][H][P][N], then decays [segments][B][H]
+template <typename T, int N>
+__global__ void __launch_bounds__(kScanWarps * 32)
+scan_step_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
+    using S = ScanShape<N>;
+    constexpr int LR = S::LR, VPL = S::VPL, RPL = S::RPL, RW = S::RW, WR = S::kWarpRows;
+    constexpr int NV4 = VPL / 4;  // float4 groups per lane and row: entries j*4*LR + lane*4
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    const int warps = blockDim.x / 32, rows_cta = warps * WR;
+    float *sB = reinterpret_cast<float *>(smem_raw);      // [kStage][N]
+    float *sC = sB + kStage * N;                          // [kStage][N]
+    float *sx = sC + kStage * N;                          // [kStage][rows_cta]: x
+    float *sg = sx + kStage * rows_cta;                   // [kStage] decay
+    float *sd = sg + kStage;                              // [kStage] step
+    pdl_trigger();
+    pdl_wait();
+
+    const int64_t rb = blockIdx.x % row_blocks;
+    int64_t rest = blockIdx.x / row_blocks;
+    const int64_t h = rest % a.H;
+    rest /= a.H;
+    const int64_t b = rest % a.B;
+    const int64_t seg = rest / a.B;
+    const int64_t g = h / (a.H / a.G);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int sub = lane % LR, grp = lane / LR;
+    const int64_t p0 = rb * rows_cta + warp * WR + grp;   // row of pass r: p0 + r * RW
+    const int64_t tile = (b * a.H + h) * a.P * N;
+    const int64_t tiles = a.B * a.H * a.P * N;
+
+    int64_t len = a.T;
+    if (a.lengths) {
+        const int64_t n = a.lengths[b];
+        len = n < 0 ? 0 : (n < a.T ? n : a.T);
+    }
+    const int64_t t_begin = seg * a.seg_steps;
+    int64_t t_end = t_begin + a.seg_steps;
+    if (t_end > len) t_end = len;
+
+    float4 s[RPL][NV4];
+#pragma unroll
+    for (int r = 0; r < RPL; ++r) {
+        const int64_t p = p0 + r * RW;
+#pragma unroll
+        for (int j = 0; j < NV4; ++j) {
+            s[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int64_t off = tile + p * N + j * 4 * LR + sub * 4;
+            if (p < a.P) {
+                if (seg == 0) {
+                    if (a.state_in) s[r][j] = *reinterpret_cast<const float4 *>(a.state_in + off);
+                } else if (phase == kScanOutput) {
+                    // the state that this segment starts from
+                    const float *dec = a.workspace + (int64_t)a.segments * tiles + b * a.H + h;
+                    float4 v = *reinterpret_cast<const float4 *>(a.workspace + off);
+                    for (int64_t i = 1; i < seg; ++i) {
+                        const float d = dec[i * a.B * a.H];
+                        const float4 e = *reinterpret_cast<const float4 *>(a.workspace + i * tiles + off);
+                        v.x = fmaf(d, v.x, e.x);
+                        v.y = fmaf(d, v.y, e.y);
+                        v.z = fmaf(d, v.z, e.z);
+                        v.w = fmaf(d, v.w, e.w);
+                    }
+                    s[r][j] = v;
+                }
+                // the first segment writes the call's state: it alone reads
+                // state_in, which may be the same buffer
+                if (phase == kScanOutput && seg == 0 && a.state_out) {
+                    const float *dec = a.workspace + (int64_t)a.segments * tiles + b * a.H + h;
+                    float4 v = *reinterpret_cast<const float4 *>(a.workspace + off);
+                    for (int64_t i = 1; i < a.segments; ++i) {
+                        const float d = dec[i * a.B * a.H];
+                        const float4 e = *reinterpret_cast<const float4 *>(a.workspace + i * tiles + off);
+                        v.x = fmaf(d, v.x, e.x);
+                        v.y = fmaf(d, v.y, e.y);
+                        v.z = fmaf(d, v.z, e.z);
+                        v.w = fmaf(d, v.w, e.w);
+                    }
+                    *reinterpret_cast<float4 *>(a.state_out + off) = v;
+                }
+            }
+        }
+    }
+    if (phase == kScanOutput && !a.y) return;
+
+    const float Ah = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const T *x = static_cast<const T *>(a.x) + b * a.x_sb + h * a.P;
+    const T *dtp = static_cast<const T *>(a.dt) + b * a.dt_sb + h;
+    const T *Bp = static_cast<const T *>(a.Bm) + b * a.b_sb + g * N;
+    const T *Cp = static_cast<const T *>(a.Cm) + b * a.c_sb + g * N;
+    const bool out = phase != kScanFold && a.y != nullptr;
+    float decay = 1.f;
+
+    for (int64_t t0 = t_begin; t0 < t_end; t0 += kStage) {
+        const int n = (int)(t_end - t0 < kStage ? t_end - t0 : kStage);
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * N; i += blockDim.x) {
+            const int t = i / N, c = i % N;
+            sB[i] = ld_f32(Bp + (t0 + t) * a.b_st + c);
+            if (out) sC[i] = ld_f32(Cp + (t0 + t) * a.c_st + c);
+        }
+        for (int i = threadIdx.x; i < n * rows_cta; i += blockDim.x) {
+            const int t = i / rows_cta, p = i % rows_cta;
+            sx[i] = rb * rows_cta + p < a.P ? ld_f32(x + (t0 + t) * a.x_st + rb * rows_cta + p) : 0.f;
+        }
+        if (threadIdx.x < n) {
+            float d = ld_f32(dtp + (t0 + threadIdx.x) * a.dt_st) + bias;
+            if (a.softplus) d = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d)));
+            sd[threadIdx.x] = d;
+            sg[threadIdx.x] = expf(d * Ah);
+        }
+        __syncthreads();
+        for (int t = 0; t < n; ++t) {
+            const float gt = sg[t], dl = sd[t];
+            decay *= gt;
+            float xv[RPL], acc[RPL];
+#pragma unroll
+            for (int r = 0; r < RPL; ++r) {
+                xv[r] = sx[t * rows_cta + warp * WR + grp + r * RW];
+                acc[r] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < NV4; ++j) {
+                const float4 Bv = *reinterpret_cast<const float4 *>(sB + t * N + j * 4 * LR + sub * 4);
+                float4 Cv = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (out) Cv = *reinterpret_cast<const float4 *>(sC + t * N + j * 4 * LR + sub * 4);
+#pragma unroll
+                for (int r = 0; r < RPL; ++r) {
+                    const float dx = dl * xv[r];
+                    const float2 dx2 = make_float2(dx, dx), g2 = make_float2(gt, gt);
+                    const float2 lo = ffma2(g2, lo2(s[r][j]), fmul2(dx2, lo2(Bv)));
+                    const float2 hi = ffma2(g2, hi2(s[r][j]), fmul2(dx2, hi2(Bv)));
+                    s[r][j] = cat4(lo, hi);
+                    if (out) {
+                        float2 z = fmul2(lo, lo2(Cv));
+                        z = ffma2(hi, hi2(Cv), z);
+                        acc[r] += z.x + z.y;
+                    }
+                }
+            }
+            if (out) {
+                // the lanes of a row share its sum out: half of the rows go to
+                // each side until a lane holds one row, then plain exchanges
+                int row = 0, left = RPL;
+#pragma unroll
+                for (int o = LR / 2; o > 0; o >>= 1) {
+                    if (left > 1) {
+                        const int half = left / 2;
+                        const bool up = (sub & o) != 0;
+#pragma unroll
+                        for (int i = 0; i < RPL / 2; ++i)
+                            if (i < half) {
+                                const float send = up ? acc[i] : acc[i + half];
+                                const float keep = up ? acc[i + half] : acc[i];
+                                acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                            }
+                        row += up ? half : 0;
+                        left = half;
+                    } else {
+                        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+                    }
+                }
+                if constexpr (RPL > LR) static_assert(RPL <= LR, "a lane ends with one row");
+                const int64_t p = p0 + row * RW;
+                const bool writer = (sub & (LR / RPL - 1)) == 0;
+                if (writer && p < a.P) {
+                    const float xr = sx[t * rows_cta + warp * WR + grp + row * RW];
+                    st_from_f32(static_cast<T *>(a.y) + ((b * a.T + t0 + t) * a.H + h) * a.P + p,
+                                fmaf(Dh, xr, acc[0]));
+                }
+            }
+        }
+    }
+
+    if (phase == kScanOutput) return;
+    float *dst = phase == kScanFold ? a.workspace + seg * tiles : a.state_out;
+    if (dst) {
+#pragma unroll
+        for (int r = 0; r < RPL; ++r) {
+            const int64_t p = p0 + r * RW;
+            if (p < a.P)
+#pragma unroll
+                for (int j = 0; j < NV4; ++j)
+                    *reinterpret_cast<float4 *>(dst + tile + p * N + j * 4 * LR + sub * 4) = s[r][j];
+        }
+    }
+    if (phase == kScanFold && rb == 0 && threadIdx.x == 0)
+        a.workspace[(int64_t)a.segments * tiles + (seg * a.B + b) * a.H + h] = decay;
+}
+
+template <int N> int64_t scan_warps(int64_t P, int64_t *row_blocks) {
+    const int64_t w = (P + ScanShape<N>::kWarpRows - 1) / ScanShape<N>::kWarpRows;
+    *row_blocks = (w + kScanWarps - 1) / kScanWarps;
+    return (w + *row_blocks - 1) / *row_blocks;
+}
+
+template <typename T, int N>
+cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
+    int64_t row_blocks;
+    const int warps = (int)scan_warps<N>(a.P, &row_blocks);
+    const size_t smem = (size_t)kStage * (2 * N + warps * ScanShape<N>::kWarpRows + 2) * 4;
+    const int64_t tiles = a.B * a.H * row_blocks;
+    if (tiles * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (a.segments == 1)
+        return launch_dependent(scan_step_kernel<T, N>, (unsigned)tiles, warps * 32, smem, s, a, (int)kScanWhole,
+                                row_blocks);
+    cudaError_t e = launch_dependent(scan_step_kernel<T, N>, (unsigned)(tiles * a.segments), warps * 32, smem, s, a,
+                                     (int)kScanFold, row_blocks);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(scan_step_kernel<T, N>, (unsigned)(a.y ? tiles * a.segments : tiles), warps * 32, smem, s,
+                            a, (int)kScanOutput, row_blocks);
+}
+
+template <typename T>
+cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
+    switch (a.N) {
+    case 16: return launch_n<T, 16>(a, s);
+    case 32: return launch_n<T, 32>(a, s);
+    case 64: return launch_n<T, 64>(a, s);
+    case 128: return launch_n<T, 128>(a, s);
+    case 256: return launch_n<T, 256>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+bool scan_supported_n(int64_t N) { return N == 16 || N == 32 || N == 64 || N == 128 || N == 256; }
+
+ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N) {
+    // enough CTAs for four on each of 152 SMs, segments of 64 steps or more
+    ScanPlan plan{1, T, 0};
+    int64_t row_blocks = 1;
+    switch (N) {
+    case 16: scan_warps<16>(P, &row_blocks); break;
+    case 32: scan_warps<32>(P, &row_blocks); break;
+    case 64: scan_warps<64>(P, &row_blocks); break;
+    case 128: scan_warps<128>(P, &row_blocks); break;
+    case 256: scan_warps<256>(P, &row_blocks); break;
+    }
+    const double ctas = (double)B * (double)H * (double)row_blocks;
+    int64_t want = ctas >= 608.0 ? 1 : (int64_t)(608.0 / ctas);
+    if (want > T / 64) want = T / 64;
+    if (want > 64) want = 64;
+    if (want > 1) {
+        const int64_t steps = ((T + want - 1) / want + kStage - 1) / kStage * kStage;
+        plan.segments = (int)((T + steps - 1) / steps);
+        plan.seg_steps = steps;
+    }
+    if (plan.segments > 1) {
+        int64_t n = 4;
+        for (int64_t d : {(int64_t)plan.segments, B, H})
+            if (__builtin_mul_overflow(n, d, &n)) return ScanPlan{0, 0, -1};
+        const int64_t decays = n;
+        for (int64_t d : {P, N})
+            if (__builtin_mul_overflow(n, d, &n)) return ScanPlan{0, 0, -1};
+        if (__builtin_add_overflow(n, decays, &plan.bytes)) return ScanPlan{0, 0, -1};
+    }
+    return plan;
+}
+
+cudaError_t launch_selective_scan(DType dt, const ScanArgs &a, int, cudaStream_t s) {
+    switch (dt) {
+    case DType::F32: return launch_t<float>(a, s);
+    case DType::BF16: return launch_t<__nv_bfloat16>(a, s);
+    case DType::F16: return launch_t<__half>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn
