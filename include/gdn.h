@@ -517,7 +517,8 @@ gdn_status gdn_gated_norm(const void *x, const void *weight, const void *gate,
  * logprob[r] = (l - max)/temperature - log(sum of e_i over the whole row).
  *
  *   logits   [R,V] dtype, row stride logits_stride; V at most 2^22.  A NaN
- *            counts as -inf (a masked token), +inf as the largest float.
+ *            counts as -inf (a masked token), +inf as the largest
+ *            finite value of its type.
  *   noise    [R,V] float32, row stride noise_stride; > 0 (anything else
  *            counts as the smallest normal float)
  *   temperature, top_k, top_p, min_p  [R] DEVICE memory, or NULL: then the
