@@ -37,7 +37,7 @@ struct ScanArgs {
     int64_t x_sb, x_st, dt_sb, dt_st, b_sb, b_st, c_sb, c_st;
     int N;
     bool softplus;
-    bool vec_bc;                        // B and C rows can be read in 4-element pieces
+    bool chunked;                       // the tensor-core form (scan_chunk.cu)
     int segments;                       // parts that the steps are split into
     int64_t seg_steps;                  // steps per part (the last may be shorter)
 };
@@ -46,8 +46,13 @@ struct ScanPlan {
     int64_t seg_steps;
     int64_t bytes;                      // workspace, -1 on overflow
 };
-ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N);
+ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool chunked);
 bool scan_supported_n(int64_t N);
+// Warps per CTA and CTAs per head of the tensor-core form; whether a call of
+// these sizes takes it (its tensors' alignment permitting).
+int scan_chunk_warps(int64_t P, int64_t *row_blocks);
+bool scan_chunk_sizes(DType dt, int64_t T, int64_t P, int64_t N);
+cudaError_t launch_scan_chunk(const ScanArgs &a, cudaStream_t s);
 cudaError_t launch_selective_scan(DType dt, const ScanArgs &a, int sm_count, cudaStream_t s);
 
 struct NormArgs {

@@ -93,8 +93,9 @@ gdn_status gdn_causal_conv(const void *x, const void *weight, const void *bias, 
 
 size_t gdn_selective_scan_workspace_size(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N) {
     if (B <= 0 || T <= 0 || H <= 0 || P <= 0 || !gdn::scan_supported_n(N)) return 0;
-    const gdn::ScanPlan plan = gdn::scan_plan(B, T, H, P, N);
-    return plan.bytes < 0 ? 0 : (size_t)std::max<int64_t>(plan.bytes, 16);
+    // whichever form the call takes
+    const gdn::ScanPlan p = gdn::scan_plan(B, T, H, P, N, false), q = gdn::scan_plan(B, T, H, P, N, true);
+    return p.bytes < 0 || q.bytes < 0 ? 0 : (size_t)std::max<int64_t>(std::max(p.bytes, q.bytes), 16);
 }
 
 gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, const void *Bm, const void *Cm,
@@ -131,7 +132,11 @@ gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, con
         return fail(GDN_ERR_MISALIGNED, "%s: state_in, state_out and workspace must be 16-byte aligned", fn);
     if (state_in && state_out && state_in != state_out && overlap(state_in, st_b, state_out, st_b))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: state_out overlaps state_in without being the same buffer", fn);
-    const gdn::ScanPlan plan = gdn::scan_plan(B, T, H, P, N);
+    const bool rows16 = aligned(x, 16) && aligned(Bm, 16) && aligned(Cm, 16) && aligned(y, 16) && st.x_t % 8 == 0 &&
+                        st.B_t % 8 == 0 && st.C_t % 8 == 0 &&
+                        (B == 1 || (st.x_b % 8 == 0 && st.B_b % 8 == 0 && st.C_b % 8 == 0));
+    const bool chunked = rows16 && gdn::scan_chunk_sizes(static_cast<gdn::DType>(dtype), T, P, N);
+    const gdn::ScanPlan plan = gdn::scan_plan(B, T, H, P, N, chunked);
     if (plan.bytes < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "%s: tensor sizes overflow int64", fn);
     if (plan.bytes > 0 && (!workspace || workspace_bytes < (size_t)plan.bytes))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: workspace too small: need %lld bytes, have %llu", fn,
@@ -179,6 +184,7 @@ gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, con
     a.c_st = st.C_t;
     a.N = (int)N;
     a.softplus = softplus != 0;
+    a.chunked = chunked;
     a.segments = plan.segments;
     a.seg_steps = plan.seg_steps;
     e = gdn::launch_selective_scan(static_cast<gdn::DType>(dtype), a, sms, reinterpret_cast<cudaStream_t>(stream));

@@ -1,0 +1,464 @@
+// scan_chunk.cu -- the selective scan over long calls in chunks of L = 64
+// steps on the tensor cores (warp-level mma.sync, bf16 operands, f32
+// accumulate).  bf16 inputs, f32 state, N = 64 or 128.
+//
+// Within a chunk, with c_t the sum of the logarithms of the decays up to and
+// including step t, and S the state (rows p, columns n) the chunk starts from,
+//     y_t = exp(c_t) S C_t + sum_{s<=t} W[t][s] x_s + D x_t,
+//           W[t][s] = (C_t . B_s) exp(c_t - c_s) dl_s
+//     S  <- exp(c_L) S + sum_s x_s (exp(c_L - c_s) dl_s) B_s^T
+// so a chunk is four products: C B^T (64 x 64 x N), S C^T (P x 64 x N), x^T W^T
+// (P x 64 x 64, the half below the diagonal) and x^T B (P x N x 64).
+//
+// A CTA owns up to 128 rows p of one head and walks the chunks of its segment
+// in order.  A warp owns 16 rows: their state stays in its registers as the
+// f32 accumulator of the last product, and is, in the same registers, the left
+// operand of the second, so the state never goes through shared memory.  The
+// next chunk's rows of x, B and C arrive by cp.async meanwhile.
+//
+// Precision: x, B and C enter as they are (bf16).  The weighted x, which goes
+// into the state, enters as three bf16 terms (24 significant bits: f32's own),
+// and the state is only ever scaled and added to in f32.  The state and W as
+// operands of y enter as two terms (16 bits): their products carry a relative
+// error of at most 2^-18, a thousandth of what rounding y to bf16 costs.  c_t
+// is summed in f64 and kept as two f32 terms, so that exp(c_t - c_s) loses
+// nothing to a chunk's large |c|.
+//
+// A call with few heads is split along the steps as in selective_scan.cu: a
+// first pass forms the segments' end states (the last product alone), the
+// second starts every segment from the fold of those before it.
+//
+// What bounds it: the tensor pipe, then the barrier after W.  About 390
+// mma.sync per warp and chunk at P = N = 128.
+#include "layer.h"
+#include "pieces.cuh"
+#include "record_mma.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kL = 64;               // steps of a chunk
+constexpr int kWPitch = kL + 8;      // elements between rows of W in shared memory
+
+struct ChunkDecay {
+    float2 c[kL];      // c_t in units of log(2), two terms
+    float dl[kL];
+    float w[kL];       // exp(c_L - c_t) dl_t
+    float ec[kL];      // exp(c_t)
+    float total;       // exp(c_L)
+    float pad[3];
+};
+
+__host__ __device__ constexpr int bc_pitch(int N) { return N + 8; }
+__host__ __device__ constexpr int x_pitch(int warps) { return warps * 16 + 8; }
+
+// Shared memory (bytes): two stages of x, B, C; W (hi, lo); two decay blocks;
+// y tiles, unless they fit over a stage's C
+__host__ __device__ constexpr size_t stage_bytes(int N, int warps) {
+    return (size_t)kL * (x_pitch(warps) + 2 * bc_pitch(N)) * 2;
+}
+__host__ __device__ constexpr bool y_over_c(int N, int warps) { return warps * kL * 16 <= kL * bc_pitch(N); }
+__host__ __device__ constexpr size_t chunk_smem(int N, int warps) {
+    return 2 * stage_bytes(N, warps) + 2 * (size_t)kL * kWPitch * 2 + 2 * sizeof(ChunkDecay) +
+           (y_over_c(N, warps) ? 0 : (size_t)warps * kL * 16 * 2);
+}
+
+__device__ __forceinline__ void stsm_x4_t(void *row, const uint32_t (&r)[4]) {
+    const unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(row));
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 16 bytes, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void *smem, const void *gmem, bool on) {
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(on ? 16 : 0) : "memory");
+}
+// (x0, x1) ~ hi + mid + lo in packed bf16 pairs: all 24 bits of the f32 values.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    hi = pack2<__nv_bfloat16>(x0, x1);
+    const float2 h = unpack2<__nv_bfloat16>(hi);
+    split_bf16x2(x0 - h.x, x1 - h.y, mid, lo);
+}
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// OUT: y is wanted (else only the state: the first pass, and calls without y).
+template <int N, bool OUT>
+__global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
+    using T = __nv_bfloat16;
+    constexpr int NT = N / 8;              // 8-column tiles of the state
+    constexpr int BP = bc_pitch(N);
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int XP = x_pitch(warps);
+    const size_t stage = stage_bytes(N, warps);
+    T *const sW = reinterpret_cast<T *>(smem_raw + 2 * stage);          // hi, then lo
+    T *const sWlo = sW + kL * kWPitch;
+    ChunkDecay *const sdec = reinterpret_cast<ChunkDecay *>(smem_raw + 2 * stage + 2 * kL * kWPitch * 2);
+    T *const sYown = reinterpret_cast<T *>(sdec + 2);
+    auto sx = [&](int b) { return reinterpret_cast<T *>(smem_raw + b * stage); };
+    auto sB = [&](int b) { return sx(b) + kL * XP; };
+    auto sC = [&](int b) { return sB(b) + kL * BP; };
+    pdl_trigger();
+    pdl_wait();
+
+    const int64_t rb = blockIdx.x % row_blocks;
+    int64_t rest = blockIdx.x / row_blocks;
+    const int64_t h = rest % a.H;
+    rest /= a.H;
+    const int64_t b = rest % a.B;
+    const int64_t seg = rest / a.B;
+    const int64_t g = h / (a.H / a.G);
+    const int64_t p_cta = rb * warps * 16;              // first row of the CTA
+    const int rows = (int)(a.P - p_cta < warps * 16 ? a.P - p_cta : warps * 16);
+    const int64_t tile = (b * a.H + h) * a.P * N, tiles = a.B * a.H * a.P * N;
+    const int gr = lane >> 2, tq = lane & 3;            // accumulator row and column pair
+
+    int64_t len = a.T;
+    if (a.lengths) {
+        const int64_t n = a.lengths[b];
+        len = n < 0 ? 0 : (n < a.T ? n : a.T);
+    }
+    const int64_t t_begin = seg * a.seg_steps;
+    const int64_t t_end = t_begin + a.seg_steps < len ? t_begin + a.seg_steps : len;
+    const int chunks = t_end > t_begin ? (int)((t_end - t_begin + kL - 1) / kL) : 0;
+
+    const T *const x = static_cast<const T *>(a.x) + b * a.x_sb + h * a.P + p_cta;
+    const T *const dtp = static_cast<const T *>(a.dt) + b * a.dt_sb + h;
+    const T *const Bp = static_cast<const T *>(a.Bm) + b * a.b_sb + g * N;
+    const T *const Cp = static_cast<const T *>(a.Cm) + b * a.c_sb + g * N;
+    const float A2 = a.A[h] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+
+    // rows past the end, and columns past the head, are zeros
+    auto fetch = [&](int c) {
+        const int64_t t0 = t_begin + (int64_t)c * kL;
+        const int buf = c & 1, n = (int)(t_end - t0 < kL ? t_end - t0 : kL);
+        const int xq = warps * 2;  // 16-byte pieces of an x row
+        for (int i = threadIdx.x; i < kL * xq; i += blockDim.x) {
+            const int t = i / xq, q = i - t * xq;
+            const bool on = t < n && q * 8 < rows;
+            cp_async16_or_zero(sx(buf) + t * XP + q * 8, on ? x + (t0 + t) * a.x_st + q * 8 : x, on);
+        }
+        for (int i = threadIdx.x; i < kL * (N / 8); i += blockDim.x) {
+            const int t = i / (N / 8), q = i % (N / 8);
+            const bool on = t < n;
+            cp_async16_or_zero(sB(buf) + t * BP + q * 8, on ? Bp + (t0 + t) * a.b_st + q * 8 : Bp, on);
+            if (OUT) cp_async16_or_zero(sC(buf) + t * BP + q * 8, on ? Cp + (t0 + t) * a.c_st + q * 8 : Cp, on);
+        }
+        cp_async_commit();
+    };
+    // the decays of a chunk, by one warp (two steps per lane)
+    auto decays = [&](int c) {
+        const int64_t t0 = t_begin + (int64_t)c * kL;
+        ChunkDecay &d = sdec[c & 1];
+        float dl[2];
+        double la[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t t = t0 + 2 * lane + i;
+            dl[i] = 0.f;
+            if (t < t_end) {
+                const float v = ld_f32(dtp + t * a.dt_st) + bias;
+                dl[i] = a.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+            }
+            // a decay below 2^-256 is zero in f32
+            const float l2 = dl[i] * A2;
+            la[i] = l2 < -256.f ? -256.0 : (double)l2;
+        }
+        double sum = la[0] + la[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const double last = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const double ct = i ? sum : sum - la[1];
+            const int t = 2 * lane + i;
+            const float hi = (float)ct;
+            d.c[t] = make_float2(hi, (float)(ct - (double)hi));
+            d.dl[t] = dl[i];
+            d.w[t] = ex2f((float)(last - ct)) * dl[i];
+            d.ec[t] = ex2f(hi);
+        }
+        if (lane == 0) d.total = ex2f((float)last);
+    };
+
+    // the state of the warp's rows: accumulator tiles of 16 x 8
+    float S[NT][4];
+    {
+        const float *ws = a.workspace;
+        const float *dec = ws + (int64_t)a.segments * tiles + b * a.H + h;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int pr = warp * 16 + gr + 8 * r;
+                float2 v = make_float2(0.f, 0.f);
+                if (pr < rows) {
+                    const int64_t off = tile + (p_cta + pr) * N + j * 8 + tq * 2;
+                    if (seg == 0) {
+                        if (a.state_in) v = *reinterpret_cast<const float2 *>(a.state_in + off);
+                    } else if (phase == 2) {
+                        v = *reinterpret_cast<const float2 *>(ws + off);
+                        for (int64_t i = 1; i < seg; ++i) {
+                            const float d = dec[i * a.B * a.H];
+                            const float2 e = *reinterpret_cast<const float2 *>(ws + i * tiles + off);
+                            v.x = fmaf(d, v.x, e.x);
+                            v.y = fmaf(d, v.y, e.y);
+                        }
+                    }
+                    // the first segment writes the call's state: it alone reads
+                    // state_in, which may be the same buffer
+                    if (phase == 2 && seg == 0 && a.state_out) {
+                        float2 s = *reinterpret_cast<const float2 *>(ws + off);
+                        for (int64_t i = 1; i < a.segments; ++i) {
+                            const float d = dec[i * a.B * a.H];
+                            const float2 e = *reinterpret_cast<const float2 *>(ws + i * tiles + off);
+                            s.x = fmaf(d, s.x, e.x);
+                            s.y = fmaf(d, s.y, e.y);
+                        }
+                        *reinterpret_cast<float2 *>(a.state_out + off) = s;
+                    }
+                }
+                S[j][2 * r] = v.x;
+                S[j][2 * r + 1] = v.y;
+            }
+    }
+    if (phase == 2 && !OUT) return;
+
+    float decay = 1.f;
+    const int lr = lane & 7, lm = lane >> 3;            // ldmatrix: row and matrix of this lane's address
+    if (chunks > 0) {
+        fetch(0);
+        if (warp == 0) decays(0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int buf = c & 1;
+        cp_async_wait_all();
+        __syncthreads();
+        if (c + 1 < chunks) {
+            fetch(c + 1);
+            if (warp == (c + 1) % warps) decays(c + 1);
+        }
+        const ChunkDecay &d = sdec[buf];
+        const T *xs = sx(buf), *Bs = sB(buf), *Cs = sC(buf);
+        float Y[kL / 8][4];
+        if constexpr (OUT) {
+            // W, 16 rows t and every other 8-column block of s at a time
+            for (int job = warp; job < 8; job += warps) {
+                const int ti = 3 - job / 2;
+                float G[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) G[i][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk) {
+                    uint32_t ca[4];
+                    ldsm_x4(ca, Cs + (ti * 16 + lr + 8 * (lm & 1)) * BP + kk * 16 + 8 * (lm >> 1));
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        // blocks 2i + job%2 and 2i + 2 + job%2 of s
+                        if (i <= ti) {
+                            uint32_t bb[4];
+                            const int sblk = 2 * (i + (lm >> 1)) + (job & 1);
+                            ldsm_x4(bb, Bs + (min(sblk, 7) * 8 + lr) * BP + kk * 16 + 8 * (lm & 1));
+                            mma_bf16_16816(G[i], ca, bb[0], bb[1]);
+                            mma_bf16_16816(G[i + 1], ca, bb[2], bb[3]);
+                        }
+                    }
+                }
+                const int t0 = ti * 16 + gr;
+                const float2 ca0 = d.c[t0], ca1 = d.c[t0 + 8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i > ti) continue;
+                    const int s0 = (2 * i + (job & 1)) * 8 + tq * 2;
+                    const float2 cs0 = d.c[s0], cs1 = d.c[s0 + 1];
+                    const float dl0 = d.dl[s0], dl1 = d.dl[s0 + 1];
+                    auto wt = [&](float gv, const float2 &ct, const float2 &cs, float dl, int t, int s) {
+                        if (s > t) return 0.f;
+                        const float w = gv * ex2f((ct.x - cs.x) + (ct.y - cs.y)) * dl;
+                        return s == t ? w + Dh : w;
+                    };
+                    uint32_t hi, lo;
+                    split_bf16x2(wt(G[i][0], ca0, cs0, dl0, t0, s0), wt(G[i][1], ca0, cs1, dl1, t0, s0 + 1), hi, lo);
+                    *reinterpret_cast<uint32_t *>(sW + t0 * kWPitch + s0) = hi;
+                    *reinterpret_cast<uint32_t *>(sWlo + t0 * kWPitch + s0) = lo;
+                    split_bf16x2(wt(G[i][2], ca1, cs0, dl0, t0 + 8, s0), wt(G[i][3], ca1, cs1, dl1, t0 + 8, s0 + 1), hi,
+                                 lo);
+                    *reinterpret_cast<uint32_t *>(sW + (t0 + 8) * kWPitch + s0) = hi;
+                    *reinterpret_cast<uint32_t *>(sWlo + (t0 + 8) * kWPitch + s0) = lo;
+                }
+            }
+            // S C^T: the state's accumulators are the left operand
+#pragma unroll
+            for (int j = 0; j < kL / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Y[j][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < N / 16; ++kk) {
+                uint32_t hi[4], lo[4];
+                split_bf16x2(S[2 * kk][0], S[2 * kk][1], hi[0], lo[0]);
+                split_bf16x2(S[2 * kk][2], S[2 * kk][3], hi[1], lo[1]);
+                split_bf16x2(S[2 * kk + 1][0], S[2 * kk + 1][1], hi[2], lo[2]);
+                split_bf16x2(S[2 * kk + 1][2], S[2 * kk + 1][3], hi[3], lo[3]);
+#pragma unroll
+                for (int j = 0; j < kL / 8; j += 2) {
+                    uint32_t cb[4];
+                    ldsm_x4(cb, Cs + ((j + (lm >> 1)) * 8 + lr) * BP + kk * 16 + 8 * (lm & 1));
+                    mma_bf16_16816(Y[j], hi, cb[0], cb[1]);
+                    mma_bf16_16816(Y[j + 1], hi, cb[2], cb[3]);
+                    mma_bf16_16816(Y[j], lo, cb[0], cb[1]);
+                    mma_bf16_16816(Y[j + 1], lo, cb[2], cb[3]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kL / 8; ++j) {
+                const float2 e = *reinterpret_cast<const float2 *>(&d.ec[j * 8 + tq * 2]);
+                Y[j][0] *= e.x;
+                Y[j][1] *= e.y;
+                Y[j][2] *= e.x;
+                Y[j][3] *= e.y;
+            }
+        }
+        {
+            const float total = d.total;
+            decay *= total;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[j][e] *= total;
+        }
+        if (OUT) __syncthreads();  // W is whole; no warp reads this stage's C any more
+#pragma unroll
+        for (int ks = 0; ks < kL / 16; ++ks) {
+            // x^T, rows p of this warp, 16 steps
+            uint32_t xa[4];
+            ldsm_x4_t(xa, xs + (ks * 16 + lr + 8 * (lm >> 1)) * XP + warp * 16 + 8 * (lm & 1));
+            if constexpr (OUT) {
+#pragma unroll
+                for (int j = 2 * ks; j < kL / 8; j += 2) {
+                    uint32_t wb[4];
+                    ldsm_x4(wb, sW + ((j + (lm >> 1)) * 8 + lr) * kWPitch + ks * 16 + 8 * (lm & 1));
+                    mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
+                    mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
+                    ldsm_x4(wb, sWlo + ((j + (lm >> 1)) * 8 + lr) * kWPitch + ks * 16 + 8 * (lm & 1));
+                    mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
+                    mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
+                }
+            }
+            // weighted by w_t, three terms
+            uint32_t hi[4], mid[4], lo[4];
+            const float2 w0 = *reinterpret_cast<const float2 *>(&d.w[ks * 16 + tq * 2]);
+            const float2 w1 = *reinterpret_cast<const float2 *>(&d.w[ks * 16 + 8 + tq * 2]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = unpack2<T>(xa[i]), w = i < 2 ? w0 : w1;
+                split3(v.x * w.x, v.y * w.y, hi[i], mid[i], lo[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                uint32_t bb[4];
+                ldsm_x4_t(bb, Bs + (ks * 16 + lr + 8 * (lm & 1)) * BP + (j + (lm >> 1)) * 8);
+                mma_bf16_16816(S[j], lo, bb[0], bb[1]);
+                mma_bf16_16816(S[j + 1], lo, bb[2], bb[3]);
+                mma_bf16_16816(S[j], mid, bb[0], bb[1]);
+                mma_bf16_16816(S[j + 1], mid, bb[2], bb[3]);
+                mma_bf16_16816(S[j], hi, bb[0], bb[1]);
+                mma_bf16_16816(S[j + 1], hi, bb[2], bb[3]);
+            }
+        }
+        if constexpr (OUT) {
+            // y: the warp's 16 rows turned into 64 rows of 16 (32 bytes; the two
+            // 16-byte halves swap places every fourth row against bank conflicts)
+            T *ys = (y_over_c(N, warps) ? sC(buf) : sYown) + warp * kL * 16;
+#pragma unroll
+            for (int j = 0; j < kL / 8; j += 2) {
+                uint32_t r[4];
+                r[0] = pack2<T>(Y[j][0], Y[j][1]);
+                r[1] = pack2<T>(Y[j][2], Y[j][3]);
+                r[2] = pack2<T>(Y[j + 1][0], Y[j + 1][1]);
+                r[3] = pack2<T>(Y[j + 1][2], Y[j + 1][3]);
+                const int t = (j + (lm >> 1)) * 8 + lr;
+                stsm_x4_t(ys + t * 16 + (((lm & 1) ^ ((t >> 2) & 1)) * 8), r);
+            }
+            __syncwarp();
+            const int64_t t0 = t_begin + (int64_t)c * kL;
+            const int n = (int)(t_end - t0 < kL ? t_end - t0 : kL);
+            const int q = lane & 1;
+            T *y = static_cast<T *>(a.y) + ((b * a.T + t0) * a.H + h) * a.P + p_cta + warp * 16 + q * 8;
+#pragma unroll
+            for (int i = 0; i < kL / 16; ++i) {
+                const int t = i * 16 + (lane >> 1);
+                if (t < n && warp * 16 + q * 8 < rows)
+                    *reinterpret_cast<uint4 *>(y + (int64_t)t * a.H * a.P) =
+                        *reinterpret_cast<const uint4 *>(ys + t * 16 + ((q ^ ((t >> 2) & 1)) * 8));
+            }
+        }
+    }
+
+    if (phase == 2) return;
+    float *dst = phase == 1 ? a.workspace + seg * tiles : a.state_out;
+    if (dst) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int pr = warp * 16 + gr + 8 * r;
+                if (pr < rows)
+                    *reinterpret_cast<float2 *>(dst + tile + (p_cta + pr) * N + j * 8 + tq * 2) =
+                        make_float2(S[j][2 * r], S[j][2 * r + 1]);
+            }
+    }
+    if (phase == 1 && rb == 0 && threadIdx.x == 0)
+        a.workspace[(int64_t)a.segments * tiles + (seg * a.B + b) * a.H + h] = decay;
+}
+
+template <int N, bool OUT>
+cudaError_t launch_phase(const ScanArgs &a, int phase, int64_t ctas, int warps, int64_t row_blocks, cudaStream_t s) {
+    const size_t smem = chunk_smem(N, warps);
+    const cudaError_t e = cudaFuncSetAttribute(scan_chunk_kernel<N, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(scan_chunk_kernel<N, OUT>, (unsigned)ctas, warps * 32, smem, s, a, phase, row_blocks);
+}
+
+template <int N> cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
+    int64_t row_blocks;
+    const int warps = scan_chunk_warps(a.P, &row_blocks);
+    const int64_t ctas = a.B * a.H * row_blocks;
+    if (ctas * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
+    if (a.segments == 1)
+        return a.y ? launch_phase<N, true>(a, 0, ctas, warps, row_blocks, s)
+                   : launch_phase<N, false>(a, 0, ctas, warps, row_blocks, s);
+    const cudaError_t e = launch_phase<N, false>(a, 1, ctas * a.segments, warps, row_blocks, s);
+    if (e != cudaSuccess) return e;
+    return a.y ? launch_phase<N, true>(a, 2, ctas * a.segments, warps, row_blocks, s)
+               : launch_phase<N, false>(a, 2, ctas, warps, row_blocks, s);
+}
+
+}  // namespace
+
+int scan_chunk_warps(int64_t P, int64_t *row_blocks) {
+    const int64_t w = (P + 15) / 16;
+    *row_blocks = (w + 7) / 8;
+    return (int)((w + *row_blocks - 1) / *row_blocks);
+}
+
+cudaError_t launch_scan_chunk(const ScanArgs &a, cudaStream_t s) {
+    switch (a.N) {
+    case 64: return launch_n<64>(a, s);
+    case 128: return launch_n<128>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn

@@ -260,23 +260,36 @@ cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
 
 bool scan_supported_n(int64_t N) { return N == 16 || N == 32 || N == 64 || N == 128 || N == 256; }
 
-ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N) {
-    // enough CTAs for four on each of 152 SMs, segments of 64 steps or more
+bool scan_chunk_sizes(DType dt, int64_t T, int64_t P, int64_t N) {
+    return dt == DType::BF16 && (N == 64 || N == 128) && P % 8 == 0 && T >= 32;
+}
+
+ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool chunked) {
     ScanPlan plan{1, T, 0};
     int64_t row_blocks = 1;
-    switch (N) {
-    case 16: scan_warps<16>(P, &row_blocks); break;
-    case 32: scan_warps<32>(P, &row_blocks); break;
-    case 64: scan_warps<64>(P, &row_blocks); break;
-    case 128: scan_warps<128>(P, &row_blocks); break;
-    case 256: scan_warps<256>(P, &row_blocks); break;
+    // CTAs that fill 152 SMs, and the fewest steps of a segment
+    double target = 608.0;
+    int64_t least = 64, unit = kStage;
+    if (chunked) {
+        // one CTA of eight warps per SM, two of four
+        target = scan_chunk_warps(P, &row_blocks) <= 4 ? 304.0 : 152.0;
+        least = 256;
+        unit = 64;
+    } else {
+        switch (N) {
+        case 16: scan_warps<16>(P, &row_blocks); break;
+        case 32: scan_warps<32>(P, &row_blocks); break;
+        case 64: scan_warps<64>(P, &row_blocks); break;
+        case 128: scan_warps<128>(P, &row_blocks); break;
+        case 256: scan_warps<256>(P, &row_blocks); break;
+        }
     }
     const double ctas = (double)B * (double)H * (double)row_blocks;
-    int64_t want = ctas >= 608.0 ? 1 : (int64_t)(608.0 / ctas);
-    if (want > T / 64) want = T / 64;
+    int64_t want = ctas >= target ? 1 : (int64_t)(target / ctas);
+    if (want > T / least) want = T / least;
     if (want > 64) want = 64;
     if (want > 1) {
-        const int64_t steps = ((T + want - 1) / want + kStage - 1) / kStage * kStage;
+        const int64_t steps = ((T + want - 1) / want + unit - 1) / unit * unit;
         plan.segments = (int)((T + steps - 1) / steps);
         plan.seg_steps = steps;
     }
@@ -293,6 +306,7 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N) {
 }
 
 cudaError_t launch_selective_scan(DType dt, const ScanArgs &a, int, cudaStream_t s) {
+    if (a.chunked) return launch_scan_chunk(a, s);
     switch (dt) {
     case DType::F32: return launch_t<float>(a, s);
     case DType::BF16: return launch_t<__nv_bfloat16>(a, s);
