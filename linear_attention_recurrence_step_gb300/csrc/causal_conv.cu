@@ -16,13 +16,15 @@ namespace gdn {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kConvBatch = 4;   // steps whose loads are issued together
+// Steps whose loads are issued together.
+template <int VEC> struct ConvBatch { static constexpr int value = VEC == 1 ? 8 : 4; };
 
 // blockIdx.x: (sequence, run of steps, block of channel pieces), channels
 // innermost.
 template <typename T, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, int run, int64_t runs,
                                                             int64_t cblocks) {
+    constexpr int BATCH = ConvBatch<VEC>::value;
     pdl_trigger();
     pdl_wait();
     const int64_t blk = blockIdx.x;
@@ -85,16 +87,24 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
     }
     if (!a.y) return;
     T *y = static_cast<T *>(a.y) + (b * a.T) * a.C + c;
-    for (int64_t t = t0; t < t1; t += kConvBatch) {
-        RawPiece<T, VEC> raw[kConvBatch];
+    // the next batch of steps is on its way while one is worked on
+    RawPiece<T, VEC> raw[BATCH];
+    auto fetch = [&](int64_t t) {
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k)
+        for (int k = 0; k < BATCH; ++k)
             if (t + k < t1) raw[k] = load_raw<T, VEC>(x + (t + k) * a.x_st);
+    };
+    fetch(t0);
+    for (int64_t t = t0; t < t1; t += BATCH) {
+        RawPiece<T, VEC> now[BATCH];
 #pragma unroll
-        for (int k = 0; k < kConvBatch; ++k) {
+        for (int k = 0; k < BATCH; ++k) now[k] = raw[k];
+        fetch(t + BATCH);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
             if (t + k < t1) {
                 float in[VEC], out[VEC];
-                widen<T, VEC>(in, raw[k]);
+                widen<T, VEC>(in, now[k]);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     float s = bias[i];

@@ -63,7 +63,8 @@ struct NormArgs {
     int64_t weight_rows;                       // 1, or K
     float scale, eps;
     bool gate_first;
-    bool vec;
+    bool vec;                                  // every row is whole 16-byte pieces
+    bool shift;                                // dense rows of another width from 16-byte aligned bases
 };
 cudaError_t launch_gated_norm(DType dt, const NormArgs &a, int sm_count, cudaStream_t s);
 

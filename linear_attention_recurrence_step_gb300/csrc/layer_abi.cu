@@ -246,9 +246,11 @@ gdn_status gdn_gated_norm(const void *x, const void *weight, const void *gate, c
     a.scale = residual_scale;
     a.eps = eps;
     a.gate_first = gate_first != 0;
-    a.vec = D * eb % 16 == 0 && (M == 1 || x_stride_m * eb % 16 == 0) &&
-            (!gate || M == 1 || gate_stride_m * eb % 16 == 0) && aligned(x, 16) && aligned(weight, 16) &&
-            aligned(gate, 16) && aligned(residual, 16) && aligned(y, 16) && aligned(residual_out, 16);
+    const bool bases = aligned(x, 16) && aligned(weight, 16) && aligned(gate, 16) && aligned(residual, 16) &&
+                       aligned(y, 16) && aligned(residual_out, 16);
+    a.vec = bases && D * eb % 16 == 0 && (M == 1 || x_stride_m * eb % 16 == 0) &&
+            (!gate || M == 1 || gate_stride_m * eb % 16 == 0);
+    a.shift = bases && !a.vec && x_dense && (!gate || g_dense);
     e = gdn::launch_gated_norm(static_cast<gdn::DType>(dtype), a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaErrorInvalidConfiguration) return fail(GDN_ERR_INVALID_ARGUMENT, "%s: grid too large", fn);
     if (e != cudaSuccess) return cuda_fail(fn, "launch", e);

@@ -1,4 +1,4 @@
-// scan_chunk.cu -- the selective scan over long calls in chunks of L = 64
+// scan_chunk.cu -- the selective scan over long calls in chunks of L = 32
 // steps on the tensor cores (warp-level mma.sync, bf16 operands, f32
 // accumulate).  bf16 inputs, f32 state, N = 64 or 128.
 //
@@ -7,8 +7,8 @@
 //     y_t = exp(c_t) S C_t + sum_{s<=t} W[t][s] x_s + D x_t,
 //           W[t][s] = (C_t . B_s) exp(c_t - c_s) dl_s
 //     S  <- exp(c_L) S + sum_s x_s (exp(c_L - c_s) dl_s) B_s^T
-// so a chunk is four products: C B^T (64 x 64 x N), S C^T (P x 64 x N), x^T W^T
-// (P x 64 x 64, the half below the diagonal) and x^T B (P x N x 64).
+// so a chunk is four products: C B^T (L x L x N), S C^T (P x L x N), x^T W^T
+// (P x L x L, the half below the diagonal) and x^T B (P x N x L).
 //
 // A CTA owns up to 128 rows p of one head and walks the chunks of its segment
 // in order.  A warp owns 16 rows: their state stays in its registers as the
@@ -18,7 +18,8 @@
 //
 // Precision: x, B and C enter as they are (bf16).  The weighted x, which goes
 // into the state, enters as three bf16 terms (24 significant bits: f32's own),
-// and the state is only ever scaled and added to in f32.  The state and W as
+// and the state is only ever scaled and added to in f32 (two terms where the
+// state goes into y alone, in a second pass).  The state and W as
 // operands of y enter as two terms (16 bits): their products carry a relative
 // error of at most 2^-18, a thousandth of what rounding y to bf16 costs.  c_t
 // is summed in f64 and kept as two f32 terms, so that exp(c_t - c_s) loses
@@ -38,7 +39,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kL = 64;               // steps of a chunk
+constexpr int kL = 32;               // steps of a chunk
 constexpr int kWPitch = kL + 8;      // elements between rows of W in shared memory
 
 struct ChunkDecay {
@@ -88,8 +89,9 @@ __device__ __forceinline__ float ex2f(float x) {
 }
 
 // OUT: y is wanted (else only the state: the first pass, and calls without y).
-template <int N, bool OUT>
-__global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
+// TERMS: bf16 terms of the weighted x (two where the state goes into y alone).
+template <int N, bool OUT, int TERMS>
+__global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
     using T = __nv_bfloat16;
     constexpr int NT = N / 8;              // 8-column tiles of the state
     constexpr int BP = bc_pitch(N);
@@ -134,15 +136,19 @@ __global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const
     const T *const Cp = static_cast<const T *>(a.Cm) + b * a.c_sb + g * N;
     const float A2 = a.A[h] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
 
-    // rows past the end, and columns past the head, are zeros
+    // rows past the end, and columns past the head, are zeros; an x row has two
+    // 16-byte pieces per warp, so the CTA copies 16 rows at a time
     auto fetch = [&](int c) {
         const int64_t t0 = t_begin + (int64_t)c * kL;
         const int buf = c & 1, n = (int)(t_end - t0 < kL ? t_end - t0 : kL);
-        const int xq = warps * 2;  // 16-byte pieces of an x row
-        for (int i = threadIdx.x; i < kL * xq; i += blockDim.x) {
-            const int t = i / xq, q = i - t * xq;
-            const bool on = t < n && q * 8 < rows;
-            cp_async16_or_zero(sx(buf) + t * XP + q * 8, on ? x + (t0 + t) * a.x_st + q * 8 : x, on);
+        {
+            const int t = threadIdx.x / (warps * 2), q = threadIdx.x % (warps * 2) * 8;
+            const T *src = x + (t0 + t) * a.x_st + q;
+#pragma unroll
+            for (int i = 0; i < kL / 16; ++i) {
+                const bool on = q < rows && t + 16 * i < n;
+                cp_async16_or_zero(sx(buf) + (t + 16 * i) * XP + q, on ? src + 16 * i * a.x_st : x, on);
+            }
         }
         for (int i = threadIdx.x; i < kL * (N / 8); i += blockDim.x) {
             const int t = i / (N / 8), q = i % (N / 8);
@@ -152,41 +158,29 @@ __global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const
         }
         cp_async_commit();
     };
-    // the decays of a chunk, by one warp (two steps per lane)
+    // the decays of a chunk, by one warp, a step per lane
     auto decays = [&](int c) {
-        const int64_t t0 = t_begin + (int64_t)c * kL;
+        const int64_t t = t_begin + (int64_t)c * kL + lane;
         ChunkDecay &d = sdec[c & 1];
-        float dl[2];
-        double la[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t t = t0 + 2 * lane + i;
-            dl[i] = 0.f;
-            if (t < t_end) {
-                const float v = ld_f32(dtp + t * a.dt_st) + bias;
-                dl[i] = a.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
-            }
-            // a decay below 2^-256 is zero in f32
-            const float l2 = dl[i] * A2;
-            la[i] = l2 < -256.f ? -256.0 : (double)l2;
+        float dl = 0.f;
+        if (t < t_end) {
+            const float v = ld_f32(dtp + t * a.dt_st) + bias;
+            dl = a.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
         }
-        double sum = la[0] + la[1];
+        // a decay below 2^-256 is zero in f32
+        const float l2 = dl * A2;
+        double ct = l2 < -256.f ? -256.0 : (double)l2;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
+            const double v = __shfl_up_sync(0xffffffffu, ct, o);
+            if (lane >= o) ct += v;
         }
-        const double last = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const double ct = i ? sum : sum - la[1];
-            const int t = 2 * lane + i;
-            const float hi = (float)ct;
-            d.c[t] = make_float2(hi, (float)(ct - (double)hi));
-            d.dl[t] = dl[i];
-            d.w[t] = ex2f((float)(last - ct)) * dl[i];
-            d.ec[t] = ex2f(hi);
-        }
+        const double last = __shfl_sync(0xffffffffu, ct, 31);
+        const float hi = (float)ct;
+        d.c[lane] = make_float2(hi, (float)(ct - (double)hi));
+        d.dl[lane] = dl;
+        d.w[lane] = ex2f((float)(last - ct)) * dl;
+        d.ec[lane] = ex2f(hi);
         if (lane == 0) d.total = ex2f((float)last);
     };
 
@@ -251,51 +245,35 @@ __global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const
         const T *xs = sx(buf), *Bs = sB(buf), *Cs = sC(buf);
         float Y[kL / 8][4];
         if constexpr (OUT) {
-            // W, 16 rows t and every other 8-column block of s at a time
-            for (int job = warp; job < 8; job += warps) {
-                const int ti = 3 - job / 2;
-                float G[4][4];
+            // W by tiles of 16 rows t and 8 columns s, those below the diagonal
+            for (int job = warp; job < 6; job += warps) {
+                const int ti = job < 4 ? 1 : 0, sb = job < 4 ? job : job - 4;
+                float G[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) G[i][e] = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < N / 16; ++kk) {
-                    uint32_t ca[4];
+                for (int kk = 0; kk < N / 16; kk += 2) {
+                    uint32_t ca[4], bb[4];
+                    ldsm_x4(bb, Bs + (sb * 8 + lr) * BP + kk * 16 + 8 * lm);
                     ldsm_x4(ca, Cs + (ti * 16 + lr + 8 * (lm & 1)) * BP + kk * 16 + 8 * (lm >> 1));
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        // blocks 2i + job%2 and 2i + 2 + job%2 of s
-                        if (i <= ti) {
-                            uint32_t bb[4];
-                            const int sblk = 2 * (i + (lm >> 1)) + (job & 1);
-                            ldsm_x4(bb, Bs + (min(sblk, 7) * 8 + lr) * BP + kk * 16 + 8 * (lm & 1));
-                            mma_bf16_16816(G[i], ca, bb[0], bb[1]);
-                            mma_bf16_16816(G[i + 1], ca, bb[2], bb[3]);
-                        }
-                    }
+                    mma_bf16_16816(G, ca, bb[0], bb[1]);
+                    ldsm_x4(ca, Cs + (ti * 16 + lr + 8 * (lm & 1)) * BP + kk * 16 + 16 + 8 * (lm >> 1));
+                    mma_bf16_16816(G, ca, bb[2], bb[3]);
                 }
-                const int t0 = ti * 16 + gr;
-                const float2 ca0 = d.c[t0], ca1 = d.c[t0 + 8];
+                const int t0 = ti * 16 + gr, s0 = sb * 8 + tq * 2;
+                const float2 cs0 = d.c[s0], cs1 = d.c[s0 + 1];
+                const float dl0 = d.dl[s0], dl1 = d.dl[s0 + 1];
+                auto wt = [&](float gv, const float2 &ct, const float2 &cs, float dl, int t, int st) {
+                    if (st > t) return 0.f;
+                    const float w = gv * ex2f((ct.x - cs.x) + (ct.y - cs.y)) * dl;
+                    return st == t ? w + Dh : w;
+                };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i > ti) continue;
-                    const int s0 = (2 * i + (job & 1)) * 8 + tq * 2;
-                    const float2 cs0 = d.c[s0], cs1 = d.c[s0 + 1];
-                    const float dl0 = d.dl[s0], dl1 = d.dl[s0 + 1];
-                    auto wt = [&](float gv, const float2 &ct, const float2 &cs, float dl, int t, int s) {
-                        if (s > t) return 0.f;
-                        const float w = gv * ex2f((ct.x - cs.x) + (ct.y - cs.y)) * dl;
-                        return s == t ? w + Dh : w;
-                    };
+                for (int r = 0; r < 2; ++r) {
+                    const int t = t0 + 8 * r;
+                    const float2 ct = d.c[t];
                     uint32_t hi, lo;
-                    split_bf16x2(wt(G[i][0], ca0, cs0, dl0, t0, s0), wt(G[i][1], ca0, cs1, dl1, t0, s0 + 1), hi, lo);
-                    *reinterpret_cast<uint32_t *>(sW + t0 * kWPitch + s0) = hi;
-                    *reinterpret_cast<uint32_t *>(sWlo + t0 * kWPitch + s0) = lo;
-                    split_bf16x2(wt(G[i][2], ca1, cs0, dl0, t0 + 8, s0), wt(G[i][3], ca1, cs1, dl1, t0 + 8, s0 + 1), hi,
-                                 lo);
-                    *reinterpret_cast<uint32_t *>(sW + (t0 + 8) * kWPitch + s0) = hi;
-                    *reinterpret_cast<uint32_t *>(sWlo + (t0 + 8) * kWPitch + s0) = lo;
+                    split_bf16x2(wt(G[2 * r], ct, cs0, dl0, t, s0), wt(G[2 * r + 1], ct, cs1, dl1, t, s0 + 1), hi, lo);
+                    *reinterpret_cast<uint32_t *>(sW + t * kWPitch + s0) = hi;
+                    *reinterpret_cast<uint32_t *>(sWlo + t * kWPitch + s0) = lo;
                 }
             }
             // S C^T: the state's accumulators are the left operand
@@ -355,21 +333,24 @@ __global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const
                     mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
                 }
             }
-            // weighted by w_t, three terms
+            // weighted by w_t
             uint32_t hi[4], mid[4], lo[4];
             const float2 w0 = *reinterpret_cast<const float2 *>(&d.w[ks * 16 + tq * 2]);
             const float2 w1 = *reinterpret_cast<const float2 *>(&d.w[ks * 16 + 8 + tq * 2]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 v = unpack2<T>(xa[i]), w = i < 2 ? w0 : w1;
-                split3(v.x * w.x, v.y * w.y, hi[i], mid[i], lo[i]);
+                if (TERMS == 3) split3(v.x * w.x, v.y * w.y, hi[i], mid[i], lo[i]);
+                else split_bf16x2(v.x * w.x, v.y * w.y, hi[i], mid[i]);
             }
 #pragma unroll
             for (int j = 0; j < NT; j += 2) {
                 uint32_t bb[4];
                 ldsm_x4_t(bb, Bs + (ks * 16 + lr + 8 * (lm & 1)) * BP + (j + (lm >> 1)) * 8);
-                mma_bf16_16816(S[j], lo, bb[0], bb[1]);
-                mma_bf16_16816(S[j + 1], lo, bb[2], bb[3]);
+                if (TERMS == 3) {
+                    mma_bf16_16816(S[j], lo, bb[0], bb[1]);
+                    mma_bf16_16816(S[j + 1], lo, bb[2], bb[3]);
+                }
                 mma_bf16_16816(S[j], mid, bb[0], bb[1]);
                 mma_bf16_16816(S[j + 1], mid, bb[2], bb[3]);
                 mma_bf16_16816(S[j], hi, bb[0], bb[1]);
@@ -422,13 +403,13 @@ __global__ void __launch_bounds__(256) scan_chunk_kernel(const ScanArgs a, const
         a.workspace[(int64_t)a.segments * tiles + (seg * a.B + b) * a.H + h] = decay;
 }
 
-template <int N, bool OUT>
+template <int N, bool OUT, int TERMS>
 cudaError_t launch_phase(const ScanArgs &a, int phase, int64_t ctas, int warps, int64_t row_blocks, cudaStream_t s) {
     const size_t smem = chunk_smem(N, warps);
-    const cudaError_t e = cudaFuncSetAttribute(scan_chunk_kernel<N, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(scan_chunk_kernel<N, OUT, TERMS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(scan_chunk_kernel<N, OUT>, (unsigned)ctas, warps * 32, smem, s, a, phase, row_blocks);
+    return launch_dependent(scan_chunk_kernel<N, OUT, TERMS>, (unsigned)ctas, warps * 32, smem, s, a, phase, row_blocks);
 }
 
 template <int N> cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
@@ -437,12 +418,12 @@ template <int N> cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
     const int64_t ctas = a.B * a.H * row_blocks;
     if (ctas * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (a.segments == 1)
-        return a.y ? launch_phase<N, true>(a, 0, ctas, warps, row_blocks, s)
-                   : launch_phase<N, false>(a, 0, ctas, warps, row_blocks, s);
-    const cudaError_t e = launch_phase<N, false>(a, 1, ctas * a.segments, warps, row_blocks, s);
+        return a.y ? launch_phase<N, true, 3>(a, 0, ctas, warps, row_blocks, s)
+                   : launch_phase<N, false, 3>(a, 0, ctas, warps, row_blocks, s);
+    const cudaError_t e = launch_phase<N, false, 3>(a, 1, ctas * a.segments, warps, row_blocks, s);
     if (e != cudaSuccess) return e;
-    return a.y ? launch_phase<N, true>(a, 2, ctas * a.segments, warps, row_blocks, s)
-               : launch_phase<N, false>(a, 2, ctas, warps, row_blocks, s);
+    return a.y ? launch_phase<N, true, 2>(a, 2, ctas * a.segments, warps, row_blocks, s)
+               : launch_phase<N, false, 3>(a, 2, ctas, warps, row_blocks, s);
 }
 
 }  // namespace

@@ -271,8 +271,8 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
     double target = 608.0;
     int64_t least = 64, unit = kStage;
     if (chunked) {
-        // one CTA of eight warps per SM, two of four
-        target = scan_chunk_warps(P, &row_blocks) <= 4 ? 304.0 : 152.0;
+        // sixteen warps per SM
+        target = 152.0 * (16 / scan_chunk_warps(P, &row_blocks));
         least = 256;
         unit = 64;
     } else {
