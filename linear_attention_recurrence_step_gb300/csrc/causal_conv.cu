@@ -22,7 +22,7 @@ template <int VEC> struct ConvBatch { static constexpr int value = VEC == 1 ? 8 
 // blockIdx.x: (sequence, run of steps, block of channel pieces), channels
 // innermost.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, int run, int64_t runs,
+__global__ void __launch_bounds__(kConvThreads, W <= 4 ? 4 : 2) conv_kernel(const ConvArgs a, int run, int64_t runs,
                                                             int64_t cblocks) {
     constexpr int BATCH = ConvBatch<VEC>::value;
     pdl_trigger();
@@ -42,32 +42,38 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
     const int64_t t0 = r * run;
     const int64_t t1 = t0 + run < len ? t0 + run : len;
 
-    float w[W][VEC], bias[VEC];
+    constexpr int NP = kPairs<VEC>;
+    float2 w[W][NP], bias[NP];
     {
         const T *wp = static_cast<const T *>(a.weight) + c * W;
+        float taps[W * VEC];  // VEC * W consecutive taps, VEC at a time
 #pragma unroll
-        for (int p = 0; p < W; ++p) {  // VEC * W consecutive taps, VEC at a time
+        for (int p = 0; p < W; ++p) {
             float piece[VEC];
             load_piece<T, VEC>(piece, wp + p * VEC);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) w[(p * VEC + i) % W][(p * VEC + i) / W] = piece[i];
+            for (int i = 0; i < VEC; ++i) taps[p * VEC + i] = piece[i];
         }
-        if (a.bias) load_piece<T, VEC>(bias, static_cast<const T *>(a.bias) + c);
-        else
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) bias[i] = 0.f;
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                w[j][i] = make_float2(taps[2 * i * W + j], 2 * i + 1 < VEC ? taps[(2 * i + 1) % VEC * W + j] : 0.f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) bias[i] = make_float2(0.f, 0.f);
+        if (a.bias) widen2<T, VEC>(bias, load_raw<T, VEC>(static_cast<const T *>(a.bias) + c));
     }
 
     // win[j]: the input W-1-j steps before the current one
-    float win[W - 1][VEC];
+    float2 win[W - 1][NP];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int64_t t = t0 - (W - 1) + j;
-        if (t >= 0) load_piece<T, VEC>(win[j], x + t * a.x_st);
-        else if (sin) load_piece<T, VEC>(win[j], sin + (W - 1 + t) * a.C);
+        if (t >= 0) widen2<T, VEC>(win[j], load_raw<T, VEC>(x + t * a.x_st));
+        else if (sin) widen2<T, VEC>(win[j], load_raw<T, VEC>(sin + (W - 1 + t) * a.C));
         else
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) win[j][i] = 0.f;
+            for (int i = 0; i < NP; ++i) win[j][i] = make_float2(0.f, 0.f);
     }
     // the first run's thread also writes the new state, a copy of inputs: it
     // alone reads state_in at its channels and has done so before it writes,
@@ -103,19 +109,19 @@ __global__ void __launch_bounds__(kConvThreads) conv_kernel(const ConvArgs a, in
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             if (t + k < t1) {
-                float in[VEC], out[VEC];
-                widen<T, VEC>(in, now[k]);
+                float2 in[NP], out[NP];
+                widen2<T, VEC>(in, now[k]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float s = bias[i];
+                for (int i = 0; i < NP; ++i) {
+                    float2 s = bias[i];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][i], win[j][i], s);
-                    s = fmaf(w[W - 1][i], in[i], s);
-                    out[i] = a.silu ? silu(s) : s;
+                    for (int j = 0; j < W - 1; ++j) s = ffma2(w[j][i], win[j][i], s);
+                    s = ffma2(w[W - 1][i], in[i], s);
+                    out[i] = a.silu ? silu2(s) : s;
                 }
-                store_piece<T, VEC>(y + (t + k) * a.C, out);
+                store_piece2<T, VEC>(y + (t + k) * a.C, out);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
+                for (int i = 0; i < NP; ++i) {
 #pragma unroll
                     for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
                     win[W - 2][i] = in[i];

@@ -53,6 +53,10 @@ bool scan_supported_n(int64_t N);
 int scan_chunk_warps(int64_t P, int64_t *row_blocks);
 bool scan_chunk_sizes(DType dt, int64_t T, int64_t P, int64_t N);
 cudaError_t launch_scan_chunk(const ScanArgs &a, cudaStream_t s);
+// What a kernel of a call does: all of it; or, of a call in segments, the
+// segments' end states (then launch_scan_join), or its output.
+enum ScanPhase { kScanWhole = 0, kScanFold = 1, kScanOutput = 2 };
+cudaError_t launch_scan_join(const ScanArgs &a, cudaStream_t s);
 cudaError_t launch_selective_scan(DType dt, const ScanArgs &a, int sm_count, cudaStream_t s);
 
 struct NormArgs {
@@ -66,7 +70,10 @@ struct NormArgs {
     bool vec;                                  // every row is whole 16-byte pieces
     bool shift;                                // dense rows of another width from 16-byte aligned bases
 };
-cudaError_t launch_gated_norm(DType dt, const NormArgs &a, int sm_count, cudaStream_t s);
+// One translation unit per element type.
+cudaError_t launch_norm_f32(const NormArgs &a, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_bf16(const NormArgs &a, int sm_count, cudaStream_t s);
+cudaError_t launch_norm_f16(const NormArgs &a, int sm_count, cudaStream_t s);
 
 struct SampleArgs {
     const void *logits;

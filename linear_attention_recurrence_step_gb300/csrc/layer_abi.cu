@@ -251,7 +251,10 @@ gdn_status gdn_gated_norm(const void *x, const void *weight, const void *gate, c
     a.vec = bases && D * eb % 16 == 0 && (M == 1 || x_stride_m * eb % 16 == 0) &&
             (!gate || M == 1 || gate_stride_m * eb % 16 == 0);
     a.shift = bases && !a.vec && x_dense && (!gate || g_dense);
-    e = gdn::launch_gated_norm(static_cast<gdn::DType>(dtype), a, sms, reinterpret_cast<cudaStream_t>(stream));
+    const auto launch = dtype == GDN_DTYPE_F32    ? gdn::launch_norm_f32
+                        : dtype == GDN_DTYPE_BF16 ? gdn::launch_norm_bf16
+                                                  : gdn::launch_norm_f16;
+    e = launch(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaErrorInvalidConfiguration) return fail(GDN_ERR_INVALID_ARGUMENT, "%s: grid too large", fn);
     if (e != cudaSuccess) return cuda_fail(fn, "launch", e);
     return ok();

@@ -91,8 +91,42 @@ __device__ __forceinline__ void store_piece(T *p, const float (&v)[VEC]) {
     }
 }
 
-// x * sigmoid(x).  __expf and __fdividef are within a few units in the last
-// place here; exp overflowing to infinity gives the limit, -0.
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// x * sigmoid(x), within a few units in the last place (the exponential's
+// argument costs |x| of them).  exp overflowing to infinity gives the limit,
+// -0.  The two-lane form takes one packed instruction for both where there is
+// one.
+__device__ __forceinline__ float silu(float x) { return x * rcpf(1.f + ex2f(-1.44269504088896341f * x)); }
+__device__ __forceinline__ float2 silu2(float2 x) {
+    const float2 t = fmul2(x, make_float2(-1.44269504088896341f, -1.44269504088896341f));
+    const float2 d = __fadd2_rn(make_float2(ex2f(t.x), ex2f(t.y)), make_float2(1.f, 1.f));
+    return fmul2(x, make_float2(rcpf(d.x), rcpf(d.y)));
+}
+
+// A piece as pairs (a single element: the first of a pair, beside a zero).
+template <int VEC> constexpr int kPairs = (VEC + 1) / 2;
+template <typename T, int VEC>
+__device__ __forceinline__ void widen2(float2 (&v)[kPairs<VEC>], const RawPiece<T, VEC> &r) {
+    float f[VEC];
+    widen<T, VEC>(f, r);
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i) v[i] = make_float2(f[2 * i], 2 * i + 1 < VEC ? f[(2 * i + 1) % VEC] : 0.f);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_piece2(T *p, const float2 (&v)[kPairs<VEC>]) {
+    float f[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = i % 2 ? v[i / 2].y : v[i / 2].x;
+    store_piece<T, VEC>(p, f);
+}
 
 }  // namespace gdn

@@ -26,8 +26,8 @@
 // nothing to a chunk's large |c|.
 //
 // A call with few heads is split along the steps as in selective_scan.cu: a
-// first pass forms the segments' end states (the last product alone), the
-// second starts every segment from the fold of those before it.
+// first pass forms the segments' end states (the last product alone), and the
+// output pass starts every segment from the state after the one before it.
 //
 // What bounds it: the tensor pipe, then the barrier after W.  About 390
 // mma.sync per warp and chunk at P = N = 128.
@@ -82,16 +82,10 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_
     const float2 h = unpack2<__nv_bfloat16>(hi);
     split_bf16x2(x0 - h.x, x1 - h.y, mid, lo);
 }
-__device__ __forceinline__ float ex2f(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // OUT: y is wanted (else only the state: the first pass, and calls without y).
-// TERMS: bf16 terms of the weighted x (two where the state goes into y alone).
-template <int N, bool OUT, int TERMS>
-__global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
+template <int N, bool OUT, int PHASE>
+__global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, const int64_t row_blocks) {
+    constexpr int TERMS = PHASE == kScanOutput ? 2 : 3;
     using T = __nv_bfloat16;
     constexpr int NT = N / 8;              // 8-column tiles of the state
     constexpr int BP = bc_pitch(N);
@@ -184,48 +178,29 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         if (lane == 0) d.total = ex2f((float)last);
     };
 
-    // the state of the warp's rows: accumulator tiles of 16 x 8
+    // the state of the warp's rows, accumulator tiles of 16 x 8: the call's
+    // state, zeros, or the state after the segment before this one
     float S[NT][4];
     {
-        const float *ws = a.workspace;
-        const float *dec = ws + (int64_t)a.segments * tiles + b * a.H + h;
+        const float *from = seg == 0 ? a.state_in : PHASE == kScanOutput ? a.workspace + (seg - 1) * tiles : nullptr;
+        // the first segment writes the call's state: it alone reads state_in,
+        // which may be the same buffer
+        const bool hand_on = PHASE == kScanOutput && seg == 0 && a.state_out;
+        const float *last = a.workspace + (a.segments - 1) * tiles;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const int pr = warp * 16 + gr + 8 * r;
+                const int64_t off = tile + (p_cta + pr) * N + j * 8 + tq * 2;
                 float2 v = make_float2(0.f, 0.f);
-                if (pr < rows) {
-                    const int64_t off = tile + (p_cta + pr) * N + j * 8 + tq * 2;
-                    if (seg == 0) {
-                        if (a.state_in) v = *reinterpret_cast<const float2 *>(a.state_in + off);
-                    } else if (phase == 2) {
-                        v = *reinterpret_cast<const float2 *>(ws + off);
-                        for (int64_t i = 1; i < seg; ++i) {
-                            const float d = dec[i * a.B * a.H];
-                            const float2 e = *reinterpret_cast<const float2 *>(ws + i * tiles + off);
-                            v.x = fmaf(d, v.x, e.x);
-                            v.y = fmaf(d, v.y, e.y);
-                        }
-                    }
-                    // the first segment writes the call's state: it alone reads
-                    // state_in, which may be the same buffer
-                    if (phase == 2 && seg == 0 && a.state_out) {
-                        float2 s = *reinterpret_cast<const float2 *>(ws + off);
-                        for (int64_t i = 1; i < a.segments; ++i) {
-                            const float d = dec[i * a.B * a.H];
-                            const float2 e = *reinterpret_cast<const float2 *>(ws + i * tiles + off);
-                            s.x = fmaf(d, s.x, e.x);
-                            s.y = fmaf(d, s.y, e.y);
-                        }
-                        *reinterpret_cast<float2 *>(a.state_out + off) = s;
-                    }
-                }
+                if (from && pr < rows) v = *reinterpret_cast<const float2 *>(from + off);
                 S[j][2 * r] = v.x;
                 S[j][2 * r + 1] = v.y;
+                if (hand_on && pr < rows)
+                    *reinterpret_cast<float2 *>(a.state_out + off) = *reinterpret_cast<const float2 *>(last + off);
             }
     }
-    if (phase == 2 && !OUT) return;
 
     float decay = 1.f;
     const int lr = lane & 7, lm = lane >> 3;            // ldmatrix: row and matrix of this lane's address
@@ -386,8 +361,8 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         }
     }
 
-    if (phase == 2) return;
-    float *dst = phase == 1 ? a.workspace + seg * tiles : a.state_out;
+    if (PHASE == kScanOutput) return;
+    float *dst = PHASE == kScanFold ? a.workspace + seg * tiles : a.state_out;
     if (dst) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -399,17 +374,17 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
                         make_float2(S[j][2 * r], S[j][2 * r + 1]);
             }
     }
-    if (phase == 1 && rb == 0 && threadIdx.x == 0)
+    if (PHASE == kScanFold && rb == 0 && threadIdx.x == 0)
         a.workspace[(int64_t)a.segments * tiles + (seg * a.B + b) * a.H + h] = decay;
 }
 
-template <int N, bool OUT, int TERMS>
-cudaError_t launch_phase(const ScanArgs &a, int phase, int64_t ctas, int warps, int64_t row_blocks, cudaStream_t s) {
+template <int N, bool OUT, int PHASE>
+cudaError_t launch_phase(const ScanArgs &a, int64_t ctas, int warps, int64_t row_blocks, cudaStream_t s) {
     const size_t smem = chunk_smem(N, warps);
-    const cudaError_t e = cudaFuncSetAttribute(scan_chunk_kernel<N, OUT, TERMS>,
+    const cudaError_t e = cudaFuncSetAttribute(scan_chunk_kernel<N, OUT, PHASE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(scan_chunk_kernel<N, OUT, TERMS>, (unsigned)ctas, warps * 32, smem, s, a, phase, row_blocks);
+    return launch_dependent(scan_chunk_kernel<N, OUT, PHASE>, (unsigned)ctas, warps * 32, smem, s, a, row_blocks);
 }
 
 template <int N> cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
@@ -418,12 +393,12 @@ template <int N> cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
     const int64_t ctas = a.B * a.H * row_blocks;
     if (ctas * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (a.segments == 1)
-        return a.y ? launch_phase<N, true, 3>(a, 0, ctas, warps, row_blocks, s)
-                   : launch_phase<N, false, 3>(a, 0, ctas, warps, row_blocks, s);
-    const cudaError_t e = launch_phase<N, false, 3>(a, 1, ctas * a.segments, warps, row_blocks, s);
-    if (e != cudaSuccess) return e;
-    return a.y ? launch_phase<N, true, 2>(a, 2, ctas * a.segments, warps, row_blocks, s)
-               : launch_phase<N, false, 3>(a, 2, ctas, warps, row_blocks, s);
+        return a.y ? launch_phase<N, true, kScanWhole>(a, ctas, warps, row_blocks, s)
+                   : launch_phase<N, false, kScanWhole>(a, ctas, warps, row_blocks, s);
+    cudaError_t e = launch_phase<N, false, kScanFold>(a, ctas * a.segments, warps, row_blocks, s);
+    if (e == cudaSuccess) e = launch_scan_join(a, s);
+    if (e != cudaSuccess || !a.y) return e;
+    return launch_phase<N, true, kScanOutput>(a, ctas * a.segments, warps, row_blocks, s);
 }
 
 }  // namespace

@@ -11,7 +11,8 @@
 // call of few steps is bound by the state's bytes.  A long call with few
 // heads is split along the steps: a first kernel folds every segment (the
 // first from state_in, the others from zero) into its end state and its total
-// decay, a second one starts each segment from the fold of those before it.
+// decay, a second one joins these into the state after every segment, and a
+// third one runs the segments from those.
 #include "layer.h"
 #include "pieces.cuh"
 
@@ -30,12 +31,10 @@ template <int N> struct ScanShape {
     static constexpr int kWarpRows = RW * RPL;
 };
 
-enum ScanPhase { kScanWhole = 0, kScanFold = 1, kScanOutput = 2 };
-
 // workspace: end states [segments][B][H][P][N], then decays [segments][B][H]
-template <typename T, int N>
+template <typename T, int N, int phase>
 __global__ void __launch_bounds__(kScanWarps * 32)
-scan_step_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
+scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
     using S = ScanShape<N>;
     constexpr int LR = S::LR, VPL = S::VPL, RPL = S::RPL, RW = S::RW, WR = S::kWarpRows;
     constexpr int NV4 = VPL / 4;  // float4 groups per lane and row: entries j*4*LR + lane*4
@@ -71,6 +70,9 @@ scan_step_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
     int64_t t_end = t_begin + a.seg_steps;
     if (t_end > len) t_end = len;
 
+    // where the segment starts: the call's state, zeros, or the state after the
+    // segment before it
+    const float *from = seg == 0 ? a.state_in : phase == kScanOutput ? a.workspace + (seg - 1) * tiles : nullptr;
     float4 s[RPL][NV4];
 #pragma unroll
     for (int r = 0; r < RPL; ++r) {
@@ -78,43 +80,24 @@ scan_step_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
 #pragma unroll
         for (int j = 0; j < NV4; ++j) {
             s[r][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int64_t off = tile + p * N + j * 4 * LR + sub * 4;
-            if (p < a.P) {
-                if (seg == 0) {
-                    if (a.state_in) s[r][j] = *reinterpret_cast<const float4 *>(a.state_in + off);
-                } else if (phase == kScanOutput) {
-                    // the state that this segment starts from
-                    const float *dec = a.workspace + (int64_t)a.segments * tiles + b * a.H + h;
-                    float4 v = *reinterpret_cast<const float4 *>(a.workspace + off);
-                    for (int64_t i = 1; i < seg; ++i) {
-                        const float d = dec[i * a.B * a.H];
-                        const float4 e = *reinterpret_cast<const float4 *>(a.workspace + i * tiles + off);
-                        v.x = fmaf(d, v.x, e.x);
-                        v.y = fmaf(d, v.y, e.y);
-                        v.z = fmaf(d, v.z, e.z);
-                        v.w = fmaf(d, v.w, e.w);
-                    }
-                    s[r][j] = v;
-                }
-                // the first segment writes the call's state: it alone reads
-                // state_in, which may be the same buffer
-                if (phase == kScanOutput && seg == 0 && a.state_out) {
-                    const float *dec = a.workspace + (int64_t)a.segments * tiles + b * a.H + h;
-                    float4 v = *reinterpret_cast<const float4 *>(a.workspace + off);
-                    for (int64_t i = 1; i < a.segments; ++i) {
-                        const float d = dec[i * a.B * a.H];
-                        const float4 e = *reinterpret_cast<const float4 *>(a.workspace + i * tiles + off);
-                        v.x = fmaf(d, v.x, e.x);
-                        v.y = fmaf(d, v.y, e.y);
-                        v.z = fmaf(d, v.z, e.z);
-                        v.w = fmaf(d, v.w, e.w);
-                    }
-                    *reinterpret_cast<float4 *>(a.state_out + off) = v;
-                }
-            }
+            if (from && p < a.P)
+                s[r][j] = *reinterpret_cast<const float4 *>(from + tile + p * N + j * 4 * LR + sub * 4);
         }
     }
-    if (phase == kScanOutput && !a.y) return;
+    if (phase == kScanOutput && seg == 0 && a.state_out) {
+        // the first segment writes the call's state: it alone reads state_in,
+        // which may be the same buffer
+        const float *last = a.workspace + (a.segments - 1) * tiles + tile;
+#pragma unroll
+        for (int r = 0; r < RPL; ++r) {
+            const int64_t p = p0 + r * RW;
+#pragma unroll
+            for (int j = 0; j < NV4; ++j)
+                if (p < a.P)
+                    *reinterpret_cast<float4 *>(a.state_out + tile + p * N + j * 4 * LR + sub * 4) =
+                        *reinterpret_cast<const float4 *>(last + p * N + j * 4 * LR + sub * 4);
+        }
+    }
 
     const float Ah = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
     const T *x = static_cast<const T *>(a.x) + b * a.x_sb + h * a.P;
@@ -221,6 +204,31 @@ scan_step_kernel(const ScanArgs a, const int phase, const int64_t row_blocks) {
         a.workspace[(int64_t)a.segments * tiles + (seg * a.B + b) * a.H + h] = decay;
 }
 
+// The segments' end states and decays, joined in place: slot i becomes the
+// state after segment i.  The last one goes to `state_out` too when that is
+// given (calls without y).
+__global__ void __launch_bounds__(256) scan_join_kernel(float *ws, float *state_out, int segments, int64_t tiles,
+                                                        int64_t heads, int64_t per_head) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= tiles) return;
+    const float *dec = ws + (int64_t)segments * tiles + i / per_head;
+    float4 v = *reinterpret_cast<const float4 *>(ws + i);
+#pragma unroll 4
+    for (int k = 1; k < segments; ++k) {
+        const float d = dec[k * heads];
+        float4 *slot = reinterpret_cast<float4 *>(ws + k * tiles + i);
+        const float4 e = *slot;
+        v.x = fmaf(d, v.x, e.x);
+        v.y = fmaf(d, v.y, e.y);
+        v.z = fmaf(d, v.z, e.z);
+        v.w = fmaf(d, v.w, e.w);
+        *slot = v;
+    }
+    if (state_out) *reinterpret_cast<float4 *>(state_out + i) = v;
+}
+
 template <int N> int64_t scan_warps(int64_t P, int64_t *row_blocks) {
     const int64_t w = (P + ScanShape<N>::kWarpRows - 1) / ScanShape<N>::kWarpRows;
     *row_blocks = (w + kScanWarps - 1) / kScanWarps;
@@ -235,13 +243,13 @@ cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
     const int64_t tiles = a.B * a.H * row_blocks;
     if (tiles * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (a.segments == 1)
-        return launch_dependent(scan_step_kernel<T, N>, (unsigned)tiles, warps * 32, smem, s, a, (int)kScanWhole,
-                                row_blocks);
-    cudaError_t e = launch_dependent(scan_step_kernel<T, N>, (unsigned)(tiles * a.segments), warps * 32, smem, s, a,
-                                     (int)kScanFold, row_blocks);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(scan_step_kernel<T, N>, (unsigned)(a.y ? tiles * a.segments : tiles), warps * 32, smem, s,
-                            a, (int)kScanOutput, row_blocks);
+        return launch_dependent(scan_step_kernel<T, N, kScanWhole>, (unsigned)tiles, warps * 32, smem, s, a, row_blocks);
+    cudaError_t e = launch_dependent(scan_step_kernel<T, N, kScanFold>, (unsigned)(tiles * a.segments), warps * 32, smem,
+                                     s, a, row_blocks);
+    if (e == cudaSuccess) e = launch_scan_join(a, s);
+    if (e != cudaSuccess || !a.y) return e;
+    return launch_dependent(scan_step_kernel<T, N, kScanOutput>, (unsigned)(tiles * a.segments), warps * 32, smem, s, a,
+                            row_blocks);
 }
 
 template <typename T>
@@ -257,6 +265,13 @@ cudaError_t launch_t(const ScanArgs &a, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t launch_scan_join(const ScanArgs &a, cudaStream_t s) {
+    const int64_t per_head = a.P * a.N, tiles = a.B * a.H * per_head, blocks = (tiles + 1023) / 1024;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_dependent(scan_join_kernel, (unsigned)blocks, 256, 0, s, a.workspace,
+                            a.y ? (float *)nullptr : a.state_out, a.segments, tiles, a.B * a.H, per_head);
+}
 
 bool scan_supported_n(int64_t N) { return N == 16 || N == 32 || N == 64 || N == 128 || N == 256; }
 
