@@ -15,9 +15,12 @@ back by repeating a call from its earlier state with ``lengths=accepted`` and
 from __future__ import annotations
 
 import ctypes
+import functools
 from collections import namedtuple
 
 import torch
+
+import linear_attention_recurrence_step_gb300 as _pkg
 
 from . import DTYPE_CODES, _check, _need, load
 
@@ -32,38 +35,57 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream(dev, stream) -> int:
     if stream is None:
-        return _raw_stream(dev.index)
+        return _raw_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# The checks below run on every call, and a short kernel takes no longer than
+# they do: each first tries the one comparison that a good argument passes,
+# and leaves the wording of the error to _need.
+def _lib():
+    return _pkg._lib or load()
+
+
 def _dense(t, name, shape, dtype, dev):
-    """The pointer of a dense tensor (None for None), or the error of ``_need``."""
+    """The pointer of a dense tensor on CUDA device `dev` (None for None), or the error of ``_need``."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
-            and t.is_contiguous()):
-        _need(t, name, shape, dtype, dev)
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, shape, dtype, torch.device("cuda", dev))
     return t.data_ptr()
 
 
 def _device_of(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    """The CUDA device index of a floating tensor."""
+    try:
+        if t.dtype in DTYPE_CODES and t.is_cuda:
+            return t.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype not in DTYPE_CODES:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
-    return t.device
+    raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
 
 
 def _strided(t, name, shape, dtype, dev):
     """Batch and step strides of a [B,T,...] tensor whose inner dimensions are dense."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.shape != shape or t.dtype is not dtype or t.device != dev:
-        _need(t.contiguous() if t.device == dev else t, name, shape, dtype, dev)
-    st = t.stride()
+    try:
+        good = t.shape == shape and t.dtype is dtype and t.get_device() == dev
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if not good:
+        at = torch.device("cuda", dev)
+        _need(t.contiguous() if t.device == at else t, name, shape, dtype, at)
     dense = 1
+    if t.is_contiguous():
+        for n in shape[2:]:
+            dense *= n
+        return dense * shape[1], dense
+    st = t.stride()
     for i in range(len(shape) - 1, 1, -1):
         if st[i] != dense and shape[i] != 1:
             raise ValueError(f"{name}'s dimensions after the second must be dense (strides {st})")
@@ -75,9 +97,14 @@ def _strided(t, name, shape, dtype, dev):
 
 def _rows(t, name, inner_dims):
     """Row stride of a tensor [..., inner] whose leading dimensions collapse into one."""
-    shape, st = t.shape, t.stride()
+    shape = t.shape
     lead = len(shape) - inner_dims
     dense = 1
+    if t.is_contiguous():
+        for n in shape[lead:]:
+            dense *= n
+        return dense
+    st = t.stride()
     for i in range(len(shape) - 1, lead - 1, -1):
         if st[i] != dense and shape[i] != 1:
             raise ValueError(f"{name}'s last dimension(s) must be dense (strides {st})")
@@ -111,12 +138,12 @@ def gdn_causal_conv(x, weight, state_in=None, *, bias=None, lengths=None, activa
     sb, st = _strided(x, "x", (B, T, C), dt, dev)
     if write_y:
         if y is None:
-            y = torch.empty((B, T, C), dtype=dt, device=dev)
+            y = torch.empty((B, T, C), dtype=dt, device=x.device)
     elif y is not None:
         raise ValueError("y is given but write_y is False")
     if state_out is None:
-        state_out = torch.empty((B, W - 1, C), dtype=dt, device=dev)
-    status = load().gdn_causal_conv(
+        state_out = torch.empty((B, W - 1, C), dtype=dt, device=x.device)
+    status = _lib().gdn_causal_conv(
         x.data_ptr(), _dense(weight, "weight", (C, W), dt, dev), _dense(bias, "bias", (C,), dt, dev),
         _dense(state_in, "state_in", (B, W - 1, C), dt, dev), _dense(lengths, "lengths", (B,), torch.int32, dev),
         _dense(y, "y", (B, T, C), dt, dev), _dense(state_out, "state_out", (B, W - 1, C), dt, dev),
@@ -133,6 +160,9 @@ class _ScanStrides(ctypes.Structure):
 def gdn_selective_scan_workspace_size(B: int, T: int, H: int, P: int, N: int) -> int:
     """Bytes of device workspace gdn_selective_scan needs (0 for invalid sizes)."""
     return int(load().gdn_selective_scan_workspace_size(B, T, H, P, N))
+
+
+_scan_workspace = functools.lru_cache(maxsize=256)(gdn_selective_scan_workspace_size)  # a function of the sizes alone
 
 
 def gdn_selective_scan(x, dt, A, B, C, state_in=None, *, D=None, dt_bias=None, softplus: bool = True,
@@ -153,21 +183,20 @@ def gdn_selective_scan(x, dt, A, B, C, state_in=None, *, D=None, dt_bias=None, s
                            *_strided(B, "B", (nb, T, G, N), et, dev), *_strided(C, "C", (nb, T, G, N), et, dev))
     if write_y:
         if y is None:
-            y = torch.empty((nb, T, H, P), dtype=et, device=dev)
+            y = torch.empty((nb, T, H, P), dtype=et, device=x.device)
     elif y is not None:
         raise ValueError("y is given but write_y is False")
     shape = (nb, H, P, N)
     if state_out is None:
-        state_out = torch.empty(shape, dtype=torch.float32, device=dev)
-    lib = load()
+        state_out = torch.empty(shape, dtype=torch.float32, device=x.device)
     if workspace is None:
-        need = lib.gdn_selective_scan_workspace_size(nb, T, H, P, N)
+        need = _scan_workspace(nb, T, H, P, N)
         if need > 16:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     f32 = torch.float32
-    status = lib.gdn_selective_scan(
+    status = _lib().gdn_selective_scan(
         x.data_ptr(), dt.data_ptr(), _dense(A, "A", (H,), f32, dev), B.data_ptr(), C.data_ptr(),
         _dense(D, "D", (H,), f32, dev), _dense(dt_bias, "dt_bias", (H,), f32, dev),
         _dense(state_in, "state_in", shape, f32, dev), _dense(lengths, "lengths", (nb,), torch.int32, dev),
@@ -197,8 +226,8 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
         raise ValueError("weight must be a tensor [D] or [K,D]")
     D = shape[-1]
     per_head = weight.dim() == 2
-    if gate is not None and (gate.shape != shape or gate.dtype is not dt or gate.device != dev):
-        _need(gate.contiguous() if gate.device == dev else gate, "gate", shape, dt, dev)
+    if gate is not None and (gate.shape != shape or gate.dtype is not dt or gate.get_device() != dev):
+        _need(gate.contiguous() if gate.device == x.device else gate, "gate", shape, dt, x.device)
     if not per_head and x.is_contiguous() and (gate is None or gate.is_contiguous()):
         K, xs, gs = 1, D, D
     else:
@@ -209,12 +238,12 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
         gs = xs if gate is None else _rows(gate, "gate", 2)
     M = x.numel() // (K * D) if x.numel() else 0
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=dev)
+        y = torch.empty(shape, dtype=dt, device=x.device)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=dt, device=dev)
+        residual_out = torch.empty(shape, dtype=dt, device=x.device)
     elif residual is None and residual_out is not None:
         raise ValueError("residual_out is given but residual is not")
-    status = load().gdn_gated_norm(
+    status = _lib().gdn_gated_norm(
         x.data_ptr(), _dense(weight, "weight", (K, D) if per_head else (D,), dt, dev),
         None if gate is None else gate.data_ptr(), _dense(residual, "residual", shape, dt, dev),
         _dense(y, "y", shape, dt, dev), _dense(residual_out, "residual_out", shape, dt, dev),
@@ -246,19 +275,19 @@ def gdn_sample(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     V, lead = shape[-1], shape[:-1]
     ls = _rows(logits, "logits", 1)
     if not isinstance(noise, torch.Tensor) or noise.shape != shape or noise.dtype is not torch.float32 \
-            or noise.device != dev:
-        _need(noise, "noise", shape, torch.float32, dev)
+            or noise.get_device() != dev:
+        _need(noise, "noise", shape, torch.float32, logits.device)
     ns = _rows(noise, "noise", 1)
     if token is None:
-        token = torch.empty(lead, dtype=torch.int32, device=dev)
+        token = torch.empty(lead, dtype=torch.int32, device=logits.device)
     if logprob is None:
-        logprob = torch.empty(lead, dtype=torch.float32, device=dev)
+        logprob = torch.empty(lead, dtype=torch.float32, device=logits.device)
     f32 = torch.float32
     tp, tv = _setting(temperature, "temperature", lead, f32, dev, float)
     kp, kv = _setting(top_k, "top_k", lead, torch.int32, dev, int)
     pp, pv = _setting(top_p, "top_p", lead, f32, dev, float)
     mp, mv = _setting(min_p, "min_p", lead, f32, dev, float)
-    status = load().gdn_sample(
+    status = _lib().gdn_sample(
         logits.data_ptr(), noise.data_ptr(), tp, kp, pp, mp, tv, kv, pv, mv,
         _dense(token, "token", lead, torch.int32, dev), _dense(logprob, "logprob", lead, f32, dev),
         logits.numel() // V if V else 0, V, ls, ns, DTYPE_CODES[dt], _stream(dev, stream))
