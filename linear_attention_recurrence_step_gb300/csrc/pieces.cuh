@@ -75,20 +75,23 @@ __device__ __forceinline__ void load_piece(float (&v)[VEC], const T *p) {
     widen<T, VEC>(v, load_raw<T, VEC>(p));
 }
 
+// f32 values rounded to the type.
+template <typename T, int VEC>
+__device__ __forceinline__ RawPiece<T, VEC> narrow_piece(const float (&v)[VEC]) {
+    RawPiece<T, VEC> r;
+    if constexpr (VEC == 1) {
+        r.w = Elem<T>::from_f32(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        r.w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    } else {
+        r.w = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+    }
+    return r;
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void store_piece(T *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        st_from_f32(p, v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-        uint4 w;
-        w.x = pack2<T>(v[0], v[1]);
-        w.y = pack2<T>(v[2], v[3]);
-        w.z = pack2<T>(v[4], v[5]);
-        w.w = pack2<T>(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(p) = w;
-    }
+    store_raw<T, VEC>(p, narrow_piece<T, VEC>(v));
 }
 
 __device__ __forceinline__ float ex2f(float x) {

@@ -12,20 +12,25 @@
 // exponential noise that draws i with probability proportional to e_i), ties
 // to the lowest index.  logprob = (l - max)/T - log(sum of all e_i).
 //
-// So no sort is needed: a cut is a threshold on the logit's ordered bits plus
-// an index limit among equal logits.  A first histogram has bins of equal
-// width in the logit, which spreads the tokens evenly; the tokens of the bin
-// that holds the cut then go into a short list (or, if they do not fit,
-// stay where they are) and histograms over 11 bits of the ordered key at a
-// time (two for 16-bit logits, three for f32) find the exact value.  Where
-// top-k is at most the threads of a CTA, the k-th largest of the threads' own
-// maxima bounds the cut from below and replaces the first histogram.  Masses
-// are summed as integers (units of 2^-40 of the largest token's), so the
-// order of the shared-memory atomics does not change any result.
-//
 // A row is read from memory once, with its maximum and its mass taken on the
-// way: a cluster of CTAs holds its slices in shared memory and goes over them
-// there; the noise is read only for tokens that are left.
+// way: a cluster of CTAs holds its slices in shared memory.  The cuts then go
+// without a sort of the row, by a list of the tokens near the cut:
+//   - top-k up to half a CTA's threads: the k-th largest of the threads' own
+//     maxima bounds the k-th logit of a slice from below, and few more than k
+//     tokens reach it.  One CTA sorts the slices' lists and finishes the row.
+//   - otherwise a histogram over bins of equal width in the logit counts the
+//     tokens.  For top-p the counts bound the mass above each bin to within
+//     the width of one, which leaves a bracket of one or two bins.  A second
+//     pass sums the mass above the bracket and lists the tokens in it; one
+//     CTA sorts the list and finds the exact token at which the cut lies.
+//   - where a list does not fit (many equal logits), histograms over 11 bits
+//     of the logit's ordered key at a time find the value at the cut, and its
+//     tokens are counted in index order.
+// Masses in those are integers (units of 2^-40 of the largest token's), sums
+// are taken in fixed orders, and the order in which a list is filled does not
+// survive its sort: results do not change from run to run.  The noise is read
+// only for tokens that are left.
+//
 #include <cfloat>
 #include <cooperative_groups.h>
 
@@ -40,43 +45,142 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;         // bins of a histogram of masses
+constexpr int kCountBins = 4096;    // bins of a histogram of counts alone (over count and lo)
 constexpr int kMaxCluster = 8;
-constexpr int kList = 1024;     // tokens of a cut's bin that a CTA lists
+constexpr int kList = 1024;         // tokens near a cut that a CTA lists
+constexpr int kSort = 2048;         // tokens near a cut that are sorted
+constexpr int kMaxK = kThreads / 2; // top-k by the threads' maxima
 
-struct SampleShared {
-    uint32_t count[kBins], lo[kBins], hi[kBins];   // histogram: tokens, mass (64 bits in two words)
-    uint2 list[kList];                             // (key, index) of tokens near a cut
-    uint32_t list_n;
-    float fslot[4];                                // this CTA's part of a cluster-wide value
-    uint32_t ties;                                 // this CTA's tokens at the threshold
-    unsigned long long best;                       // this CTA's (key, ~index)
-    float redf[kWarps], redz[kWarps];
-    unsigned long long redm[kWarps];
-    uint32_t redc[kWarps];
-    unsigned long long found_mass;                 // mass before the bin that holds the cut
-    uint32_t found_bin, found_count, found_n;
-    unsigned long long found_w;
-    uint32_t limit;                                // index limit among equal logits
-    float race;                                    // lower bound on the best key so far
+// What is left so far: logits above `l`, and those equal to it with an index
+// below `end`.  Masked tokens (-inf) are never left.
+struct alignas(8) Cut {
+    float l;
+    uint32_t end;
+    __device__ __forceinline__ bool keeps(float x, uint32_t idx) const { return x > l || (x == l && idx < end); }
+};
+__device__ __forceinline__ Cut no_cut() { return Cut{-FLT_MAX, 0xffffffffu}; }
+
+// Shared memory before the row's slice, in 32-bit words, each read and written
+// by itself: word offsets.  A histogram of masses holds tokens, and mass in
+// two words; over the same memory lie a histogram of counts alone, and the
+// list that is sorted (ordered bits, then indexes).
+constexpr uint32_t kCount = 0, kLo = kBins, kHi = 2 * kBins;
+constexpr uint32_t kSortKey = 0, kSortIdx = kSort;
+constexpr uint32_t kListKey = 3 * kBins, kListIdx = kListKey + kList;   // tokens near a cut, of this CTA
+constexpr uint32_t kRed = kListIdx + kList;                             // one word per warp, three times
+constexpr uint32_t kRed2 = kRed + kWarps, kRed3 = kRed2 + kWarps;
+constexpr uint32_t kWords = kRed3 + kWarps;                             // single words
+constexpr uint32_t kPartMax = kWords, kPartZ = kWords + 1, kPartLeast = kWords + 2, kPartSum = kWords + 3,
+                   kPartAbove = kWords + 4, kListN = kWords + 5, kTies = kWords + 6, kBestKey = kWords + 7,
+                   kBestIdx = kWords + 8, kFoundBin = kWords + 9, kFoundLast = kWords + 10, kFoundCount = kWords + 11,
+                   kFoundN = kWords + 12, kFoundMassLo = kWords + 13, kFoundMassHi = kWords + 14,
+                   kFoundWLo = kWords + 15, kFoundWHi = kWords + 16, kLimit = kWords + 17, kCutL = kWords + 18,
+                   kCutEnd = kWords + 19, kRace = kWords + 20;
+constexpr uint32_t kSharedBytes = (kWords + 24) * 4;
+static_assert(kCountBins <= 3 * kBins && 2 * kSort <= 3 * kBins && kSharedBytes % 16 == 0, "layout");
+
+// Word accesses at a CTA's own shared memory, and at that of another CTA of
+// the cluster (`cs` CTAs; a CTA alone takes its own).
+struct Shared {
+    uint32_t base;
+    int cs;
+    __device__ __forceinline__ uint32_t at(uint32_t w) const { return base + 4 * w; }
+    __device__ __forceinline__ uint32_t get(uint32_t w) const {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at(w)) : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void put(uint32_t w, uint32_t v) const {
+        asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(at(w)), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ float getf(uint32_t w) const { return __uint_as_float(get(w)); }
+    __device__ __forceinline__ void putf(uint32_t w, float v) const { put(w, __float_as_uint(v)); }
+    __device__ __forceinline__ uint32_t add(uint32_t w, uint32_t v) const {  // returns what was there
+        uint32_t old;
+        asm volatile("atom.shared.add.u32 %0, [%1], %2;\n" : "=r"(old) : "r"(at(w)), "r"(v) : "memory");
+        return old;
+    }
+    __device__ __forceinline__ void add_only(uint32_t w, uint32_t v) const {
+        asm volatile("red.shared.add.u32 [%0], %1;\n" ::"r"(at(w)), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ void max_only(uint32_t w, uint32_t v) const {
+        asm volatile("red.shared.max.u32 [%0], %1;\n" ::"r"(at(w)), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ uint32_t mapped(uint32_t w, int rank) const {
+        uint32_t a;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(at(w)), "r"(rank));
+        return a;
+    }
+    __device__ __forceinline__ uint32_t get(uint32_t w, int rank) const {
+        if (cs == 1) return get(w);
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(mapped(w, rank)) : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void put(uint32_t w, int rank, uint32_t v) const {
+        if (cs == 1) return put(w, v);
+        asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(mapped(w, rank)), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ float getf(uint32_t w, int rank) const { return __uint_as_float(get(w, rank)); }
+    // every CTA of the cluster in step, and its writes visible to the others
+    __device__ __forceinline__ void sync() const {
+        if (cs > 1) cg::this_cluster().sync();
+        else __syncthreads();
+    }
 };
 
 // The logit as the rules see it: NaN is masked, +inf is the largest finite
-// value of its type, -0 is 0.
-template <typename T> __device__ __forceinline__ float canonical(float x);
-template <> __device__ __forceinline__ float canonical<float>(float x) {
-    return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.f;
+// value of its type.
+template <typename T> __device__ __forceinline__ float largest();
+template <> __device__ __forceinline__ float largest<float>() { return FLT_MAX; }
+template <> __device__ __forceinline__ float largest<__nv_bfloat16>() { return __uint_as_float(0x7f7f0000u); }
+template <> __device__ __forceinline__ float largest<__half>() { return 65504.f; }
+template <typename T> __device__ __forceinline__ float logit(T x) {
+    return fminf(fmaxf(Elem<T>::to_f32(x), -INFINITY), largest<T>());
 }
-template <> __device__ __forceinline__ float canonical<__nv_bfloat16>(float x) {
-    return fminf(fmaxf(x, -INFINITY), __uint_as_float(0x7f7f0000u)) + 0.f;
+// The same for a 16-byte piece, and its largest logit.
+__device__ __forceinline__ uint4 clean(const RawPiece<float, 4> &r) {
+    float v[4];
+    widen<float, 4>(v, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fminf(fmaxf(v[i], -INFINITY), FLT_MAX);
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
-template <> __device__ __forceinline__ float canonical<__half>(float x) {
-    return fminf(fmaxf(x, -INFINITY), 65504.f) + 0.f;
+template <typename H2> __device__ __forceinline__ uint32_t clean2(uint32_t w, uint32_t low, uint32_t high) {
+    const H2 x = __hmin2(__hmax2(*reinterpret_cast<const H2 *>(&w), *reinterpret_cast<const H2 *>(&low)),
+                         *reinterpret_cast<const H2 *>(&high));
+    return *reinterpret_cast<const uint32_t *>(&x);
 }
-template <typename T> __device__ __forceinline__ float logit(T x) { return canonical<T>(Elem<T>::to_f32(x)); }
+__device__ __forceinline__ uint4 clean(const RawPiece<__nv_bfloat16, 8> &r) {
+    constexpr uint32_t low = 0xff80ff80u, high = 0x7f7f7f7fu;
+    return make_uint4(clean2<__nv_bfloat162>(r.w.x, low, high), clean2<__nv_bfloat162>(r.w.y, low, high),
+                      clean2<__nv_bfloat162>(r.w.z, low, high), clean2<__nv_bfloat162>(r.w.w, low, high));
+}
+__device__ __forceinline__ uint4 clean(const RawPiece<__half, 8> &r) {
+    constexpr uint32_t low = 0xfc00fc00u, high = 0x7bff7bffu;
+    return make_uint4(clean2<__half2>(r.w.x, low, high), clean2<__half2>(r.w.y, low, high),
+                      clean2<__half2>(r.w.z, low, high), clean2<__half2>(r.w.w, low, high));
+}
+template <typename H2> __device__ __forceinline__ float max8(const uint4 &w) {
+    const H2 a = __hmax2(*reinterpret_cast<const H2 *>(&w.x), *reinterpret_cast<const H2 *>(&w.y));
+    const H2 b = __hmax2(*reinterpret_cast<const H2 *>(&w.z), *reinterpret_cast<const H2 *>(&w.w));
+    const H2 c = __hmax2(a, b);
+    return fmaxf(__low2float(c), __high2float(c));
+}
+template <typename T> __device__ __forceinline__ float piece_max(const uint4 &w);
+template <> __device__ __forceinline__ float piece_max<__nv_bfloat16>(const uint4 &w) { return max8<__nv_bfloat162>(w); }
+template <> __device__ __forceinline__ float piece_max<__half>(const uint4 &w) { return max8<__half2>(w); }
+template <> __device__ __forceinline__ float piece_max<float>(const uint4 &w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
 __device__ __forceinline__ uint32_t order_bits(float l) {
-    const uint32_t u = __float_as_uint(l);
+    const uint32_t u = __float_as_uint(l + 0.f);  // -0 is 0
     return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_order_bits(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -84,97 +188,147 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// What is left so far: the key's high bits above `prefix`, or equal to it
-// with an index of at most `limit`.
-struct Cut {
-    uint32_t prefix = 0, limit = 0xffffffffu;
-    int shift = 10;
-    __device__ __forceinline__ bool keeps(uint32_t key, uint32_t idx) const {
-        const uint32_t p = key >> shift;
-        return p > prefix || (p == prefix && idx <= limit);
-    }
-};
+__device__ __forceinline__ uint4 piece_at(uint32_t shared_addr) {
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(shared_addr)
+                 : "memory");
+    return w;
+}
+// 16 bytes of a row, and one noise value; the addresses are aligned by how they
+// are made, and kept so.
+__device__ __forceinline__ uint4 row_piece(const void *p) {
+    uint4 w;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(reinterpret_cast<uint64_t>(p) & ~(uint64_t)15));
+    return w;
+}
+__device__ __forceinline__ float noise_at(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];\n" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void put_piece(uint32_t shared_addr, const uint4 &w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(shared_addr), "r"(w.x), "r"(w.y), "r"(w.z),
+                 "r"(w.w)
+                 : "memory");
+}
+template <typename T> __device__ __forceinline__ float element_at(uint32_t shared_addr);
+template <> __device__ __forceinline__ float element_at<float>(uint32_t shared_addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(shared_addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint16_t half_at(uint32_t shared_addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(shared_addr) : "memory");
+    return v;
+}
+template <> __device__ __forceinline__ float element_at<__nv_bfloat16>(uint32_t shared_addr) {
+    return unpack2<__nv_bfloat16>(half_at(shared_addr)).x;
+}
+template <> __device__ __forceinline__ float element_at<__half>(uint32_t shared_addr) {
+    return unpack2<__half>(half_at(shared_addr)).x;
+}
 
 template <typename T, bool CACHED> struct Row {
-    const T *buf;        // shared memory (CACHED) or the row's slice in memory
-    int mis;             // buf[mis] is the slice's first token when CACHED
+    uint32_t pieces;     // CACHED: shared address of the slice's pieces (16-byte aligned)
+    int mis;             // CACHED: elements before the slice's first in its first piece
+    const T *src;        // the slice in memory
     int64_t n;           // tokens in the slice
     uint32_t base;       // index of the first
-    // f(logit, index) for every token of the slice, thread by thread; pieces
-    // in shared memory hold logits as logit() gives them, and -inf around the
-    // slice
-    template <typename F> __device__ __forceinline__ void each(F &&f) const {
+    // f(logit, index) for every token of the slice with a logit of at least
+    // `low` (above -inf), thread by thread.  Pieces in shared memory hold
+    // clean logits, and -inf around the slice; a piece without such a token
+    // costs one comparison.
+    template <typename F> __device__ __forceinline__ void each(float low, F &&f) const {
         if constexpr (CACHED) {
             constexpr int VE = 16 / sizeof(T);
             const int nvec = (int)((mis + n + VE - 1) / VE);
             for (int j = threadIdx.x; j < nvec; j += kThreads) {
+                RawPiece<T, VE> raw;
+                raw.w = piece_at(pieces + 16 * j);
+                if (piece_max<T>(raw.w) < low) continue;
                 float v[VE];
-                load_piece<T, VE>(v, buf + (int64_t)j * VE);
+                widen<T, VE>(v, raw);
 #pragma unroll
-                for (int e = 0; e < VE; ++e) f(v[e], base + (uint32_t)(j * VE + e - mis));
+                for (int e = 0; e < VE; ++e)
+                    if (v[e] >= low) f(v[e], base + (uint32_t)(j * VE + e - mis));
             }
         } else {
-            for (int64_t i = threadIdx.x; i < n; i += kThreads) f(logit(buf[i]), base + (uint32_t)i);
+            for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+                const float l = logit(src[i]);
+                if (l >= low) f(l, base + (uint32_t)i);
+            }
         }
     }
     __device__ __forceinline__ float at(int64_t i) const {
-        return CACHED ? Elem<T>::to_f32(buf[mis + i]) : logit(buf[i]);
+        return CACHED ? element_at<T>(pieces + (uint32_t)((mis + i) * sizeof(T))) : logit(src[i]);
     }
 };
 
-__device__ __forceinline__ float block_sum(float v, SampleShared &sh) {
+__device__ __forceinline__ unsigned long long join64(uint32_t lo, uint32_t hi) {
+    return (unsigned long long)lo | ((unsigned long long)hi << 32);
+}
+
+__device__ __forceinline__ float block_sum(float v, const Shared &sh) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.redf[threadIdx.x / 32] = v;
+    if (threadIdx.x % 32 == 0) sh.putf(kRed + threadIdx.x / 32, v);
     __syncthreads();
     v = 0.f;
-    for (int i = 0; i < kWarps; ++i) v += sh.redf[i];
+    for (int i = 0; i < kWarps; ++i) v += sh.getf(kRed + i);
     return v;
 }
 
-__device__ __forceinline__ void cluster_sync(int cs) {
-    if (cs > 1) cg::this_cluster().sync();
-    else __syncthreads();
-}
-// A value in another CTA's shared memory of the cluster.
-template <typename V> __device__ __forceinline__ V *remote(V *p, int rank, int cs) {
-    return cs > 1 ? cg::this_cluster().map_shared_rank(p, rank) : p;
+// Sums `words` counters over the CTAs: each adds up its share and hands the
+// sums to all; it alone reads and writes those.
+__device__ __forceinline__ void merge_bins(const Shared &sh, uint32_t first, int words, int rank) {
+    const int share = words / sh.cs;
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+        const uint32_t w = first + rank * share + i;
+        uint32_t part[kMaxCluster], sum = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) part[q] = q < sh.cs ? sh.get(w, q) : 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) sum += part[q];
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+            if (q < sh.cs) sh.put(w, q, sum);
+    }
 }
 
 // The bin, counted from the top, of a histogram (over all CTAs of the cluster)
 // in which the running count reaches `k` or the running mass reaches
-// `target`; found_bin stays ~0 if none does.  Counts and masses of higher
-// bins than any of the histogram are given.
+// `target`; kFoundBin stays ~0 if none does.  The running values start from
+// `above_count` and `above_mass`.
 template <bool MASS>
-__device__ void find_bin(SampleShared &sh, int cs, int rank, uint32_t above_count, unsigned long long above_mass,
-                         uint32_t k, double target) {
-    if (cs > 1) {
-        // each CTA adds up its share of the bins and hands the sums to all; it
-        // alone reads and writes those bins
-        cg::this_cluster().sync();
-        const int share = kBins / cs;
+__device__ __forceinline__ void find_bin(const Shared &sh, int rank, uint32_t above_count,
+                                         unsigned long long above_mass, uint32_t k, double target) {
+    sh.sync();
+    if (sh.cs > 1) {
+        // two-word masses: the CTAs' low words are summed apart from their carry
+        const int share = kBins / sh.cs;
         for (int i = threadIdx.x; i < share; i += kThreads) {
-            const int bin = rank * share + i;
+            const uint32_t bin = rank * share + i;
             uint32_t c = 0;
             unsigned long long m = 0;
-            for (int q = 0; q < cs; ++q) {
-                c += *remote(&sh.count[bin], q, cs);
-                if (MASS)
-                    m += (unsigned long long)*remote(&sh.lo[bin], q, cs) +
-                         ((unsigned long long)*remote(&sh.hi[bin], q, cs) << 32);
+            for (int q = 0; q < sh.cs; ++q) {
+                c += sh.get(kCount + bin, q);
+                if (MASS) m += join64(sh.get(kLo + bin, q), sh.get(kHi + bin, q));
             }
-            for (int q = 0; q < cs; ++q) {
-                *remote(&sh.count[bin], q, cs) = c;
+            for (int q = 0; q < sh.cs; ++q) {
+                sh.put(kCount + bin, q, c);
                 if (MASS) {
-                    *remote(&sh.lo[bin], q, cs) = (uint32_t)m;
-                    *remote(&sh.hi[bin], q, cs) = (uint32_t)(m >> 32);
+                    sh.put(kLo + bin, q, (uint32_t)m);
+                    sh.put(kHi + bin, q, (uint32_t)(m >> 32));
                 }
             }
         }
-        cg::this_cluster().sync();
-    } else {
-        __syncthreads();
+        sh.sync();
     }
     // running sums from the top bin: PB bins per thread
     constexpr int PB = kBins / kThreads;
@@ -182,9 +336,9 @@ __device__ void find_bin(SampleShared &sh, int cs, int rank, uint32_t above_coun
     unsigned long long m[PB], mtot = 0;
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
-        const int bin = kBins - 1 - (threadIdx.x * PB + j);
-        c[j] = sh.count[bin];
-        m[j] = MASS ? (unsigned long long)sh.lo[bin] + ((unsigned long long)sh.hi[bin] << 32) : 0;
+        const uint32_t bin = kBins - 1 - (threadIdx.x * PB + j);
+        c[j] = sh.get(kCount + bin);
+        m[j] = MASS ? join64(sh.get(kLo + bin), sh.get(kHi + bin)) : 0;
         ctot += c[j];
         mtot += m[j];
     }
@@ -201,26 +355,29 @@ __device__ void find_bin(SampleShared &sh, int cs, int rank, uint32_t above_coun
         }
     }
     if (lane == 31) {
-        sh.redc[warp] = cin;
-        sh.redm[warp] = min_;
+        sh.put(kRed + warp, cin);
+        sh.put(kRed2 + warp, (uint32_t)min_);
+        sh.put(kRed3 + warp, (uint32_t)(min_ >> 32));
     }
     __syncthreads();
     uint32_t cbase = above_count + cin - ctot;
     unsigned long long mbase = above_mass + min_ - mtot;
     for (int i = 0; i < warp; ++i) {
-        cbase += sh.redc[i];
-        mbase += sh.redm[i];
+        cbase += sh.get(kRed + i);
+        mbase += join64(sh.get(kRed2 + i), sh.get(kRed3 + i));
     }
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
         const bool before = MASS ? (double)mbase < target : cbase < k;
         const bool reached = MASS ? (double)(mbase + m[j]) >= target : cbase + c[j] >= k;
         if (before && reached) {
-            sh.found_bin = kBins - 1 - (threadIdx.x * PB + j);
-            sh.found_count = cbase;
-            sh.found_mass = mbase;
-            sh.found_n = c[j];
-            sh.found_w = m[j];
+            sh.put(kFoundBin, kBins - 1 - (threadIdx.x * PB + j));
+            sh.put(kFoundCount, cbase);
+            sh.put(kFoundMassLo, (uint32_t)mbase);
+            sh.put(kFoundMassHi, (uint32_t)(mbase >> 32));
+            sh.put(kFoundN, c[j]);
+            sh.put(kFoundWLo, (uint32_t)m[j]);
+            sh.put(kFoundWHi, (uint32_t)(m[j] >> 32));
         }
         cbase += c[j];
         mbase += m[j];
@@ -228,179 +385,340 @@ __device__ void find_bin(SampleShared &sh, int cs, int rank, uint32_t above_coun
     __syncthreads();
 }
 
-// Clears the histogram; a barrier follows.
-template <bool MASS> __device__ __forceinline__ void clear_bins(SampleShared &sh) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        sh.count[i] = 0;
-        if (MASS) sh.lo[i] = sh.hi[i] = 0;
-    }
-    if (threadIdx.x == 0) sh.found_bin = 0xffffffffu;
-    __syncthreads();
-}
-
 // e in units of 2^-40 added to a bin's mass.
-__device__ __forceinline__ void add_mass(SampleShared &sh, uint32_t bin, float e) {
+__device__ __forceinline__ void add_mass(const Shared &sh, uint32_t bin, float e) {
     uint32_t wh = 0;
     if (e >= 0x1p-8f) {
         wh = __float2uint_rz(e * 0x1p8f);
         e -= (float)wh * 0x1p-8f;
     }
     const uint32_t wl = __float2uint_rz(e * 0x1p40f);
-    const uint32_t old = atomicAdd(&sh.lo[bin], wl);
+    const uint32_t old = sh.add(kLo + bin, wl);
     if (old + wl < old) ++wh;
-    if (wh) atomicAdd(&sh.hi[bin], wh);
+    if (wh) sh.add_only(kHi + bin, wh);
 }
 
-// Narrows `cut` to the tokens before the place where the running count reaches
-// `k` (or the running mass reaches `target`), in the order (l descending,
-// index ascending), among those of which `in(l, idx)` holds; `mass(l)` is a
-// token's e.  scale > 0: a histogram of bins of width 1/scale below `mx` comes
-// first.  Without it, the tokens that take part should be few.
+// `cut`, narrowed to the tokens before the place where the running count
+// reaches `k` (or the running mass reaches `target`), in the order (l
+// descending, index ascending), among those of logit `low` or more of which
+// `in(l, idx)` holds; `mass(l)` is a token's e.  For any number of tokens at
+// the cut.
 template <bool MASS, int ROUNDS, typename RowT, typename In, typename Mass>
-__device__ void narrow(const RowT &row, SampleShared &sh, int cs, int rank, Cut &cut, uint32_t k, double target,
-                       float mx, float scale, In &&in, Mass &&mass) {
-    uint32_t above_count = 0;
+__device__ __forceinline__ Cut narrow(const RowT &row, const Shared &sh, int rank, const Cut cut, uint32_t k,
+                                      double target, float low, In &&in, Mass &&mass) {
+    uint32_t above_count = 0, prefix = 0;
     unsigned long long above_mass = 0;
-    auto linear = [&](float l) { return kBins - 1 - min(kBins - 1, __float2int_rz((mx - l) * scale)); };
-    int lin_bin = -1;
-    if (scale > 0.f) {
-        clear_bins<MASS>(sh);
-        row.each([&](float l, uint32_t idx) {
-            if (!in(l, idx)) return;
-            const int bin = linear(l);
-            if (MASS) add_mass(sh, bin, mass(l));
-            else atomicAdd(&sh.count[bin], 1u);
-        });
-        find_bin<MASS>(sh, cs, rank, 0, 0, k, target);
-        if (sh.found_bin == 0xffffffffu) return;  // every token that takes part is left
-        lin_bin = (int)sh.found_bin;
-        above_count = sh.found_count;
-        above_mass = sh.found_mass;
-    }
-    // the tokens of that bin, listed
-    auto near = [&](float l, uint32_t idx) { return (lin_bin < 0 || linear(l) == lin_bin) && in(l, idx); };
-    __syncthreads();
-    if (threadIdx.x == 0) sh.list_n = 0;
-    __syncthreads();
-    row.each([&](float l, uint32_t idx) {
-        if (!near(l, idx)) return;
-        const uint32_t at = atomicAdd(&sh.list_n, 1u);
-        if (at < kList) sh.list[at] = make_uint2(__float_as_uint(l), idx);
-    });
-    __syncthreads();
-    const uint32_t listed = sh.list_n;
-    const bool in_list = listed <= kList;
-    auto visit = [&](auto &&f) {
-        if (in_list)
-            for (uint32_t i = threadIdx.x; i < listed; i += kThreads) f(__uint_as_float(sh.list[i].x), sh.list[i].y);
-        else
-            row.each([&](float l, uint32_t idx) {
-                if (near(l, idx)) f(l, idx);
-            });
-    };
-    uint32_t prefix = 0;
     int shift = 32;
 #pragma unroll 1
     for (int round = 0; round < ROUNDS; ++round) {
         const int bits = round == 2 ? 10 : 11;
         const int next = shift - bits;
-        clear_bins<MASS>(sh);
-        visit([&](float l, uint32_t) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            sh.put(kCount + i, 0);
+            if (MASS) {
+                sh.put(kLo + i, 0);
+                sh.put(kHi + i, 0);
+            }
+        }
+        if (threadIdx.x == 0) sh.put(kFoundBin, 0xffffffffu);
+        __syncthreads();
+        row.each(low, [&](float l, uint32_t idx) {
             const uint32_t key = order_bits(l);
-            if (round > 0 && (key >> shift) != prefix) return;
+            if ((round > 0 && (key >> shift) != prefix) || !in(l, idx)) return;
             const uint32_t bin = (key >> next) & ((1u << bits) - 1);
-            atomicAdd(&sh.count[bin], 1u);
+            sh.add_only(kCount + bin, 1u);
             if (MASS) add_mass(sh, bin, mass(l));
         });
-        find_bin<MASS>(sh, cs, rank, above_count, above_mass, k, target);
-        if (sh.found_bin == 0xffffffffu) return;  // every token that takes part is left
-        prefix = (prefix << bits) | sh.found_bin;
+        find_bin<MASS>(sh, rank, above_count, above_mass, k, target);
+        const uint32_t bin = sh.get(kFoundBin);
+        if (bin == 0xffffffffu) return cut;  // every token that takes part is left
+        prefix = (prefix << bits) | bin;
         shift = next;
-        above_count = sh.found_count;
-        above_mass = sh.found_mass;
-        __syncthreads();
+        above_count = sh.get(kFoundCount);
+        above_mass = join64(sh.get(kFoundMassLo), sh.get(kFoundMassHi));
     }
-    // the tokens of the last bin are equal: the first `want` of them stay
-    const uint32_t n_eq = sh.found_n;
+    // the tokens of the last bin are equal (16-bit logits have equal low bits
+    // of the key): the first `want` of them stay
+    const float l_eq =
+        from_order_bits((prefix << shift) | (shift > 0 && prefix >> (31 - shift) == 0 ? (1u << shift) - 1 : 0));
+    const uint32_t n_eq = sh.get(kFoundN);
     uint32_t want;
     if (MASS) {
-        const double each = (double)sh.found_w / n_eq;
+        const double each = (double)join64(sh.get(kFoundWLo), sh.get(kFoundWHi)) / n_eq;
         const double q = each > 0 ? ceil((target - (double)above_mass) / each) : 1.0;
         want = q < 1 ? 1 : (q > (double)n_eq ? n_eq : (uint32_t)q);
     } else {
         want = k - above_count;
     }
-    uint32_t limit = 0xffffffffu;
+    uint32_t end = 0xffffffffu;
     if (want < n_eq) {
-        // index of the want-th of them: the CTAs' slices are in index order
+        // index of the want-th of them: the CTAs' slices are in index order,
+        // and so are the warps' parts of a slice
         const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
         const int64_t per = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
         const int64_t i0 = warp * per, i1 = i0 + per < row.n ? i0 + per : row.n;
-        auto equal = [&](int64_t i) {
-            if (i >= i1) return false;
-            const float l = row.at(i);
-            return (order_bits(l) >> shift) == prefix && near(l, row.base + (uint32_t)i);
-        };
-        uint32_t mine = 0;  // this warp's share: of the list, or of the slice (contiguous ranges)
-        if (in_list) {
-            for (uint32_t i = threadIdx.x; i < (listed + 31) / 32 * 32; i += kThreads)
-                mine += __popc(__ballot_sync(0xffffffffu, i < listed && (order_bits(__uint_as_float(sh.list[i].x)) >> shift) == prefix));
-        } else {
-            for (int64_t i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i + lane)));
-        }
-        if (lane == 0) sh.redc[warp] = mine;
+        auto equal = [&](int64_t i) { return i < i1 && row.at(i) == l_eq && in(l_eq, row.base + (uint32_t)i); };
+        uint32_t mine = 0;
+        for (int64_t i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i + lane)));
+        if (lane == 0) sh.put(kRed + warp, mine);
         __syncthreads();
         if (threadIdx.x == 0) {
             uint32_t s = 0;
-            for (int i = 0; i < kWarps; ++i) s += sh.redc[i];
-            sh.ties = s;
+            for (int i = 0; i < kWarps; ++i) s += sh.get(kRed + i);
+            sh.put(kTies, s);
         }
-        cluster_sync(cs);
+        sh.sync();
         uint32_t before = 0;
-        for (int q = 0; q < rank; ++q) before += *remote(&sh.ties, q, cs);
-        if (in_list) {
-            if (before < want && want <= before + sh.ties)
-                for (uint32_t i = threadIdx.x; i < listed; i += kThreads) {
-                    if ((order_bits(__uint_as_float(sh.list[i].x)) >> shift) != prefix) continue;
-                    const uint32_t idx = sh.list[i].y;
-                    uint32_t at = before;  // equal ones of a lower index
-                    for (uint32_t j = 0; j < listed; ++j)
-                        at += (order_bits(__uint_as_float(sh.list[j].x)) >> shift) == prefix && sh.list[j].y < idx;
-                    if (at == want - 1)
-                        for (int q = 0; q < cs; ++q) *remote(&sh.limit, q, cs) = idx;
+        for (int q = 0; q < rank; ++q) before += sh.get(kTies, q);
+        for (int i = 0; i < warp; ++i) before += sh.get(kRed + i);
+        if (before < want && want <= before + mine) {
+            uint32_t left = want - before;  // the left-th of this warp's
+            for (int64_t i = i0; i < i1; i += 32) {
+                const uint32_t m = __ballot_sync(0xffffffffu, equal(i + lane));
+                const uint32_t c = __popc(m);
+                if (left <= c) {
+                    const int pos = __fns(m, 0, (int)left);
+                    if (lane == 0)
+                        for (int q = 0; q < sh.cs; ++q) sh.put(kLimit, q, row.base + (uint32_t)(i + pos));
+                    break;
                 }
-        } else {
-            for (int i = 0; i < warp; ++i) before += sh.redc[i];
-            if (before < want && want <= before + mine) {
-                uint32_t left = want - before;  // the left-th of this warp's
-                for (int64_t i = i0; i < i1; i += 32) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, equal(i + lane));
-                    const uint32_t c = __popc(m);
-                    if (left <= c) {
-                        const int pos = __fns(m, 0, (int)left);
-                        if (lane == 0)
-                            for (int q = 0; q < cs; ++q) *remote(&sh.limit, q, cs) = row.base + (uint32_t)(i + pos);
-                        break;
-                    }
-                    left -= c;
+                left -= c;
+            }
+        }
+        sh.sync();
+        end = sh.get(kLimit) + 1;
+    }
+    return Cut{l_eq, end};
+}
+
+// Appends a token to this CTA's list (past its end, only counts it).
+__device__ __forceinline__ void enlist(const Shared &sh, float l, uint32_t idx) {
+    const uint32_t at = sh.add(kListN, 1u);
+    if (at < kList) {
+        sh.put(kListKey + at, order_bits(l));
+        sh.put(kListIdx + at, idx);
+    }
+}
+
+// After the lists are full and the cluster is in step: tokens in all lists, or
+// -1 if one of them or their sum does not fit.
+__device__ __forceinline__ int listed(const Shared &sh) {
+    int total = 0;
+    bool fits = true;
+    for (int q = 0; q < sh.cs; ++q) {
+        const uint32_t c = sh.get(kListN, q);
+        fits = fits && c <= kList;
+        total += (int)(c <= kList ? c : 0);
+    }
+    return fits && total <= kSort ? total : -1;
+}
+
+// The lists of all CTAs sorted, the first token of the order first.
+__device__ __forceinline__ void sort_lists(const Shared &sh, int total) {
+    int at = 0;
+    for (int q = 0; q < sh.cs; ++q) {
+        const int c = (int)sh.get(kListN, q);
+        for (int i = threadIdx.x; i < c; i += kThreads) {
+            sh.put(kSortKey + at + i, sh.get(kListKey + i, q));
+            sh.put(kSortIdx + at + i, sh.get(kListIdx + i, q));
+        }
+        at += c;
+    }
+    int n = 32;
+    while (n < total) n *= 2;
+    for (int i = total + threadIdx.x; i < n; i += kThreads) {  // after every token
+        sh.put(kSortKey + i, 0);
+        sh.put(kSortIdx + i, 0xffffffffu);
+    }
+    for (int size = 2; size <= n; size *= 2)
+        for (int step = size / 2; step > 0; step /= 2) {
+            __syncthreads();
+            for (int p = threadIdx.x; p < n / 2; p += kThreads) {
+                const int i = 2 * p - (p & (step - 1)), j = i + step;
+                const uint32_t kx = sh.get(kSortKey + i), ky = sh.get(kSortKey + j);
+                const uint32_t ix = sh.get(kSortIdx + i), iy = sh.get(kSortIdx + j);
+                const bool first = kx > ky || (kx == ky && ix < iy);  // x before y
+                if (first != ((i & size) == 0)) {
+                    sh.put(kSortKey + i, ky);
+                    sh.put(kSortKey + j, kx);
+                    sh.put(kSortIdx + i, iy);
+                    sh.put(kSortIdx + j, ix);
                 }
             }
         }
-        cluster_sync(cs);
-        limit = sh.limit;
+    __syncthreads();
+}
+
+// Of the first n sorted tokens, how many have less than `target` of mass
+// before them, with `above` before the first; *total is the mass of the n.
+template <typename Mass>
+__device__ __forceinline__ int mass_prefix(const Shared &sh, int n, double above, double target, Mass &&mass,
+                                           double *total) {
+    constexpr int PER = kSort / kThreads;
+    double own[PER], sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = threadIdx.x * PER + j;
+        own[j] = i < n ? (double)mass(from_order_bits(sh.get(kSortKey + i))) : 0.0;
+        sum += own[j];
     }
-    cut.prefix = prefix;
-    cut.shift = shift;
-    cut.limit = limit;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    double in = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double v = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += v;
+    }
+    __syncthreads();
+    if (lane == 31) {
+        const unsigned long long w = (unsigned long long)__double_as_longlong(in);
+        sh.put(kRed + warp, (uint32_t)w);
+        sh.put(kRed2 + warp, (uint32_t)(w >> 32));
+    }
+    __syncthreads();
+    double before = above, all = 0.0;
+    for (int i = 0; i < kWarps; ++i) {
+        const double v = __longlong_as_double((long long)join64(sh.get(kRed + i), sh.get(kRed2 + i)));
+        if (i < warp) before += v;
+        all += v;
+    }
+    before += in - sum;
+    *total = all;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if ((int)threadIdx.x * PER + j < n && before < target) ++count;
+        before += own[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    __syncthreads();
+    if (lane == 0) sh.put(kRed + warp, (uint32_t)count);
+    __syncthreads();
+    count = 0;
+    for (int i = 0; i < kWarps; ++i) count += (int)sh.get(kRed + i);
+    return count;
+}
+
+// The cut at which the running count of tokens reaches `k`, or the running
+// mass `target`, by a histogram of counts over bins of width 1/scale below
+// `mx` and a sorted list of the bin (of the bracket) that holds it; `width` is
+// a bin's in units of log(e).  False: the list does not fit.
+template <bool MASS, typename RowT, typename In, typename Mass>
+__device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, int rank, Cut &cut, uint32_t k,
+                                            double target, float mx, float scale, float width, float low, In &&in,
+                                            Mass &&mass) {
+    // 0 is the top bin
+    auto bin_of = [&](float l) { return max(0, min(kCountBins - 1, __float2int_rz((mx - l) * scale))); };
+    __syncthreads();
+    for (int i = threadIdx.x; i < kCountBins; i += kThreads) sh.put(kCount + i, 0);
+    if (threadIdx.x == 0) {
+        sh.put(kFoundBin, kCountBins - 1);
+        sh.put(kFoundLast, kCountBins - 1);
+        sh.put(kFoundCount, 0);
+        sh.put(kListN, 0);
+    }
+    __syncthreads();
+    row.each(low, [&](float l, uint32_t idx) {
+        if (in(l, idx)) sh.add_only(kCount + bin_of(l), 1u);
+    });
+    sh.sync();
+    if (sh.cs > 1) {
+        merge_bins(sh, kCount, kCountBins, rank);
+        sh.sync();
+    }
+    // running sums over the bins: of tokens, or of an upper bound on their mass
+    // (a token's e is at most that of its bin's upper edge, and at least that
+    // times exp(-width): the true sum lies between the bound and that share)
+    constexpr int PB = kCountBins / kThreads;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    float part[PB], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+        const int bin = threadIdx.x * PB + j;
+        part[j] = (float)sh.get(kCount + bin);
+        if (MASS) part[j] *= ex2(-1.44269504088896341f * width * (float)bin);
+        sum += part[j];
+    }
+    float incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.putf(kRed + warp, incl);
+    __syncthreads();
+    float run = 0.f;
+    for (int i = 0; i < warp; ++i) run += sh.getf(kRed + i);
+    run += incl - sum;
+    // counts are exact in f32 up to 2^24; masses have room for the roundings
+    const float first = MASS ? (float)target * 0.9999f : (float)k;
+    const float last = MASS ? (float)target * 1.0001f * expf(width) : (float)k;
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+        const int bin = threadIdx.x * PB + j;
+        const float next = run + part[j];
+        if (run < first && next >= first) {
+            sh.put(kFoundBin, bin);
+            sh.put(kFoundCount, (uint32_t)run);
+        }
+        if (run < last && next >= last) sh.put(kFoundLast, bin);
+        run = next;
+    }
+    __syncthreads();
+    const int b0 = (int)sh.get(kFoundBin), b1 = (int)sh.get(kFoundLast);
+    const uint32_t above_count = sh.get(kFoundCount);
+    float above = 0.f;
+    row.each(low, [&](float l, uint32_t idx) {
+        const int bin = bin_of(l);
+        if (bin > b1 || !in(l, idx)) return;
+        if (bin >= b0) enlist(sh, l, idx);
+        else if (MASS) above += mass(l);
+    });
+    if (MASS) {
+        above = block_sum(above, sh);
+        if (threadIdx.x == 0) sh.putf(kPartAbove, above);
+    }
+    sh.sync();
+    const int total = listed(sh);
+    if (total < 0) return false;
+    if (rank == 0) {
+        double mass_above = 0.0;
+        if (MASS)
+            for (int q = 0; q < sh.cs; ++q) mass_above += (double)sh.getf(kPartAbove, q);
+        sort_lists(sh, total);
+        int keep;
+        if (MASS) {
+            double all;
+            keep = mass_prefix(sh, total, mass_above, target, mass, &all);
+        } else {
+            keep = min(total, (int)(k - above_count));
+        }
+        if ((int)threadIdx.x < sh.cs) {
+            float l = -FLT_MAX;
+            uint32_t end = 0xffffffffu;
+            if (total > 0) {  // none kept: everything above the first of the list
+                const int i = keep > 0 ? keep - 1 : 0;
+                l = from_order_bits(sh.get(kSortKey + i));
+                end = keep > 0 ? sh.get(kSortIdx + i) + 1 : 0;
+            }
+            sh.put(kCutL, (int)threadIdx.x, __float_as_uint(l));
+            sh.put(kCutEnd, (int)threadIdx.x, end);
+        }
+    }
+    sh.sync();
+    cut.l = sh.getf(kCutL);
+    cut.end = sh.get(kCutEnd);
+    return true;
 }
 
 template <typename T, bool CACHED>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, const int cs, const int64_t slice) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, const int cs, const int64_t slice) {
     constexpr int VE = 16 / sizeof(T);
     constexpr int ROUNDS = sizeof(T) == 2 ? 2 : 3;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    SampleShared &sh = *reinterpret_cast<SampleShared *>(smem_raw);
-    T *buf = reinterpret_cast<T *>(smem_raw + align16(sizeof(SampleShared)));
+    const Shared sh{static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)), cs};
     pdl_trigger();
     pdl_wait();
     const int64_t r = blockIdx.x / cs;
@@ -410,21 +728,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, co
     const T *src = static_cast<const T *>(a.logits) + r * a.logits_st + base;
     const float *noise = a.noise + r * a.noise_st;
 
-    // the row's settings
+    // the row's settings; a temperature below 2^-100 acts as that
     float temp = a.temperature ? a.temperature[r] : a.temperature_v;
     const float top_p = a.top_p ? a.top_p[r] : a.top_p_v;
     const float min_p = a.min_p ? a.min_p[r] : a.min_p_v;
     const int32_t top_k = a.top_k ? a.top_k[r] : a.top_k_v;
     const bool only_first = !(temp > 0.f) || top_p <= 0.f || min_p > 1.f || top_k == 1;
-    temp = temp > 0.f ? fminf(temp, FLT_MAX) : 1.f;
+    temp = temp > 0.f ? fminf(fmaxf(temp, 0x1p-100f), FLT_MAX) : 1.f;
     const bool use_k = !only_first && top_k > 0 && top_k < a.V;
     const bool use_p = !only_first && top_p < 1.f;
     const bool use_m = !only_first && min_p > 0.f;
     const float to_log2 = 1.44269504088896341f / temp;
-    const bool safe_scale = to_log2 < 1e30f;  // a temperature near zero: divide instead
-    auto e_below = [&](float l, float top) {
-        return safe_scale ? ex2((l - top) * to_log2) : ex2((l - top) / temp * 1.44269504088896341f);
-    };
+    auto e_below = [&](float l, float top) { return ex2((l - top) * to_log2); };
 
     // the slice into shared memory, with each thread's maximum and mass
     Row<T, CACHED> row;
@@ -432,20 +747,27 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, co
     row.base = (uint32_t)base;
     row.mis = CACHED ? (int)(reinterpret_cast<uintptr_t>(src) / sizeof(T) % VE) : 0;
     float my_max = -INFINITY, my_z = 0.f;
-    auto take = [&](const float (&v)[VE]) {
-        float top = v[0];
-#pragma unroll
-        for (int e = 1; e < VE; ++e) top = fmaxf(top, v[e]);
+    auto take = [&](const uint4 &w) {
+        const float top = piece_max<T>(w);
         if (top > my_max) {
             my_z *= e_below(my_max, top);
             my_max = top;
         }
-        if (my_max > -INFINITY)
+        if (top == -INFINITY) return;
+        RawPiece<T, VE> raw;
+        raw.w = w;
+        float v[VE];
+        widen<T, VE>(v, raw);
+        const float2 m2 = make_float2(-my_max, -my_max), c2 = make_float2(to_log2, to_log2);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) my_z += e_below(v[e], my_max);
+        for (int e = 0; e < VE; e += 2) {
+            const float2 d = fmul2(__fadd2_rn(make_float2(v[e], v[e + 1]), m2), c2);
+            my_z += ex2(d.x) + ex2(d.y);
+        }
     };
+    row.src = src;
+    row.pieces = sh.base + kSharedBytes;
     if constexpr (CACHED) {
-        row.buf = buf;
         const int nvec = (int)((row.mis + n + VE - 1) / VE);
         constexpr int AHEAD = 4;  // pieces of a thread in flight
         for (int j0 = threadIdx.x; j0 < nvec; j0 += AHEAD * kThreads) {
@@ -453,34 +775,40 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, co
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int64_t i = (int64_t)(j0 + u * kThreads) * VE - row.mis;
-                if (i >= 0 && i + VE <= n) raw[u] = load_raw<T, VE>(src + i);
+                if (i >= 0 && i + VE <= n) {
+                    raw[u].w = row_piece(src + i);
+                } else {  // the slice's ends: -inf beside it
+                    float v[VE];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        v[e] = i + e >= 0 && i + e < n ? Elem<T>::to_f32(src[i + e]) : -INFINITY;
+                    raw[u] = narrow_piece<T, VE>(v);
+                }
             }
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int j = j0 + u * kThreads;
-                if (j >= nvec) break;
-                const int64_t i = (int64_t)j * VE - row.mis;
-                float v[VE];
-                if (i >= 0 && i + VE <= n) {
-                    widen<T, VE>(v, raw[u]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        v[e] = i + e >= 0 && i + e < n ? Elem<T>::to_f32(src[i + e]) : -INFINITY;
+                if (j < nvec) {
+                    const uint4 w = clean(raw[u]);
+                    put_piece(row.pieces + 16 * j, w);
+                    take(w);
                 }
-#pragma unroll
-                for (int e = 0; e < VE; ++e) v[e] = canonical<T>(v[e]);
-                store_piece<T, VE>(buf + (int64_t)j * VE, v);
-                take(v);
             }
         }
     } else {
-        row.buf = src;
         for (int64_t i0 = (int64_t)threadIdx.x * VE; i0 < n; i0 += (int64_t)kThreads * VE) {
-            float v[VE];
+            float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) v[e] = i0 + e < n ? logit(src[i0 + e]) : -INFINITY;
-            take(v);
+            for (int e = 0; e < VE; ++e)
+                if (i0 + e < n) top = fmaxf(top, logit(src[i0 + e]));
+            if (top > my_max) {
+                my_z *= e_below(my_max, top);
+                my_max = top;
+            }
+            if (top > -INFINITY)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (i0 + e < n) my_z += e_below(logit(src[i0 + e]), my_max);
         }
     }
     // the row's maximum and mass: warps, then warps of the CTA, then CTAs, each
@@ -497,31 +825,41 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, co
         join(om, oz);
     }
     if (threadIdx.x % 32 == 0) {
-        sh.redf[threadIdx.x / 32] = mx;
-        sh.redz[threadIdx.x / 32] = z;
+        sh.putf(kRed + threadIdx.x / 32, mx);
+        sh.putf(kRed2 + threadIdx.x / 32, z);
     }
-    if (threadIdx.x == 0) sh.race = 0.f;
+    if (threadIdx.x == 0) {
+        sh.putf(kRace, 0.f);
+        sh.put(kListN, 0);
+    }
     __syncthreads();
-    mx = sh.redf[0];
-    z = sh.redz[0];
-    for (int i = 1; i < kWarps; ++i) join(sh.redf[i], sh.redz[i]);
+    mx = sh.getf(kRed);
+    z = sh.getf(kRed2);
+    for (int i = 1; i < kWarps; ++i) join(sh.getf(kRed + i), sh.getf(kRed2 + i));
     if (cs > 1) {
         if (threadIdx.x == 0) {
-            sh.fslot[0] = mx;
-            sh.fslot[1] = z;
+            sh.putf(kPartMax, mx);
+            sh.putf(kPartZ, z);
         }
-        cluster_sync(cs);
-        mx = *remote(&sh.fslot[0], 0, cs);
-        z = *remote(&sh.fslot[1], 0, cs);
-        for (int q = 1; q < cs; ++q) join(*remote(&sh.fslot[0], q, cs), *remote(&sh.fslot[1], q, cs));
+        sh.sync();
+        mx = sh.getf(kPartMax, 0);
+        z = sh.getf(kPartZ, 0);
+        for (int q = 1; q < cs; ++q) join(sh.getf(kPartMax, q), sh.getf(kPartZ, q));
     }
 
+    auto finish = [&](uint32_t token) {
+        a.token[r] = (int32_t)token;
+        if (a.logprob) {
+            const float l = logit(static_cast<const T *>(a.logits)[r * a.logits_st + token]);
+            a.logprob[r] = (l - mx) / temp - logf(z);
+        }
+    };
     if (mx == -INFINITY) {  // nothing is left in this row
         if (rank == 0 && threadIdx.x == 0) {
             a.token[r] = -1;
             if (a.logprob) a.logprob[r] = -INFINITY;
         }
-        cluster_sync(cs);
+        sh.sync();
         return;
     }
     auto fast_e = [&](float l) { return e_below(l, mx); };
@@ -531,141 +869,165 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, co
         if (fabsf(e - min_p) <= 1e-4f * min_p) return exact_e(l) >= min_p;
         return e >= min_p;
     };
-    Cut cut;
-    if (use_k) {
-        if (top_k <= kThreads / 2) {
-            // the k-th largest of the threads' maxima: at least k tokens of
-            // this slice reach it, so it keeps all that can be among the first
-            // k, and not many more
-            const uint32_t mine = order_bits(my_max);
-            uint32_t floor_ = 0;
-#pragma unroll 1
-            for (int bit = 31; bit >= (sizeof(T) == 2 ? 13 : 0); --bit) {
-                const uint32_t t = floor_ | (1u << bit);
-                if (__syncthreads_count(mine >= t) >= top_k) floor_ = t;
+    // the race: a key is worked out in full only if it may be the best
+    float best = -1.f;
+    uint32_t best_i = 0xffffffffu;
+    auto run = [&](float l, uint32_t idx, float nz) {
+        const float ahead = fmaxf(best, sh.getf(kRace));
+        if (!(fast_e(l) < 0.9999f * ahead * nz)) {
+            const float key = exact_e(l) / fmaxf(nz, FLT_MIN);
+            if (l > -INFINITY && (key > best || (key == best && idx < best_i))) {
+                best = key;
+                best_i = idx;
+                if (key > ahead) sh.max_only(kRace, __float_as_uint(key));
             }
-            narrow<false, ROUNDS>(row, sh, cs, rank, cut, (uint32_t)top_k, 0.0, mx, 0.f,
-                                  [&](float l, uint32_t) { return order_bits(l) >= floor_; }, fast_e);
-        } else {
-            // bins from the largest logit to past the least of the threads' maxima
-            float least = my_max;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-            __syncthreads();
-            if (threadIdx.x % 32 == 0) sh.redf[threadIdx.x / 32] = least;
-            __syncthreads();
-            for (int i = 0; i < kWarps; ++i) least = fminf(least, sh.redf[i]);
-            if (cs > 1) {
-                if (threadIdx.x == 0) sh.fslot[3] = least;
-                cluster_sync(cs);
-                for (int q = 0; q < cs; ++q) least = fminf(least, *remote(&sh.fslot[3], q, cs));
-            }
-            const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
-            narrow<false, ROUNDS>(row, sh, cs, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kBins / range, 1e30f),
-                                  [&](float, uint32_t) { return true; }, fast_e);
         }
+    };
+    // this CTA's winner, as (key, ~index), in every thread
+    auto winner = [&]() {
+        unsigned long long w = best < 0.f ? 0ull : join64(0xffffffffu - best_i, __float_as_uint(best));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const unsigned long long p = __shfl_xor_sync(0xffffffffu, w, o);
+            if (p > w) w = p;
+        }
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) {
+            sh.put(kRed + threadIdx.x / 32, (uint32_t)w);
+            sh.put(kRed2 + threadIdx.x / 32, (uint32_t)(w >> 32));
+        }
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) {
+            const unsigned long long p = join64(sh.get(kRed + i), sh.get(kRed2 + i));
+            if (p > w) w = p;
+        }
+        return w;
+    };
+
+    Cut cut = no_cut();
+    if (use_k && top_k <= kMaxK) {
+        // at least k tokens of a slice reach the k-th largest of its threads'
+        // maxima, so it lets all pass that can be among the first k
+        const uint32_t mine = order_bits(my_max);
+        uint32_t floor_ = 0;
+#pragma unroll 1
+        for (int bit = 31; bit >= (sizeof(T) == 2 ? 13 : 0); --bit) {
+            const uint32_t t = floor_ | (1u << bit);
+            if (__syncthreads_count(mine >= t) >= top_k) floor_ = t;
+        }
+        const float low = floor_ > order_bits(-FLT_MAX) ? from_order_bits(floor_) : -FLT_MAX;
+        row.each(low, [&](float l, uint32_t idx) { enlist(sh, l, idx); });
+        sh.sync();
+        const int total = listed(sh);
+        if (total >= 0) {
+            if (rank == 0) {
+                sort_lists(sh, total);
+                int left = min(total, (int)top_k);
+                if (use_p) {
+                    double zk, all;
+                    mass_prefix(sh, left, 0.0, 0.0, fast_e, &zk);
+                    left = max(1, mass_prefix(sh, left, 0.0, (double)top_p * zk, fast_e, &all));
+                }
+                if ((int)threadIdx.x < left) {
+                    const float l = from_order_bits(sh.get(kSortKey + threadIdx.x));
+                    const uint32_t idx = sh.get(kSortIdx + threadIdx.x);
+                    if (!use_m || threadIdx.x == 0 || over_min(l)) run(l, idx, noise_at(noise + idx));
+                }
+                const unsigned long long w = winner();
+                if (threadIdx.x == 0) finish(0xffffffffu - (uint32_t)w);
+            }
+            sh.sync();  // no CTA leaves while another reads its list
+            return;
+        }
+        cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
+                              [](float, uint32_t) { return true; }, fast_e);
+    } else if (use_k) {
+        // bins from the largest logit to past the least of the threads' maxima
+        float least = my_max;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) sh.putf(kRed + threadIdx.x / 32, least);
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) least = fminf(least, sh.getf(kRed + i));
+        if (cs > 1) {
+            if (threadIdx.x == 0) sh.putf(kPartLeast, least);
+            sh.sync();
+            for (int q = 0; q < cs; ++q) least = fminf(least, sh.getf(kPartLeast, q));
+        }
+        const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
+        if (!cut_by_list<false>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
+                                -FLT_MAX, [](float, uint32_t) { return true; }, fast_e))
+            cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
+                                  [](float, uint32_t) { return true; }, fast_e);
     }
     if (use_p) {
         float zk = z;
         if (use_k) {
             zk = 0.f;
-            row.each([&](float l, uint32_t idx) {
-                if (cut.keeps(order_bits(l), idx)) zk += fast_e(l);
+            row.each(cut.l, [&](float l, uint32_t idx) {
+                if (cut.keeps(l, idx)) zk += fast_e(l);
             });
             zk = block_sum(zk, sh);
             if (cs > 1) {
-                if (threadIdx.x == 0) sh.fslot[2] = zk;
-                cluster_sync(cs);
+                if (threadIdx.x == 0) sh.putf(kPartSum, zk);
+                sh.sync();
                 zk = 0.f;
-                for (int q = 0; q < cs; ++q) zk += *remote(&sh.fslot[2], q, cs);
+                for (int q = 0; q < cs; ++q) zk += sh.getf(kPartSum, q);
             }
         }
         // tokens of less than this e lie past the cut whatever their order: all
         // of them together hold less than 1 - top_p of the mass
         const float least = 0.5f * (1.f - top_p) * zk / (float)a.V;
-        const float range = fmaxf(-logf(least), 1.f) * temp;   // of logits
-        const float lowest = mx - 1.0001f * range;
+        const float range = fmaxf(-logf(least), 1.f);
+        const float low = fmaxf(mx - 1.0001f * range * temp, cut.l);
         const Cut k_cut = cut;
-        narrow<true, ROUNDS>(row, sh, cs, rank, cut, 0, (double)top_p * zk * 0x1p40, mx,
-                             fminf(kBins / range, 1e30f),
-                             [&](float l, uint32_t idx) { return l >= lowest && k_cut.keeps(order_bits(l), idx); },
-                             fast_e);
+        auto in = [&](float l, uint32_t idx) { return k_cut.keeps(l, idx); };
+        const float scale = kCountBins / (range * temp);
+        if (!(scale < 1e30f) ||
+            !cut_by_list<true>(row, sh, rank, cut, 0, (double)top_p * zk, mx, scale, range / kCountBins, low, in,
+                               fast_e))
+            cut = narrow<true, ROUNDS>(row, sh, rank, cut, 0, (double)top_p * zk * 0x1p40, low, in, fast_e);
     }
 
-    // the race
-    float best = -1.f;
-    uint32_t best_i = 0xffffffffu;
-    const bool all = !use_k && !use_p && !use_m && !only_first;
-    auto run = [&](float l, uint32_t idx, float nz) {
-        nz = fmaxf(nz, FLT_MIN);
-        const float rough = __fdividef(fast_e(l), nz);
-        const float floor_ = fmaxf(best, *(volatile float *)&sh.race);
-        if (rough >= 0.9999f * floor_ || nz > 0x1p120f) {
-            const float key = exact_e(l) / nz;
-            if (key > best || (key == best && idx < best_i)) {
-                best = key;
-                best_i = idx;
-                if (key > floor_) atomicMax(reinterpret_cast<int *>(&sh.race), __float_as_int(key));
-            }
-        }
-    };
     if (only_first) {
-        row.each([&](float l, uint32_t idx) {
-            if (l == mx && idx < best_i) {
-                best = 1.f;
-                best_i = idx;
-            }
+        row.each(mx, [&](float, uint32_t idx) {
+            best = 1.f;
+            if (idx < best_i) best_i = idx;
         });
-    } else if (all) {
-        // four tokens per thread in flight, neighbouring threads on
-        // neighbouring tokens
+    } else if (!use_k && !use_p && !use_m) {
+        // neighbouring threads on neighbouring tokens, four of each in flight
         int64_t i = threadIdx.x;
         for (; i + 3 * kThreads < n; i += 4 * kThreads) {
             float nz[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) nz[u] = noise[base + i + u * kThreads];
+            for (int u = 0; u < 4; ++u) nz[u] = noise_at(noise + base + i + u * kThreads);
 #pragma unroll
             for (int u = 0; u < 4; ++u) run(row.at(i + u * kThreads), (uint32_t)(base + i + u * kThreads), nz[u]);
         }
-        for (; i < n; i += kThreads) run(row.at(i), (uint32_t)(base + i), noise[base + i]);
+        for (; i < n; i += kThreads) run(row.at(i), (uint32_t)(base + i), noise_at(noise + base + i));
     } else {
-        row.each([&](float l, uint32_t idx) {
-            // (a masked token cannot win, and a piece's places around the slice
-            // hold -inf: no noise is read for either)
-            if (l == -INFINITY || !cut.keeps(order_bits(l), idx)) return;
-            if (use_m && l != mx && !over_min(l)) return;
-            run(l, idx, noise[idx]);
+        const float low = use_m ? fmaxf(cut.l, mx + 1.0001f * logf(0.999f * min_p) * temp) : cut.l;
+        row.each(low, [&](float l, uint32_t idx) {
+            if (!cut.keeps(l, idx) || (use_m && l != mx && !over_min(l))) return;
+            run(l, idx, noise_at(noise + idx));
         });
     }
-    unsigned long long pack =
-        best < 0.f ? 0ull : ((unsigned long long)__float_as_uint(best) << 32) | (0xffffffffu - best_i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long p = __shfl_xor_sync(0xffffffffu, pack, o);
-        if (p > pack) pack = p;
-    }
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.redm[threadIdx.x / 32] = pack;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps; ++i)
-            if (sh.redm[i] > pack) pack = sh.redm[i];
-        sh.best = pack;
-    }
-    cluster_sync(cs);
-    if (rank == 0 && threadIdx.x == 0) {
-        for (int q = 0; q < cs; ++q) {
-            const unsigned long long p = *remote(&sh.best, q, cs);
-            if (p > pack) pack = p;
+    unsigned long long w = winner();
+    if (cs > 1) {
+        if (threadIdx.x == 0) {
+            sh.put(kBestIdx, (uint32_t)w);
+            sh.put(kBestKey, (uint32_t)(w >> 32));
         }
-        const uint32_t token = 0xffffffffu - (uint32_t)pack;
-        a.token[r] = (int32_t)token;
-        if (a.logprob) {
-            const float l = logit(static_cast<const T *>(a.logits)[r * a.logits_st + token]);
-            a.logprob[r] = (l - mx) / temp - logf(z);
-        }
+        sh.sync();
+        if (rank == 0 && threadIdx.x == 0)
+            for (int q = 0; q < cs; ++q) {
+                const unsigned long long p = join64(sh.get(kBestIdx, q), sh.get(kBestKey, q));
+                if (p > w) w = p;
+            }
     }
-    cluster_sync(cs);  // no CTA leaves while another reads its shared memory
+    if (rank == 0 && threadIdx.x == 0) finish(0xffffffffu - (uint32_t)w);
+    sh.sync();  // no CTA leaves while another reads its shared memory
 }
 
 constexpr size_t kMostShared = 200 * 1024;
@@ -699,7 +1061,7 @@ cudaError_t launch_t(const SampleArgs &a, int sm_count, cudaStream_t s) {
     constexpr int VE = 16 / sizeof(T);
     const int64_t sms = sm_count > 0 ? sm_count : 152;
     auto slice_of = [&](int cs) { return ((a.V + cs - 1) / cs + VE - 1) / VE * VE; };
-    auto bytes_of = [&](int cs) { return align16(sizeof(SampleShared)) + (size_t)(slice_of(cs) + VE) * sizeof(T); };
+    auto bytes_of = [&](int cs) { return kSharedBytes + (size_t)(slice_of(cs) + VE) * sizeof(T); };
     // a row over as few CTAs as leave room for two of them on an SM, so that
     // one loads while another computes; over more while SMs would stay idle
     int cs = 1;
@@ -707,7 +1069,7 @@ cudaError_t launch_t(const SampleArgs &a, int sm_count, cudaStream_t s) {
     while (cs < kMaxCluster && a.R * cs * 2 <= sms && slice_of(cs) > 4096) cs *= 2;
     if (a.R * cs > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (bytes_of(cs) > kMostShared)
-        return launch_cs<T, false>(a, cs, slice_of(cs), align16(sizeof(SampleShared)), s);
+        return launch_cs<T, false>(a, cs, slice_of(cs), kSharedBytes, s);
     return launch_cs<T, true>(a, cs, slice_of(cs), bytes_of(cs), s);
 }
 
