@@ -63,12 +63,13 @@ __device__ __forceinline__ Cut no_cut() { return Cut{-FLT_MAX, 0xffffffffu}; }
 
 // Shared memory before the row's slice, in 32-bit words, each read and written
 // by itself: word offsets.  A histogram of masses holds tokens, and mass in
-// two words; over the same memory lie a histogram of counts alone, and the
-// list that is sorted (ordered bits, then indexes).
+// two words; over the same memory lie a histogram of counts alone and, behind
+// it, this CTA's list of tokens near a cut (ordered bits, then indexes).  The
+// first CTA of a cluster has the lists of all in its sort memory.
 constexpr uint32_t kCount = 0, kLo = kBins, kHi = 2 * kBins;
-constexpr uint32_t kSortKey = 0, kSortIdx = kSort;
-constexpr uint32_t kListKey = 3 * kBins, kListIdx = kListKey + kList;   // tokens near a cut, of this CTA
-constexpr uint32_t kRed = kListIdx + kList;                             // one word per warp, three times
+constexpr uint32_t kListKey = kHi, kListIdx = kListKey + kList;
+constexpr uint32_t kSortKey = 3 * kBins, kSortIdx = kSortKey + kSort;
+constexpr uint32_t kRed = kSortIdx + kSort;                             // one word per warp, three times
 constexpr uint32_t kRed2 = kRed + kWarps, kRed3 = kRed2 + kWarps;
 constexpr uint32_t kWords = kRed3 + kWarps;                             // single words
 constexpr uint32_t kPartMax = kWords, kPartZ = kWords + 1, kPartLeast = kWords + 2, kPartSum = kWords + 3,
@@ -76,9 +77,9 @@ constexpr uint32_t kPartMax = kWords, kPartZ = kWords + 1, kPartLeast = kWords +
                    kBestIdx = kWords + 8, kFoundBin = kWords + 9, kFoundLast = kWords + 10, kFoundCount = kWords + 11,
                    kFoundN = kWords + 12, kFoundMassLo = kWords + 13, kFoundMassHi = kWords + 14,
                    kFoundWLo = kWords + 15, kFoundWHi = kWords + 16, kLimit = kWords + 17, kCutL = kWords + 18,
-                   kCutEnd = kWords + 19, kRace = kWords + 20;
+                   kCutEnd = kWords + 19, kRace = kWords + 20, kSortN = kWords + 21, kSortAt = kWords + 22;
 constexpr uint32_t kSharedBytes = (kWords + 24) * 4;
-static_assert(kCountBins <= 3 * kBins && 2 * kSort <= 3 * kBins && kSharedBytes % 16 == 0, "layout");
+static_assert(kCountBins <= kHi && 2 * kList <= kBins && kSharedBytes % 16 == 0, "layout");
 
 // Word accesses at a CTA's own shared memory, and at that of another CTA of
 // the cluster (`cs` CTAs; a CTA alone takes its own).
@@ -122,7 +123,26 @@ struct Shared {
         if (cs == 1) return put(w, v);
         asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(mapped(w, rank)), "r"(v) : "memory");
     }
-    __device__ __forceinline__ float getf(uint32_t w, int rank) const { return __uint_as_float(get(w, rank)); }
+    // atomic on another CTA's word; returns what was there
+    __device__ __forceinline__ uint32_t add(uint32_t w, int rank, uint32_t v) const {
+        if (cs == 1) return add(w, v);
+        uint32_t old;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;\n" : "=r"(old) : "r"(mapped(w, rank)), "r"(v) : "memory");
+        return old;
+    }
+    // the word of every CTA, lane q of a warp taking that of CTA q (the others
+    // `none`): one trip for all of them
+    __device__ __forceinline__ uint32_t each_cta(uint32_t w, uint32_t none) const {
+        const int lane = threadIdx.x % 32;
+        return lane < cs ? get(w, lane) : none;
+    }
+    // sum of a float of every CTA, in the order of the CTAs
+    __device__ __forceinline__ float sum_ctas(uint32_t w) const {
+        const float v = __uint_as_float(each_cta(w, 0));
+        float s = __shfl_sync(0xffffffffu, v, 0);
+        for (int q = 1; q < cs; ++q) s += __shfl_sync(0xffffffffu, v, q);
+        return s;
+    }
     // every CTA of the cluster in step, and its writes visible to the others
     __device__ __forceinline__ void sync() const {
         if (cs > 1) cg::this_cluster().sync();
@@ -501,30 +521,29 @@ __device__ __forceinline__ void enlist(const Shared &sh, float l, uint32_t idx) 
     }
 }
 
-// After the lists are full and the cluster is in step: tokens in all lists, or
-// -1 if one of them or their sum does not fit.
-__device__ __forceinline__ int listed(const Shared &sh) {
-    int total = 0;
-    bool fits = true;
-    for (int q = 0; q < sh.cs; ++q) {
-        const uint32_t c = sh.get(kListN, q);
-        fits = fits && c <= kList;
-        total += (int)(c <= kList ? c : 0);
+// Hands this CTA's list to the first CTA, in no order (the sort makes one).
+// All CTAs' lists are there once the cluster is in step; then kSortN of the
+// first CTA is their length, or above kSort if they do not fit.
+__device__ __forceinline__ void send_list(const Shared &sh) {
+    __syncthreads();
+    const uint32_t c = sh.get(kListN);
+    if (threadIdx.x == 0) sh.put(kSortAt, sh.add(kSortN, 0, c <= kList ? c : kSort + 1));
+    __syncthreads();
+    const uint32_t at = sh.get(kSortAt);
+    if (c > kList || at > kSort || at + c > kSort) return;
+    for (uint32_t i = threadIdx.x; i < c; i += kThreads) {
+        sh.put(kSortKey + at + i, 0, sh.get(kListKey + i));
+        sh.put(kSortIdx + at + i, 0, sh.get(kListIdx + i));
     }
-    return fits && total <= kSort ? total : -1;
+}
+// Their length in every CTA, or -1.
+__device__ __forceinline__ int listed(const Shared &sh) {
+    const uint32_t n = sh.get(kSortN, 0);
+    return n <= kSort ? (int)n : -1;
 }
 
-// The lists of all CTAs sorted, the first token of the order first.
+// Sorts the lists in the first CTA, the first token of the order first.
 __device__ __forceinline__ void sort_lists(const Shared &sh, int total) {
-    int at = 0;
-    for (int q = 0; q < sh.cs; ++q) {
-        const int c = (int)sh.get(kListN, q);
-        for (int i = threadIdx.x; i < c; i += kThreads) {
-            sh.put(kSortKey + at + i, sh.get(kListKey + i, q));
-            sh.put(kSortIdx + at + i, sh.get(kListIdx + i, q));
-        }
-        at += c;
-    }
     int n = 32;
     while (n < total) n *= 2;
     for (int i = total + threadIdx.x; i < n; i += kThreads) {  // after every token
@@ -550,36 +569,40 @@ __device__ __forceinline__ void sort_lists(const Shared &sh, int total) {
     __syncthreads();
 }
 
+// e, a mass, in units of 2^-40 of the largest token's.
+__device__ __forceinline__ unsigned long long units(float e) { return __float2ull_rn(e * 0x1p40f); }
+
 // Of the first n sorted tokens, how many have less than `target` of mass
 // before them, with `above` before the first; *total is the mass of the n.
+// In whole units, so in no order.
 template <typename Mass>
-__device__ __forceinline__ int mass_prefix(const Shared &sh, int n, double above, double target, Mass &&mass,
-                                           double *total) {
+__device__ __forceinline__ int mass_prefix(const Shared &sh, int n, unsigned long long above,
+                                           unsigned long long target, Mass &&mass, unsigned long long *total) {
     constexpr int PER = kSort / kThreads;
-    double own[PER], sum = 0.0;
+    unsigned long long own[PER], sum = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int i = threadIdx.x * PER + j;
-        own[j] = i < n ? (double)mass(from_order_bits(sh.get(kSortKey + i))) : 0.0;
+        own[j] = i < n ? units(mass(from_order_bits(sh.get(kSortKey + i)))) : 0;
         sum += own[j];
     }
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    double in = sum;
+    unsigned long long in = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, in, o);
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, in, o);
         if (lane >= o) in += v;
     }
     __syncthreads();
     if (lane == 31) {
-        const unsigned long long w = (unsigned long long)__double_as_longlong(in);
-        sh.put(kRed + warp, (uint32_t)w);
-        sh.put(kRed2 + warp, (uint32_t)(w >> 32));
+        sh.put(kRed + warp, (uint32_t)in);
+        sh.put(kRed2 + warp, (uint32_t)(in >> 32));
     }
     __syncthreads();
-    double before = above, all = 0.0;
+    unsigned long long before = above, all = 0;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) {
-        const double v = __longlong_as_double((long long)join64(sh.get(kRed + i), sh.get(kRed2 + i)));
+        const unsigned long long v = join64(sh.get(kRed + i), sh.get(kRed2 + i));
         if (i < warp) before += v;
         all += v;
     }
@@ -591,12 +614,12 @@ __device__ __forceinline__ int mass_prefix(const Shared &sh, int n, double above
         if ((int)threadIdx.x * PER + j < n && before < target) ++count;
         before += own[j];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    count = __reduce_add_sync(0xffffffffu, count);
     __syncthreads();
     if (lane == 0) sh.put(kRed + warp, (uint32_t)count);
     __syncthreads();
     count = 0;
+#pragma unroll
     for (int i = 0; i < kWarps; ++i) count += (int)sh.get(kRed + i);
     return count;
 }
@@ -618,6 +641,7 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         sh.put(kFoundLast, kCountBins - 1);
         sh.put(kFoundCount, 0);
         sh.put(kListN, 0);
+        sh.put(kSortN, 0);
     }
     __syncthreads();
     row.each(low, [&](float l, uint32_t idx) {
@@ -680,18 +704,16 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         above = block_sum(above, sh);
         if (threadIdx.x == 0) sh.putf(kPartAbove, above);
     }
+    send_list(sh);
     sh.sync();
     const int total = listed(sh);
     if (total < 0) return false;
     if (rank == 0) {
-        double mass_above = 0.0;
-        if (MASS)
-            for (int q = 0; q < sh.cs; ++q) mass_above += (double)sh.getf(kPartAbove, q);
         sort_lists(sh, total);
         int keep;
         if (MASS) {
-            double all;
-            keep = mass_prefix(sh, total, mass_above, target, mass, &all);
+            unsigned long long all;
+            keep = mass_prefix(sh, total, units(sh.sum_ctas(kPartAbove)), units((float)target), mass, &all);
         } else {
             keep = min(total, (int)(k - above_count));
         }
@@ -831,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (threadIdx.x == 0) {
         sh.putf(kRace, 0.f);
         sh.put(kListN, 0);
+        sh.put(kSortN, 0);
     }
     __syncthreads();
     mx = sh.getf(kRed);
@@ -842,9 +865,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             sh.putf(kPartZ, z);
         }
         sh.sync();
-        mx = sh.getf(kPartMax, 0);
-        z = sh.getf(kPartZ, 0);
-        for (int q = 1; q < cs; ++q) join(sh.getf(kPartMax, q), sh.getf(kPartZ, q));
+        const float om = __uint_as_float(sh.each_cta(kPartMax, __float_as_uint(-INFINITY)));
+        const float oz = __uint_as_float(sh.each_cta(kPartZ, 0));
+        mx = __shfl_sync(0xffffffffu, om, 0);
+        z = __shfl_sync(0xffffffffu, oz, 0);
+        for (int q = 1; q < cs; ++q) join(__shfl_sync(0xffffffffu, om, q), __shfl_sync(0xffffffffu, oz, q));
     }
 
     auto finish = [&](uint32_t token) {
@@ -917,6 +942,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         const float low = floor_ > order_bits(-FLT_MAX) ? from_order_bits(floor_) : -FLT_MAX;
         row.each(low, [&](float l, uint32_t idx) { enlist(sh, l, idx); });
+        send_list(sh);
         sh.sync();
         const int total = listed(sh);
         if (total >= 0) {
@@ -924,9 +950,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 sort_lists(sh, total);
                 int left = min(total, (int)top_k);
                 if (use_p) {
-                    double zk, all;
-                    mass_prefix(sh, left, 0.0, 0.0, fast_e, &zk);
-                    left = max(1, mass_prefix(sh, left, 0.0, (double)top_p * zk, fast_e, &all));
+                    unsigned long long zk, all;
+                    mass_prefix(sh, left, 0, 0, fast_e, &zk);
+                    const unsigned long long target = __double2ull_ru((double)top_p * (double)zk);
+                    left = max(1, mass_prefix(sh, left, 0, target, fast_e, &all));
                 }
                 if ((int)threadIdx.x < left) {
                     const float l = from_order_bits(sh.get(kSortKey + threadIdx.x));
@@ -953,7 +980,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         if (cs > 1) {
             if (threadIdx.x == 0) sh.putf(kPartLeast, least);
             sh.sync();
-            for (int q = 0; q < cs; ++q) least = fminf(least, sh.getf(kPartLeast, q));
+            least = __uint_as_float(sh.each_cta(kPartLeast, __float_as_uint(INFINITY)));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+            least = __shfl_sync(0xffffffffu, least, 0);
         }
         const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
         if (!cut_by_list<false>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
@@ -972,8 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (cs > 1) {
                 if (threadIdx.x == 0) sh.putf(kPartSum, zk);
                 sh.sync();
-                zk = 0.f;
-                for (int q = 0; q < cs; ++q) zk += sh.getf(kPartSum, q);
+                zk = sh.sum_ctas(kPartSum);
             }
         }
         // tokens of less than this e lie past the cut whatever their order: all
@@ -1020,11 +1049,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             sh.put(kBestKey, (uint32_t)(w >> 32));
         }
         sh.sync();
-        if (rank == 0 && threadIdx.x == 0)
-            for (int q = 0; q < cs; ++q) {
-                const unsigned long long p = join64(sh.get(kBestIdx, q), sh.get(kBestKey, q));
+        if (rank == 0 && threadIdx.x < 32) {
+            w = join64(sh.each_cta(kBestIdx, 0), sh.each_cta(kBestKey, 0));
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                const unsigned long long p = __shfl_xor_sync(0xffffffffu, w, o);
                 if (p > w) w = p;
             }
+        }
     }
     if (rank == 0 && threadIdx.x == 0) finish(0xffffffffu - (uint32_t)w);
     sh.sync();  // no CTA leaves while another reads its shared memory
