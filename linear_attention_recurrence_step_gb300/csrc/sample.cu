@@ -284,6 +284,21 @@ template <typename T, bool CACHED> struct Row {
             }
         }
     }
+    // f(logits of a piece, index of its first) for every piece of a CACHED
+    // slice that has a logit of at least `low`; places beside the slice hold
+    // -inf
+    template <typename F> __device__ __forceinline__ void each_piece(float low, F &&f) const {
+        constexpr int VE = 16 / sizeof(T);
+        const int nvec = (int)((mis + n + VE - 1) / VE);
+        for (int j = threadIdx.x; j < nvec; j += kThreads) {
+            RawPiece<T, VE> raw;
+            raw.w = piece_at(pieces + 16 * j);
+            if (piece_max<T>(raw.w) < low) continue;
+            float2 v[VE / 2];
+            widen2<T, VE>(v, raw);
+            f(v, base + (uint32_t)(j * VE - mis));
+        }
+    }
     __device__ __forceinline__ float at(int64_t i) const {
         return CACHED ? element_at<T>(pieces + (uint32_t)((mis + i) * sizeof(T))) : logit(src[i]);
     }
@@ -625,15 +640,23 @@ __device__ __forceinline__ int mass_prefix(const Shared &sh, int n, unsigned lon
 }
 
 // The cut at which the running count of tokens reaches `k`, or the running
-// mass `target`, by a histogram of counts over bins of width 1/scale below
-// `mx` and a sorted list of the bin (of the bracket) that holds it; `width` is
-// a bin's in units of log(e).  False: the list does not fit.
-template <bool MASS, typename RowT, typename In, typename Mass>
+// mass `target`, by a histogram of counts over bins of width 1/scale about the
+// multiples of that below `mx`, and a sorted list of the bin (of the bracket)
+// that holds it; `width` is a bin's in units of log(e).  ALL: every token of
+// logit `low` or more takes part, and the bins cover all of those; else those
+// of which `in(l, idx)` holds, the last bin taking what lies below.  False:
+// the list does not fit.
+template <bool MASS, bool ALL, bool CACHED, typename RowT, typename In, typename Mass>
 __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, int rank, Cut &cut, uint32_t k,
                                             double target, float mx, float scale, float width, float low, In &&in,
                                             Mass &&mass) {
-    // 0 is the top bin
-    auto bin_of = [&](float l) { return max(0, min(kCountBins - 1, __float2int_rz((mx - l) * scale))); };
+    constexpr bool PIECES = ALL && CACHED;
+    // 0 is the top bin: the distance from mx in bins, rounded by the sum with
+    // 2^23, whose low bits it then is (above all bins for -inf)
+    constexpr float kMagic = 0x1p23f;
+    auto bin_of = [&](float l) { return __float_as_uint(fmaf(mx - l, scale, kMagic)) - 0x4b000000u; };
+    auto clamped = [&](float l) { return min((uint32_t)kCountBins - 1, bin_of(l)); };
+    const float2 nmx = make_float2(-mx, -mx);
     __syncthreads();
     for (int i = threadIdx.x; i < kCountBins; i += kThreads) sh.put(kCount + i, 0);
     if (threadIdx.x == 0) {
@@ -644,16 +667,29 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         sh.put(kSortN, 0);
     }
     __syncthreads();
-    row.each(low, [&](float l, uint32_t idx) {
-        if (in(l, idx)) sh.add_only(kCount + bin_of(l), 1u);
-    });
+    if constexpr (PIECES) {
+        row.each_piece(low, [&](const auto &v, uint32_t) {
+#pragma unroll
+            for (const float2 &w : v) {
+                const float2 d = __fadd2_rn(w, nmx);
+                const float2 m = ffma2(d, make_float2(-scale, -scale), make_float2(kMagic, kMagic));
+                const uint32_t bx = __float_as_uint(m.x) - 0x4b000000u, by = __float_as_uint(m.y) - 0x4b000000u;
+                if (bx < kCountBins) sh.add_only(kCount + bx, 1u);
+                if (by < kCountBins) sh.add_only(kCount + by, 1u);
+            }
+        });
+    } else {
+        row.each(low, [&](float l, uint32_t idx) {
+            if (in(l, idx)) sh.add_only(kCount + clamped(l), 1u);
+        });
+    }
     sh.sync();
     if (sh.cs > 1) {
         merge_bins(sh, kCount, kCountBins, rank);
         sh.sync();
     }
     // running sums over the bins: of tokens, or of an upper bound on their mass
-    // (a token's e is at most that of its bin's upper edge, and at least that
+    // (a token's e is at most that at its bin's upper edge, and at least that
     // times exp(-width): the true sum lies between the bound and that share)
     constexpr int PB = kCountBins / kThreads;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -662,7 +698,7 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     for (int j = 0; j < PB; ++j) {
         const int bin = threadIdx.x * PB + j;
         part[j] = (float)sh.get(kCount + bin);
-        if (MASS) part[j] *= ex2(-1.44269504088896341f * width * (float)bin);
+        if (MASS) part[j] *= ex2(-1.44269504088896341f * width * ((float)bin - 0.5f));
         sum += part[j];
     }
     float incl = sum;
@@ -691,15 +727,35 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         run = next;
     }
     __syncthreads();
-    const int b0 = (int)sh.get(kFoundBin), b1 = (int)sh.get(kFoundLast);
+    const uint32_t b0 = sh.get(kFoundBin), b1 = sh.get(kFoundLast);
     const uint32_t above_count = sh.get(kFoundCount);
     float above = 0.f;
-    row.each(low, [&](float l, uint32_t idx) {
-        const int bin = bin_of(l);
-        if (bin > b1 || !in(l, idx)) return;
-        if (bin >= b0) enlist(sh, l, idx);
-        else if (MASS) above += mass(l);
-    });
+    if constexpr (PIECES) {
+        row.each_piece(low, [&](const auto &v, uint32_t idx) {
+            bool some = false;  // of the piece is in the bracket
+#pragma unroll
+            for (const float2 &w : v) {
+                const uint32_t bx = bin_of(w.x), by = bin_of(w.y);
+                if (MASS) above += (bx < b0 ? mass(w.x) : 0.f) + (by < b0 ? mass(w.y) : 0.f);
+                some = some || bx - b0 <= b1 - b0 || by - b0 <= b1 - b0;
+            }
+            if (some) {
+#pragma unroll
+                for (const float2 &w : v) {
+                    if (bin_of(w.x) - b0 <= b1 - b0) enlist(sh, w.x, idx);
+                    if (bin_of(w.y) - b0 <= b1 - b0) enlist(sh, w.y, idx + 1);
+                    idx += 2;
+                }
+            }
+        });
+    } else {
+        row.each(low, [&](float l, uint32_t idx) {
+            const uint32_t bin = clamped(l);
+            if (bin > b1 || !in(l, idx)) return;
+            if (bin >= b0) enlist(sh, l, idx);
+            else if (MASS) above += mass(l);
+        });
+    }
     if (MASS) {
         above = block_sum(above, sh);
         if (threadIdx.x == 0) sh.putf(kPartAbove, above);
@@ -897,15 +953,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     // the race: a key is worked out in full only if it may be the best
     float best = -1.f;
     uint32_t best_i = 0xffffffffu;
+    auto behind = [&](float l, float nz, float ahead) { return fast_e(l) < ahead * nz; };
+    auto ahead_now = [&]() { return 0.9999f * fmaxf(best, sh.getf(kRace)); };
     auto run = [&](float l, uint32_t idx, float nz) {
-        const float ahead = fmaxf(best, sh.getf(kRace));
-        if (!(fast_e(l) < 0.9999f * ahead * nz)) {
-            const float key = exact_e(l) / fmaxf(nz, FLT_MIN);
-            if (l > -INFINITY && (key > best || (key == best && idx < best_i))) {
-                best = key;
-                best_i = idx;
-                if (key > ahead) sh.max_only(kRace, __float_as_uint(key));
-            }
+        const float key = exact_e(l) / fmaxf(nz, FLT_MIN);
+        if (l > -INFINITY && (key > best || (key == best && idx < best_i))) {
+            if (key > best) sh.max_only(kRace, __float_as_uint(key));
+            best = key;
+            best_i = idx;
         }
     };
     // this CTA's winner, as (key, ~index), in every thread
@@ -986,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             least = __shfl_sync(0xffffffffu, least, 0);
         }
         const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
-        if (!cut_by_list<false>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
+        if (!cut_by_list<false, false, CACHED>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
                                 -FLT_MAX, [](float, uint32_t) { return true; }, fast_e))
             cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
                                   [](float, uint32_t) { return true; }, fast_e);
@@ -1013,9 +1068,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const Cut k_cut = cut;
         auto in = [&](float l, uint32_t idx) { return k_cut.keeps(l, idx); };
         const float scale = kCountBins / (range * temp);
-        if (!(scale < 1e30f) ||
-            !cut_by_list<true>(row, sh, rank, cut, 0, (double)top_p * zk, mx, scale, range / kCountBins, low, in,
-                               fast_e))
+        bool done = false;
+        if (scale < 1e30f) {
+            const float width = range / kCountBins;
+            const double target = (double)top_p * zk;
+            done = use_k ? cut_by_list<true, false, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in, fast_e)
+                         : cut_by_list<true, true, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in,
+                                                           fast_e);
+        }
+        if (!done)
             cut = narrow<true, ROUNDS>(row, sh, rank, cut, 0, (double)top_p * zk * 0x1p40, low, in, fast_e);
     }
 
@@ -1025,22 +1086,53 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (idx < best_i) best_i = idx;
         });
     } else if (!use_k && !use_p && !use_m) {
-        // neighbouring threads on neighbouring tokens, four of each in flight
-        int64_t i = threadIdx.x;
-        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
-            float nz[4];
+        // neighbouring threads on neighbouring tokens, eight of each in flight
+        constexpr int U = 8;
+        for (int64_t i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+            float nz[U], l[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) nz[u] = noise_at(noise + base + i + u * kThreads);
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * kThreads < n) nz[u] = noise_at(noise + base + i0 + u * kThreads);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) run(row.at(i + u * kThreads), (uint32_t)(base + i + u * kThreads), nz[u]);
+            for (int u = 0; u < U; ++u) l[u] = i0 + u * kThreads < n ? row.at(i0 + u * kThreads) : -INFINITY;
+            const float ahead = ahead_now();
+            uint32_t may = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * kThreads < n && !behind(l[u], nz[u], ahead)) may |= 1u << u;
+            if (may)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (may >> u & 1) run(l[u], (uint32_t)(base + i0 + u * kThreads), nz[u]);
         }
-        for (; i < n; i += kThreads) run(row.at(i), (uint32_t)(base + i), noise_at(noise + base + i));
     } else {
         const float low = use_m ? fmaxf(cut.l, mx + 1.0001f * logf(0.999f * min_p) * temp) : cut.l;
-        row.each(low, [&](float l, uint32_t idx) {
-            if (!cut.keeps(l, idx) || (use_m && l != mx && !over_min(l))) return;
-            run(l, idx, noise_at(noise + idx));
-        });
+        auto left = [&](float l, uint32_t idx) { return cut.keeps(l, idx) && (!use_m || l == mx || over_min(l)); };
+        if constexpr (CACHED) {
+            row.each_piece(low, [&](const auto &v, uint32_t idx) {
+                // (a masked token is never left, nor is a place beside the slice:
+                // no noise is read for either)
+                float nz[VE];
+                uint32_t on = 0;
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (left(e % 2 ? v[e / 2].y : v[e / 2].x, idx + e)) {
+                        on |= 1u << e;
+                        nz[e] = noise_at(noise + (uint32_t)(idx + e));  // (idx may be below 0, mod 2^32)
+                    }
+                if (!on) return;
+                const float ahead = ahead_now();
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float l = e % 2 ? v[e / 2].y : v[e / 2].x;
+                    if ((on >> e & 1) && !behind(l, nz[e], ahead)) run(l, idx + e, nz[e]);
+                }
+            });
+        } else {
+            row.each(low, [&](float l, uint32_t idx) {
+                if (left(l, idx)) run(l, idx, noise_at(noise + idx));
+            });
+        }
     }
     unsigned long long w = winner();
     if (cs > 1) {
