@@ -254,53 +254,49 @@ template <> __device__ __forceinline__ float element_at<__half>(uint32_t shared_
 }
 
 template <typename T, bool CACHED> struct Row {
+    [[maybe_unused]] static constexpr int VE = 16 / sizeof(T);
     uint32_t pieces;     // CACHED: shared address of the slice's pieces (16-byte aligned)
     int mis;             // CACHED: elements before the slice's first in its first piece
     const T *src;        // the slice in memory
-    int64_t n;           // tokens in the slice
+    int n;               // tokens in the slice
     uint32_t base;       // index of the first
+    __device__ __forceinline__ int count() const { return (mis + n + VE - 1) / VE; }  // pieces
     // f(logit, index) for every token of the slice with a logit of at least
     // `low` (above -inf), thread by thread.  Pieces in shared memory hold
     // clean logits, and -inf around the slice; a piece without such a token
     // costs one comparison.
     template <typename F> __device__ __forceinline__ void each(float low, F &&f) const {
         if constexpr (CACHED) {
-            constexpr int VE = 16 / sizeof(T);
-            const int nvec = (int)((mis + n + VE - 1) / VE);
-            for (int j = threadIdx.x; j < nvec; j += kThreads) {
-                RawPiece<T, VE> raw;
-                raw.w = piece_at(pieces + 16 * j);
-                if (piece_max<T>(raw.w) < low) continue;
-                float v[VE];
-                widen<T, VE>(v, raw);
+            each_piece(low, [&](const float2 (&v)[VE / 2], int i0) {
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (v[e] >= low) f(v[e], base + (uint32_t)(j * VE + e - mis));
-            }
+                for (int e = 0; e < VE; ++e) {
+                    const float l = e % 2 ? v[e / 2].y : v[e / 2].x;
+                    if (l >= low) f(l, base + (uint32_t)(i0 + e));
+                }
+            });
         } else {
-            for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+            for (int i = threadIdx.x; i < n; i += kThreads) {
                 const float l = logit(src[i]);
                 if (l >= low) f(l, base + (uint32_t)i);
             }
         }
     }
-    // f(logits of a piece, index of its first) for every piece of a CACHED
-    // slice that has a logit of at least `low`; places beside the slice hold
-    // -inf
+    // f(logits of a piece, place of its first in the slice) for every piece of
+    // a CACHED slice that has a logit of at least `low`; the first piece's
+    // place may be below 0, and places outside the slice hold -inf
     template <typename F> __device__ __forceinline__ void each_piece(float low, F &&f) const {
-        constexpr int VE = 16 / sizeof(T);
-        const int nvec = (int)((mis + n + VE - 1) / VE);
-        for (int j = threadIdx.x; j < nvec; j += kThreads) {
+        const int end = count();
+        for (int j = threadIdx.x; j < end; j += kThreads) {
             RawPiece<T, VE> raw;
             raw.w = piece_at(pieces + 16 * j);
             if (piece_max<T>(raw.w) < low) continue;
             float2 v[VE / 2];
             widen2<T, VE>(v, raw);
-            f(v, base + (uint32_t)(j * VE - mis));
+            f(v, j * VE - mis);
         }
     }
-    __device__ __forceinline__ float at(int64_t i) const {
-        return CACHED ? element_at<T>(pieces + (uint32_t)((mis + i) * sizeof(T))) : logit(src[i]);
+    __device__ __forceinline__ float at(int i) const {
+        return CACHED ? element_at<T>(pieces + (uint32_t)(mis + i) * (uint32_t)sizeof(T)) : logit(src[i]);
     }
 };
 
@@ -491,11 +487,11 @@ __device__ __forceinline__ Cut narrow(const RowT &row, const Shared &sh, int ran
         // index of the want-th of them: the CTAs' slices are in index order,
         // and so are the warps' parts of a slice
         const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-        const int64_t per = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const int64_t i0 = warp * per, i1 = i0 + per < row.n ? i0 + per : row.n;
-        auto equal = [&](int64_t i) { return i < i1 && row.at(i) == l_eq && in(l_eq, row.base + (uint32_t)i); };
+        const int per = ((row.n + kWarps - 1) / kWarps + 31) / 32 * 32;
+        const int i0 = warp * per, i1 = i0 + per < row.n ? i0 + per : row.n;
+        auto equal = [&](int i) { return i < i1 && row.at(i) == l_eq && in(l_eq, row.base + (uint32_t)i); };
         uint32_t mine = 0;
-        for (int64_t i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i + lane)));
+        for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, equal(i + lane)));
         if (lane == 0) sh.put(kRed + warp, mine);
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -509,7 +505,7 @@ __device__ __forceinline__ Cut narrow(const RowT &row, const Shared &sh, int ran
         for (int i = 0; i < warp; ++i) before += sh.get(kRed + i);
         if (before < want && want <= before + mine) {
             uint32_t left = want - before;  // the left-th of this warp's
-            for (int64_t i = i0; i < i1; i += 32) {
+            for (int i = i0; i < i1; i += 32) {
                 const uint32_t m = __ballot_sync(0xffffffffu, equal(i + lane));
                 const uint32_t c = __popc(m);
                 if (left <= c) {
@@ -646,17 +642,19 @@ __device__ __forceinline__ int mass_prefix(const Shared &sh, int n, unsigned lon
 // logit `low` or more takes part, and the bins cover all of those; else those
 // of which `in(l, idx)` holds, the last bin taking what lies below.  False:
 // the list does not fit.
-template <bool MASS, bool ALL, bool CACHED, typename RowT, typename In, typename Mass>
+template <bool MASS, bool ALL, bool CACHED, typename RowT, typename In, typename Mass, typename Mass2>
 __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, int rank, Cut &cut, uint32_t k,
                                             double target, float mx, float scale, float width, float low, In &&in,
-                                            Mass &&mass) {
+                                            Mass &&mass, Mass2 &&mass2) {
     constexpr bool PIECES = ALL && CACHED;
     // 0 is the top bin: the distance from mx in bins, rounded by the sum with
     // 2^23, whose low bits it then is (above all bins for -inf)
     constexpr float kMagic = 0x1p23f;
     auto bin_of = [&](float l) { return __float_as_uint(fmaf(mx - l, scale, kMagic)) - 0x4b000000u; };
     auto clamped = [&](float l) { return min((uint32_t)kCountBins - 1, bin_of(l)); };
-    const float2 nmx = make_float2(-mx, -mx);
+    auto in_bins = [&](float2 w) {
+        return ffma2(__fadd2_rn(w, make_float2(-mx, -mx)), make_float2(-scale, -scale), make_float2(kMagic, kMagic));
+    };
     __syncthreads();
     for (int i = threadIdx.x; i < kCountBins; i += kThreads) sh.put(kCount + i, 0);
     if (threadIdx.x == 0) {
@@ -668,11 +666,10 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     }
     __syncthreads();
     if constexpr (PIECES) {
-        row.each_piece(low, [&](const auto &v, uint32_t) {
+        row.each_piece(low, [&](const auto &v, int) {
 #pragma unroll
             for (const float2 &w : v) {
-                const float2 d = __fadd2_rn(w, nmx);
-                const float2 m = ffma2(d, make_float2(-scale, -scale), make_float2(kMagic, kMagic));
+                const float2 m = in_bins(w);
                 const uint32_t bx = __float_as_uint(m.x) - 0x4b000000u, by = __float_as_uint(m.y) - 0x4b000000u;
                 if (bx < kCountBins) sh.add_only(kCount + bx, 1u);
                 if (by < kCountBins) sh.add_only(kCount + by, 1u);
@@ -731,23 +728,31 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     const uint32_t above_count = sh.get(kFoundCount);
     float above = 0.f;
     if constexpr (PIECES) {
-        row.each_piece(low, [&](const auto &v, uint32_t idx) {
+        const float f0 = kMagic + (float)b0, f1 = kMagic + (float)b1;
+        float2 sum2 = make_float2(0.f, 0.f);
+        row.each_piece(low, [&](const auto &v, int i0) {
             bool some = false;  // of the piece is in the bracket
 #pragma unroll
             for (const float2 &w : v) {
-                const uint32_t bx = bin_of(w.x), by = bin_of(w.y);
-                if (MASS) above += (bx < b0 ? mass(w.x) : 0.f) + (by < b0 ? mass(w.y) : 0.f);
-                some = some || bx - b0 <= b1 - b0 || by - b0 <= b1 - b0;
+                const float2 m = in_bins(w);
+                if (MASS) {
+                    const float2 e = mass2(w);
+                    sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? e.x : 0.f, m.y < f0 ? e.y : 0.f));
+                }
+                some = some || (m.x >= f0 && m.x <= f1) || (m.y >= f0 && m.y <= f1);
             }
             if (some) {
+                uint32_t idx = row.base + (uint32_t)i0;
 #pragma unroll
                 for (const float2 &w : v) {
-                    if (bin_of(w.x) - b0 <= b1 - b0) enlist(sh, w.x, idx);
-                    if (bin_of(w.y) - b0 <= b1 - b0) enlist(sh, w.y, idx + 1);
+                    const float2 m = in_bins(w);
+                    if (m.x >= f0 && m.x <= f1) enlist(sh, w.x, idx);
+                    if (m.y >= f0 && m.y <= f1) enlist(sh, w.y, idx + 1);
                     idx += 2;
                 }
             }
         });
+        above = sum2.x + sum2.y;
     } else {
         row.each(low, [&](float l, uint32_t idx) {
             const uint32_t bin = clamped(l);
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const int64_t r = blockIdx.x / cs;
     const int rank = blockIdx.x % cs;
     const int64_t base = rank * slice;
-    const int64_t n = a.V - base < slice ? (a.V > base ? a.V - base : 0) : slice;
+    const int n = (int)(a.V - base < slice ? (a.V > base ? a.V - base : 0) : slice);
     const T *src = static_cast<const T *>(a.logits) + r * a.logits_st + base;
     const float *noise = a.noise + r * a.noise_st;
 
@@ -846,35 +851,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     row.src = src;
     row.pieces = sh.base + kSharedBytes;
     if constexpr (CACHED) {
-        const int nvec = (int)((row.mis + n + VE - 1) / VE);
+        // the pieces that lie inside the slice, then those across its ends, with
+        // -inf beside it
+        const int first = row.mis > 0, end = (row.mis + n) / VE, all = row.count();
+        const T *at = src - row.mis;
         constexpr int AHEAD = 4;  // pieces of a thread in flight
-        for (int j0 = threadIdx.x; j0 < nvec; j0 += AHEAD * kThreads) {
+        int j = first + (int)threadIdx.x;
+        for (; j + (AHEAD - 1) * kThreads < end; j += AHEAD * kThreads) {
             RawPiece<T, VE> raw[AHEAD];
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const int64_t i = (int64_t)(j0 + u * kThreads) * VE - row.mis;
-                if (i >= 0 && i + VE <= n) {
-                    raw[u].w = row_piece(src + i);
-                } else {  // the slice's ends: -inf beside it
-                    float v[VE];
-#pragma unroll
-                    for (int e = 0; e < VE; ++e)
-                        v[e] = i + e >= 0 && i + e < n ? Elem<T>::to_f32(src[i + e]) : -INFINITY;
-                    raw[u] = narrow_piece<T, VE>(v);
-                }
-            }
+            for (int u = 0; u < AHEAD; ++u) raw[u].w = row_piece(at + (int64_t)(j + u * kThreads) * VE);
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
-                const int j = j0 + u * kThreads;
-                if (j < nvec) {
-                    const uint4 w = clean(raw[u]);
-                    put_piece(row.pieces + 16 * j, w);
-                    take(w);
-                }
+                const uint4 w = clean(raw[u]);
+                put_piece(row.pieces + 16 * (j + u * kThreads), w);
+                take(w);
             }
         }
+        for (; j < end; j += kThreads) {
+            RawPiece<T, VE> raw;
+            raw.w = row_piece(at + (int64_t)j * VE);
+            const uint4 w = clean(raw);
+            put_piece(row.pieces + 16 * j, w);
+            take(w);
+        }
+        // (one thread per end; a slice within one piece has one)
+        const bool head = threadIdx.x == 0 && first && all > 0, tail = threadIdx.x == 1 && end < all && end >= first;
+        if (head || tail) {
+            const int k = head ? 0 : end;
+            float v[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const int i = k * VE + e - row.mis;
+                v[e] = i >= 0 && i < n ? Elem<T>::to_f32(src[i]) : -INFINITY;
+            }
+            const uint4 w = clean(narrow_piece<T, VE>(v));
+            put_piece(row.pieces + 16 * k, w);
+            take(w);
+        }
+        __syncthreads();
     } else {
-        for (int64_t i0 = (int64_t)threadIdx.x * VE; i0 < n; i0 += (int64_t)kThreads * VE) {
+        for (int i0 = (int)threadIdx.x * VE; i0 < n; i0 += kThreads * VE) {
             float top = -INFINITY;
 #pragma unroll
             for (int e = 0; e < VE; ++e)
@@ -944,6 +961,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         return;
     }
     auto fast_e = [&](float l) { return e_below(l, mx); };
+    auto fast_e2 = [&](float2 l) {
+        const float2 d = fmul2(__fadd2_rn(l, make_float2(-mx, -mx)), make_float2(to_log2, to_log2));
+        return make_float2(ex2(d.x), ex2(d.y));
+    };
     auto exact_e = [&](float l) { return expf((l - mx) / temp); };
     auto over_min = [&](float l) {
         const float e = fast_e(l);
@@ -1042,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
         if (!cut_by_list<false, false, CACHED>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
-                                -FLT_MAX, [](float, uint32_t) { return true; }, fast_e))
+                                -FLT_MAX, [](float, uint32_t) { return true; }, fast_e, fast_e2))
             cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
                                   [](float, uint32_t) { return true; }, fast_e);
     }
@@ -1072,9 +1093,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         if (scale < 1e30f) {
             const float width = range / kCountBins;
             const double target = (double)top_p * zk;
-            done = use_k ? cut_by_list<true, false, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in, fast_e)
+            done = use_k ? cut_by_list<true, false, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in, fast_e,
+                                                            fast_e2)
                          : cut_by_list<true, true, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in,
-                                                           fast_e);
+                                                           fast_e, fast_e2);
         }
         if (!done)
             cut = narrow<true, ROUNDS>(row, sh, rank, cut, 0, (double)top_p * zk * 0x1p40, low, in, fast_e);
@@ -1088,37 +1110,56 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     } else if (!use_k && !use_p && !use_m) {
         // neighbouring threads on neighbouring tokens, eight of each in flight
         constexpr int U = 8;
-        for (int64_t i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-            float nz[U], l[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * kThreads < n) nz[u] = noise_at(noise + base + i0 + u * kThreads);
-#pragma unroll
-            for (int u = 0; u < U; ++u) l[u] = i0 + u * kThreads < n ? row.at(i0 + u * kThreads) : -INFINITY;
+        const float *nb = noise + base;
+        auto some = [&](const float (&l)[U], const float (&nz)[U], int i0) {
             const float ahead = ahead_now();
-            uint32_t may = 0;
+            bool may = false;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * kThreads < n && !behind(l[u], nz[u], ahead)) may |= 1u << u;
+            for (int u = 0; u < U; u += 2) {
+                const float2 e = fast_e2(make_float2(l[u], l[u + 1]));
+                may = may || !(e.x < ahead * nz[u]) || !(e.y < ahead * nz[u + 1]);
+            }
             if (may)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (may >> u & 1) run(l[u], (uint32_t)(base + i0 + u * kThreads), nz[u]);
+                    if (i0 + u * kThreads < n && !behind(l[u], nz[u], ahead))
+                        run(l[u], (uint32_t)(base + i0 + u * kThreads), nz[u]);
+        };
+        int i0 = threadIdx.x;
+        for (; i0 + (U - 1) * kThreads < n; i0 += U * kThreads) {
+            float nz[U], l[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) nz[u] = noise_at(nb + i0 + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < U; ++u) l[u] = row.at(i0 + u * kThreads);
+            some(l, nz, i0);
+        }
+        if (i0 < n) {
+            float nz[U], l[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = i0 + u * kThreads < n;
+                nz[u] = in ? noise_at(nb + i0 + u * kThreads) : 1.f;
+                l[u] = in ? row.at(i0 + u * kThreads) : -INFINITY;
+            }
+            some(l, nz, i0);
         }
     } else {
         const float low = use_m ? fmaxf(cut.l, mx + 1.0001f * logf(0.999f * min_p) * temp) : cut.l;
         auto left = [&](float l, uint32_t idx) { return cut.keeps(l, idx) && (!use_m || l == mx || over_min(l)); };
         if constexpr (CACHED) {
-            row.each_piece(low, [&](const auto &v, uint32_t idx) {
-                // (a masked token is never left, nor is a place beside the slice:
-                // no noise is read for either)
+            // (a masked token is never left, nor is a place outside the slice: no
+            // noise is read for either)
+            row.each_piece(low, [&](const auto &v, int i0) {
                 float nz[VE];
                 uint32_t on = 0;
+                const float *np = noise + base + i0;
+                const uint32_t idx = row.base + (uint32_t)i0;
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
                     if (left(e % 2 ? v[e / 2].y : v[e / 2].x, idx + e)) {
                         on |= 1u << e;
-                        nz[e] = noise_at(noise + (uint32_t)(idx + e));  // (idx may be below 0, mod 2^32)
+                        nz[e] = noise_at(np + e);
                     }
                 if (!on) return;
                 const float ahead = ahead_now();
