@@ -17,18 +17,21 @@
 // without a sort of the row, by a list of the tokens near the cut:
 //   - top-k up to half a CTA's threads: the k-th largest of the threads' own
 //     maxima bounds the k-th logit of a slice from below, and few more than k
-//     tokens reach it.  One CTA sorts the slices' lists and finishes the row.
+//     tokens reach it.  One CTA takes the slices' lists and finishes the row.
 //   - otherwise a histogram over bins of equal width in the logit counts the
 //     tokens.  For top-p the counts bound the mass above each bin to within
 //     the width of one, which leaves a bracket of one or two bins.  A second
 //     pass sums the mass above the bracket and lists the tokens in it; one
-//     CTA sorts the list and finds the exact token at which the cut lies.
+//     CTA finds the exact token of the list at which the cut lies.
+//   - a list is not sorted either: its tokens lie in the CTA's registers, and
+//     the logit at the cut (then, among equal ones, the index) is found bit by
+//     bit, with one block-wide sum per bit.
 //   - where a list does not fit (many equal logits), histograms over 11 bits
 //     of the logit's ordered key at a time find the value at the cut, and its
 //     tokens are counted in index order.
 // Masses in those are integers (units of 2^-40 of the largest token's), sums
-// are taken in fixed orders, and the order in which a list is filled does not
-// survive its sort: results do not change from run to run.  The noise is read
+// are taken in fixed orders, and the order in which a list is filled is not
+// looked at: results do not change from run to run.  The noise is read
 // only for tokens that are left.
 //
 #include <cfloat>
@@ -49,7 +52,8 @@ constexpr int kBins = 2048;         // bins of a histogram of masses
 constexpr int kCountBins = 4096;    // bins of a histogram of counts alone (over count and lo)
 constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;         // tokens near a cut that a CTA lists
-constexpr int kSort = 2048;         // tokens near a cut that are sorted
+constexpr int kNear = 2048;         // tokens near a cut that one CTA takes
+constexpr int kOwn = kNear / kThreads;
 constexpr int kMaxK = kThreads / 2; // top-k by the threads' maxima
 
 // What is left so far: logits above `l`, and those equal to it with an index
@@ -65,19 +69,18 @@ __device__ __forceinline__ Cut no_cut() { return Cut{-FLT_MAX, 0xffffffffu}; }
 // by itself: word offsets.  A histogram of masses holds tokens, and mass in
 // two words; over the same memory lie a histogram of counts alone and, behind
 // it, this CTA's list of tokens near a cut (ordered bits, then indexes).  The
-// first CTA of a cluster has the lists of all in its sort memory.
+// first CTA of a cluster has the lists of all behind that.
 constexpr uint32_t kCount = 0, kLo = kBins, kHi = 2 * kBins;
 constexpr uint32_t kListKey = kHi, kListIdx = kListKey + kList;
-constexpr uint32_t kSortKey = 3 * kBins, kSortIdx = kSortKey + kSort;
-constexpr uint32_t kRed = kSortIdx + kSort;                             // one word per warp, three times
+constexpr uint32_t kNearKey = 3 * kBins, kNearIdx = kNearKey + kNear;
+constexpr uint32_t kRed = kNearIdx + kNear;                             // one word per warp, three times
 constexpr uint32_t kRed2 = kRed + kWarps, kRed3 = kRed2 + kWarps;
 constexpr uint32_t kWords = kRed3 + kWarps;                             // single words
 constexpr uint32_t kPartMax = kWords, kPartZ = kWords + 1, kPartLeast = kWords + 2, kPartSum = kWords + 3,
-                   kPartAbove = kWords + 4, kListN = kWords + 5, kTies = kWords + 6, kBestKey = kWords + 7,
-                   kBestIdx = kWords + 8, kFoundBin = kWords + 9, kFoundLast = kWords + 10, kFoundCount = kWords + 11,
+                   kPartAbove = kWords + 4, kListN = kWords + 5, kTies = kWords + 6, kFoundBin = kWords + 9, kFoundLast = kWords + 10, kFoundCount = kWords + 11,
                    kFoundN = kWords + 12, kFoundMassLo = kWords + 13, kFoundMassHi = kWords + 14,
                    kFoundWLo = kWords + 15, kFoundWHi = kWords + 16, kLimit = kWords + 17, kCutL = kWords + 18,
-                   kCutEnd = kWords + 19, kRace = kWords + 20, kSortN = kWords + 21, kSortAt = kWords + 22;
+                   kCutEnd = kWords + 19, kRace = kWords + 20, kNearN = kWords + 21, kNearAt = kWords + 22;
 constexpr uint32_t kSharedBytes = (kWords + 24) * 4;
 static_assert(kCountBins <= kHi && 2 * kList <= kBins && kSharedBytes % 16 == 0, "layout");
 
@@ -107,6 +110,9 @@ struct Shared {
     }
     __device__ __forceinline__ void max_only(uint32_t w, uint32_t v) const {
         asm volatile("red.shared.max.u32 [%0], %1;\n" ::"r"(at(w)), "r"(v) : "memory");
+    }
+    __device__ __forceinline__ void min_only(uint32_t w, uint32_t v) const {
+        asm volatile("red.shared.min.u32 [%0], %1;\n" ::"r"(at(w)), "r"(v) : "memory");
     }
     __device__ __forceinline__ uint32_t mapped(uint32_t w, int rank) const {
         uint32_t a;
@@ -142,6 +148,20 @@ struct Shared {
         float s = __shfl_sync(0xffffffffu, v, 0);
         for (int q = 1; q < cs; ++q) s += __shfl_sync(0xffffffffu, v, q);
         return s;
+    }
+    // sum over the CTA's threads, by a counter that is zero before
+    __device__ __forceinline__ uint32_t block_add(uint32_t w, uint32_t v) const {
+        v = __reduce_add_sync(0xffffffffu, v);
+        if (threadIdx.x % 32 == 0) add_only(w, v);
+        __syncthreads();
+        return get(w);
+    }
+    // the last step of a row in whose words no CTA but the first is still read:
+    // that one goes on when all have come, the others do not wait for it
+    __device__ __forceinline__ void leave(int rank) const {
+        if (cs == 1) return;
+        asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        if (rank == 0) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     }
     // every CTA of the cluster in step, and its writes visible to the others
     __device__ __forceinline__ void sync() const {
@@ -290,6 +310,23 @@ template <typename T, bool CACHED> struct Row {
             RawPiece<T, VE> raw;
             raw.w = piece_at(pieces + 16 * j);
             if (piece_max<T>(raw.w) < low) continue;
+            float2 v[VE / 2];
+            widen2<T, VE>(v, raw);
+            f(v, j * VE - mis);
+        }
+    }
+    // the same, all lanes of a warp together (those without a piece get -inf)
+    template <typename F> __device__ __forceinline__ void each_piece_warp(float low, F &&f) const {
+        const int end = count();
+        for (int j0 = threadIdx.x / 32 * 32; j0 < end; j0 += kThreads) {
+            const int j = j0 + threadIdx.x % 32;
+            RawPiece<T, VE> raw;
+            float v1[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) v1[e] = -INFINITY;
+            if (j < end) raw.w = piece_at(pieces + 16 * j);
+            else raw = narrow_piece<T, VE>(v1);
+            if (!__any_sync(0xffffffffu, piece_max<T>(raw.w) >= low)) continue;
             float2 v[VE / 2];
             widen2<T, VE>(v, raw);
             f(v, j * VE - mis);
@@ -532,120 +569,166 @@ __device__ __forceinline__ void enlist(const Shared &sh, float l, uint32_t idx) 
     }
 }
 
-// Hands this CTA's list to the first CTA, in no order (the sort makes one).
-// All CTAs' lists are there once the cluster is in step; then kSortN of the
-// first CTA is their length, or above kSort if they do not fit.
+// The same for the tokens of a piece whose bits are set in `on` (all lanes of
+// the warp take part): one atomic per warp.
+template <int VE>
+__device__ __forceinline__ void enlist_piece(const Shared &sh, const float2 (&v)[VE / 2], uint32_t idx, uint32_t on) {
+    const int lane = threadIdx.x % 32;
+    const uint32_t mine = __popc(on);
+    uint32_t before = 0, total = 0;  // of this lane, and of the warp: bit planes of the counts (at most 8)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const uint32_t m = __ballot_sync(0xffffffffu, mine >> b & 1);
+        before += __popc(m & ((1u << lane) - 1)) << b;
+        total += __popc(m) << b;
+    }
+    if (total == 0) return;
+    uint32_t at = 0;
+    if (lane == 0) at = sh.add(kListN, total);
+    at = __shfl_sync(0xffffffffu, at, 0) + before;
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+        if (on >> e & 1) {
+            if (at < kList) {
+                sh.put(kListKey + at, order_bits(e % 2 ? v[e / 2].y : v[e / 2].x));
+                sh.put(kListIdx + at, idx + e);
+            }
+            ++at;
+        }
+}
+
+// Hands this CTA's list to the first CTA, in no order.
+// All CTAs' lists are there once the cluster is in step; then kNearN of the
+// first CTA is their length, or above kNear if they do not fit.
 __device__ __forceinline__ void send_list(const Shared &sh) {
     __syncthreads();
     const uint32_t c = sh.get(kListN);
-    if (threadIdx.x == 0) sh.put(kSortAt, sh.add(kSortN, 0, c <= kList ? c : kSort + 1));
+    if (threadIdx.x == 0) sh.put(kNearAt, sh.add(kNearN, 0, c <= kList ? c : kNear + 1));
     __syncthreads();
-    const uint32_t at = sh.get(kSortAt);
-    if (c > kList || at > kSort || at + c > kSort) return;
+    const uint32_t at = sh.get(kNearAt);
+    if (c > kList || at > kNear || at + c > kNear) return;
     for (uint32_t i = threadIdx.x; i < c; i += kThreads) {
-        sh.put(kSortKey + at + i, 0, sh.get(kListKey + i));
-        sh.put(kSortIdx + at + i, 0, sh.get(kListIdx + i));
+        sh.put(kNearKey + at + i, 0, sh.get(kListKey + i));
+        sh.put(kNearIdx + at + i, 0, sh.get(kListIdx + i));
     }
 }
 // Their length in every CTA, or -1.
 __device__ __forceinline__ int listed(const Shared &sh) {
-    const uint32_t n = sh.get(kSortN, 0);
-    return n <= kSort ? (int)n : -1;
+    const uint32_t n = sh.get(kNearN, 0);
+    return n <= kNear ? (int)n : -1;
 }
 
-// Sorts the lists in the first CTA, the first token of the order first.
-__device__ __forceinline__ void sort_lists(const Shared &sh, int total) {
-    int n = 32;
-    while (n < total) n *= 2;
-    for (int i = total + threadIdx.x; i < n; i += kThreads) {  // after every token
-        sh.put(kSortKey + i, 0);
-        sh.put(kSortIdx + i, 0xffffffffu);
-    }
-    for (int size = 2; size <= n; size *= 2)
-        for (int step = size / 2; step > 0; step /= 2) {
-            __syncthreads();
-            for (int p = threadIdx.x; p < n / 2; p += kThreads) {
-                const int i = 2 * p - (p & (step - 1)), j = i + step;
-                const uint32_t kx = sh.get(kSortKey + i), ky = sh.get(kSortKey + j);
-                const uint32_t ix = sh.get(kSortIdx + i), iy = sh.get(kSortIdx + j);
-                const bool first = kx > ky || (kx == ky && ix < iy);  // x before y
-                if (first != ((i & size) == 0)) {
-                    sh.put(kSortKey + i, ky);
-                    sh.put(kSortKey + j, kx);
-                    sh.put(kSortIdx + i, iy);
-                    sh.put(kSortIdx + j, ix);
-                }
-            }
+// The lists in the first CTA, in registers: token j of a thread has key 0 if
+// there is none.
+struct Near {
+    uint32_t key[kOwn], idx[kOwn];
+    __device__ __forceinline__ void load(const Shared &sh, int total) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = threadIdx.x + j * kThreads;
+            key[j] = i < total ? sh.get(kNearKey + i) : 0;
+            idx[j] = i < total ? sh.get(kNearIdx + i) : 0;
         }
-    __syncthreads();
-}
+    }
+};
 
-// e, a mass, in units of 2^-40 of the largest token's.
-__device__ __forceinline__ unsigned long long units(float e) { return __float2ull_rn(e * 0x1p40f); }
-
-// Of the first n sorted tokens, how many have less than `target` of mass
-// before them, with `above` before the first; *total is the mass of the n.
-// In whole units, so in no order.
-template <typename Mass>
-__device__ __forceinline__ int mass_prefix(const Shared &sh, int n, unsigned long long above,
-                                           unsigned long long target, Mass &&mass, unsigned long long *total) {
-    constexpr int PER = kSort / kThreads;
-    unsigned long long own[PER], sum = 0;
+// The cut in a list: the first token, in the order (l descending, index
+// ascending), at which the running weight reaches `target`, and with it all
+// before; the last token if the weights do not reach it.  LOW: the key's bits
+// below it say nothing (16-bit logits).  Weights are at most 2^30.  Counters
+// lie over the histogram.
+template <int LOW>
+__device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, const uint32_t (&weight)[kOwn],
+                                        unsigned long long target, int64_t V) {
+    uint32_t slot = kCount;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += kThreads) sh.put(kCount + i, i == 1 ? 0xffffffffu : 0);
+    __syncthreads();
+    // the range of the keys: its common high bits need no rounds
+    uint32_t most = 0, least = 0xffffffffu;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int i = threadIdx.x * PER + j;
-        own[j] = i < n ? units(mass(from_order_bits(sh.get(kSortKey + i)))) : 0;
-        sum += own[j];
-    }
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    unsigned long long in = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long v = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += v;
+    for (int j = 0; j < kOwn; ++j)
+        if (near.key[j]) {
+            most = max(most, near.key[j]);
+            least = min(least, near.key[j]);
+        }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (threadIdx.x % 32 == 0) {
+        sh.max_only(slot, most);
+        sh.min_only(slot + 1, least);
     }
     __syncthreads();
-    if (lane == 31) {
-        sh.put(kRed + warp, (uint32_t)in);
-        sh.put(kRed2 + warp, (uint32_t)(in >> 32));
-    }
-    __syncthreads();
-    unsigned long long before = above, all = 0;
+    most = sh.get(slot);
+    least = sh.get(slot + 1);
+    slot += 2;
+    auto sum = [&](auto &&counts) {  // of the weights of the tokens that count
+        unsigned long long v = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const unsigned long long v = join64(sh.get(kRed + i), sh.get(kRed2 + i));
-        if (i < warp) before += v;
-        all += v;
-    }
-    before += in - sum;
-    *total = all;
-    int count = 0;
+        for (int j = 0; j < kOwn; ++j)
+            if (near.key[j] && counts(j)) v += weight[j];
+        const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7fffu);
+        const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 15));
+        if (threadIdx.x % 32 == 0) {
+            sh.add_only(slot, lo);
+            sh.add_only(slot + 1, hi);
+        }
+        __syncthreads();
+        v = sh.get(slot) + ((unsigned long long)sh.get(slot + 1) << 15);
+        slot += 2;
+        return v;
+    };
+    auto number = [&](auto &&counts) {
+        uint32_t v = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        if ((int)threadIdx.x * PER + j < n && before < target) ++count;
-        before += own[j];
+        for (int j = 0; j < kOwn; ++j) v += near.key[j] && counts(j);
+        v = sh.block_add(slot, v);
+        ++slot;
+        return v;
+    };
+    const unsigned long long all = sum([](int) { return true; });
+    if (all < target) return Cut{from_order_bits(least), 0xffffffffu};
+    uint32_t at = least;
+    if (most != least) {
+        const int top = 31 - __clz(most ^ least);
+        at = top == 31 ? 0 : most >> (top + 1) << (top + 1);
+#pragma unroll 1
+        for (int bit = top; bit >= LOW; --bit) {
+            const uint32_t t = at | (1u << bit);
+            if (sum([&](int j) { return near.key[j] >= t; }) >= target) at = t;
+        }
     }
-    count = __reduce_add_sync(0xffffffffu, count);
-    __syncthreads();
-    if (lane == 0) sh.put(kRed + warp, (uint32_t)count);
-    __syncthreads();
-    count = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) count += (int)sh.get(kRed + i);
-    return count;
+    auto equal = [&](int j) { return near.key[j] >> LOW == at >> LOW; };
+    const unsigned long long before = sum([&](int j) { return near.key[j] >> LOW > at >> LOW; });
+    const uint32_t n_eq = number(equal);
+    const unsigned long long of_eq = sum(equal);
+    const unsigned long long each = of_eq / n_eq;  // (equal logits have equal weights)
+    const unsigned long long want = each > 0 ? (target - before + each - 1) / each : 1;
+    // 16-bit logits have equal low bits of the key: ones below 0
+    const float l = from_order_bits(LOW > 0 && at >> 31 == 0 ? at | ((1u << LOW) - 1) : at);
+    if (want >= n_eq) return Cut{l, 0xffffffffu};
+    uint32_t end = 0;  // index of the want-th
+#pragma unroll 1
+    for (int bit = 31 - __clz((uint32_t)V); bit >= 0; --bit) {
+        const uint32_t t = end | (1u << bit);
+        if (number([&](int j) { return equal(j) && near.idx[j] < t; }) < want) end = t;
+    }
+    return Cut{l, end + 1};
 }
 
 // The cut at which the running count of tokens reaches `k`, or the running
 // mass `target`, by a histogram of counts over bins of width 1/scale about the
-// multiples of that below `mx`, and a sorted list of the bin (of the bracket)
-// that holds it; `width` is a bin's in units of log(e).  ALL: every token of
+// multiples of that below `mx`, and a list of the bin (of the bracket) that
+// holds it; `width` is a bin's in units of log(e).  ALL: every token of
 // logit `low` or more takes part, and the bins cover all of those; else those
 // of which `in(l, idx)` holds, the last bin taking what lies below.  False:
 // the list does not fit.
-template <bool MASS, bool ALL, bool CACHED, typename RowT, typename In, typename Mass, typename Mass2>
+template <bool MASS, bool ALL, bool CACHED, int LOW, typename RowT, typename In, typename Mass, typename Mass2,
+          typename Prefetch>
 __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, int rank, Cut &cut, uint32_t k,
-                                            double target, float mx, float scale, float width, float low, In &&in,
-                                            Mass &&mass, Mass2 &&mass2) {
+                                            double target, float mx, float scale, float width, float low, int64_t V,
+                                            In &&in, Mass &&mass, Mass2 &&mass2,
+                                            Prefetch &&prefetch) {
     constexpr bool PIECES = ALL && CACHED;
     // 0 is the top bin: the distance from mx in bins, rounded by the sum with
     // 2^23, whose low bits it then is (above all bins for -inf)
@@ -662,7 +745,7 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         sh.put(kFoundLast, kCountBins - 1);
         sh.put(kFoundCount, 0);
         sh.put(kListN, 0);
-        sh.put(kSortN, 0);
+        sh.put(kNearN, 0);
     }
     __syncthreads();
     if constexpr (PIECES) {
@@ -730,8 +813,8 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     if constexpr (PIECES) {
         const float f0 = kMagic + (float)b0, f1 = kMagic + (float)b1;
         float2 sum2 = make_float2(0.f, 0.f);
-        row.each_piece(low, [&](const auto &v, int i0) {
-            bool some = false;  // of the piece is in the bracket
+        row.each_piece_warp(low, [&](const auto &v, int i0) {
+            bool some = false, ahead = false;  // of the piece is in the bracket, above it
 #pragma unroll
             for (const float2 &w : v) {
                 const float2 m = in_bins(w);
@@ -739,17 +822,19 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
                     const float2 e = mass2(w);
                     sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? e.x : 0.f, m.y < f0 ? e.y : 0.f));
                 }
+                ahead = ahead || m.x < f0 || m.y < f0;
                 some = some || (m.x >= f0 && m.x <= f1) || (m.y >= f0 && m.y <= f1);
             }
-            if (some) {
-                uint32_t idx = row.base + (uint32_t)i0;
+            if (ahead) prefetch(i0);
+            if (__any_sync(0xffffffffu, some)) {
+                constexpr int VE = sizeof(v) / sizeof(float);
+                uint32_t on = 0;
 #pragma unroll
-                for (const float2 &w : v) {
-                    const float2 m = in_bins(w);
-                    if (m.x >= f0 && m.x <= f1) enlist(sh, w.x, idx);
-                    if (m.y >= f0 && m.y <= f1) enlist(sh, w.y, idx + 1);
-                    idx += 2;
+                for (int e = 0; e < VE; e += 2) {
+                    const float2 m = in_bins(v[e / 2]);
+                    on |= (m.x >= f0 && m.x <= f1 ? 1u << e : 0) | (m.y >= f0 && m.y <= f1 ? 2u << e : 0);
                 }
+                enlist_piece<VE>(sh, v, row.base + (uint32_t)i0, on);
             }
         });
         above = sum2.x + sum2.y;
@@ -770,24 +855,31 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     const int total = listed(sh);
     if (total < 0) return false;
     if (rank == 0) {
-        sort_lists(sh, total);
-        int keep;
-        if (MASS) {
-            unsigned long long all;
-            keep = mass_prefix(sh, total, units(sh.sum_ctas(kPartAbove)), units((float)target), mass, &all);
-        } else {
-            keep = min(total, (int)(k - above_count));
+        Cut c = no_cut();
+        if (total > 0) {
+            Near near;
+            near.load(sh, total);
+            uint32_t weight[kOwn];
+            unsigned long long want;
+            if (MASS) {
+                // weights in units of 2^-30 of the bracket's largest mass
+                const float most = mass(mx - ((float)b0 - 0.5f) / scale);
+                const float unit = 0x1p30f / fmaxf(most, FLT_MIN);
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j)
+                    weight[j] = min(__float2uint_rn(mass(from_order_bits(near.key[j])) * unit), 1u << 30);
+                const double left = (target - (double)sh.sum_ctas(kPartAbove)) * (double)unit;
+                want = left > 1 ? __double2ull_ru(left) : 1;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) weight[j] = 1;
+                want = k - above_count;
+            }
+            c = cut_near<LOW>(sh, near, weight, want, V);
         }
         if ((int)threadIdx.x < sh.cs) {
-            float l = -FLT_MAX;
-            uint32_t end = 0xffffffffu;
-            if (total > 0) {  // none kept: everything above the first of the list
-                const int i = keep > 0 ? keep - 1 : 0;
-                l = from_order_bits(sh.get(kSortKey + i));
-                end = keep > 0 ? sh.get(kSortIdx + i) + 1 : 0;
-            }
-            sh.put(kCutL, (int)threadIdx.x, __float_as_uint(l));
-            sh.put(kCutEnd, (int)threadIdx.x, end);
+            sh.put(kCutL, (int)threadIdx.x, __float_as_uint(c.l));
+            sh.put(kCutEnd, (int)threadIdx.x, c.end);
         }
     }
     sh.sync();
@@ -800,6 +892,7 @@ template <typename T, bool CACHED>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, const int cs, const int64_t slice) {
     constexpr int VE = 16 / sizeof(T);
     constexpr int ROUNDS = sizeof(T) == 2 ? 2 : 3;
+    constexpr int LOW = sizeof(T) == 2 ? 13 : 0;  // bits of a key that say nothing
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const Shared sh{static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)), cs};
     pdl_trigger();
@@ -926,12 +1019,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (threadIdx.x == 0) {
         sh.putf(kRace, 0.f);
         sh.put(kListN, 0);
-        sh.put(kSortN, 0);
+        sh.put(kNearN, 0);
     }
     __syncthreads();
-    mx = sh.getf(kRed);
-    z = sh.getf(kRed2);
-    for (int i = 1; i < kWarps; ++i) join(sh.getf(kRed + i), sh.getf(kRed2 + i));
+    mx = sh.getf(kRed + threadIdx.x % kWarps);
+    z = sh.getf(kRed2 + threadIdx.x % kWarps);
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, mx, o), oz = __shfl_xor_sync(0xffffffffu, z, o);
+        join(om, oz);
+    }
+    z = __shfl_sync(0xffffffffu, z, 0);  // (the lanes' sums may differ in their last bit)
     if (cs > 1) {
         if (threadIdx.x == 0) {
             sh.putf(kPartMax, mx);
@@ -957,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             a.token[r] = -1;
             if (a.logprob) a.logprob[r] = -INFINITY;
         }
-        sh.sync();
+        sh.sync();  // no CTA leaves while another reads its words
         return;
     }
     auto fast_e = [&](float l) { return e_below(l, mx); };
@@ -1023,23 +1121,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const int total = listed(sh);
         if (total >= 0) {
             if (rank == 0) {
-                sort_lists(sh, total);
-                int left = min(total, (int)top_k);
+                Near near;
+                near.load(sh, total);
+                uint32_t weight[kOwn];
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) weight[j] = 1;
+                cut = cut_near<LOW>(sh, near, weight, (unsigned long long)top_k, a.V);
                 if (use_p) {
-                    unsigned long long zk, all;
-                    mass_prefix(sh, left, 0, 0, fast_e, &zk);
-                    const unsigned long long target = __double2ull_ru((double)top_p * (double)zk);
-                    left = max(1, mass_prefix(sh, left, 0, target, fast_e, &all));
+                    unsigned long long own = 0;
+#pragma unroll
+                    for (int j = 0; j < kOwn; ++j) {
+                        const float l = from_order_bits(near.key[j]);
+                        if (near.key[j] && !cut.keeps(l, near.idx[j])) near.key[j] = 0;
+                        weight[j] = near.key[j] ? __float2uint_rn(fast_e(l) * 0x1p30f) : 0;
+                        own += weight[j];
+                    }
+                    const uint32_t lo = sh.block_add(kCount + 254, (uint32_t)own & 0x7fffu);
+                    const uint32_t hi = sh.block_add(kCount + 255, (uint32_t)(own >> 15));
+                    const double zk = (double)(lo + ((unsigned long long)hi << 15));
+                    cut = cut_near<LOW>(sh, near, weight, __double2ull_ru((double)top_p * zk), a.V);
                 }
-                if ((int)threadIdx.x < left) {
-                    const float l = from_order_bits(sh.get(kSortKey + threadIdx.x));
-                    const uint32_t idx = sh.get(kSortIdx + threadIdx.x);
-                    if (!use_m || threadIdx.x == 0 || over_min(l)) run(l, idx, noise_at(noise + idx));
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) {
+                    const float l = from_order_bits(near.key[j]);
+                    if (near.key[j] && cut.keeps(l, near.idx[j]) && (!use_m || l == mx || over_min(l)))
+                        run(l, near.idx[j], noise_at(noise + near.idx[j]));
                 }
                 const unsigned long long w = winner();
                 if (threadIdx.x == 0) finish(0xffffffffu - (uint32_t)w);
             }
-            sh.sync();  // no CTA leaves while another reads its list
+            sh.leave(rank);  // the first CTA stays while another reads its words
             return;
         }
         cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
@@ -1062,8 +1173,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             least = __shfl_sync(0xffffffffu, least, 0);
         }
         const float range = least > -INFINITY ? fmaxf(1.5f * (mx - least), 1e-20f) : 16.f * temp;
-        if (!cut_by_list<false, false, CACHED>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
-                                -FLT_MAX, [](float, uint32_t) { return true; }, fast_e, fast_e2))
+        if (!cut_by_list<false, false, CACHED, LOW>(row, sh, rank, cut, (uint32_t)top_k, 0.0, mx, fminf(kCountBins / range, 1e30f), 0.f,
+                                -FLT_MAX, a.V, [](float, uint32_t) { return true; }, fast_e, fast_e2, [](int) {}))
             cut = narrow<false, ROUNDS>(row, sh, rank, cut, (uint32_t)top_k, 0.0, -FLT_MAX,
                                   [](float, uint32_t) { return true; }, fast_e);
     }
@@ -1093,10 +1204,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         if (scale < 1e30f) {
             const float width = range / kCountBins;
             const double target = (double)top_p * zk;
-            done = use_k ? cut_by_list<true, false, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in, fast_e,
-                                                            fast_e2)
-                         : cut_by_list<true, true, CACHED>(row, sh, rank, cut, 0, target, mx, scale, width, low, in,
-                                                           fast_e, fast_e2);
+            // the noise of what is above the bracket will be wanted
+            auto prefetch = [&](int i0) {
+                asm volatile("prefetch.global.L2 [%0];\n" ::"l"(noise + base + max(i0, 0)));
+            };
+            done = use_k ? cut_by_list<true, false, CACHED, LOW>(row, sh, rank, cut, 0, target, mx, scale, width, low,
+                                                                 a.V, in, fast_e, fast_e2, prefetch)
+                         : cut_by_list<true, true, CACHED, LOW>(row, sh, rank, cut, 0, target, mx, scale, width, low,
+                                                                a.V, in, fast_e, fast_e2, prefetch);
         }
         if (!done)
             cut = narrow<true, ROUNDS>(row, sh, rank, cut, 0, (double)top_p * zk * 0x1p40, low, in, fast_e);
@@ -1177,13 +1292,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     unsigned long long w = winner();
     if (cs > 1) {
+        // each CTA's into the first one's memory
         if (threadIdx.x == 0) {
-            sh.put(kBestIdx, (uint32_t)w);
-            sh.put(kBestKey, (uint32_t)(w >> 32));
+            sh.put(kNearKey + rank, 0, (uint32_t)(w >> 32));
+            sh.put(kNearIdx + rank, 0, (uint32_t)w);
         }
         sh.sync();
         if (rank == 0 && threadIdx.x < 32) {
-            w = join64(sh.each_cta(kBestIdx, 0), sh.each_cta(kBestKey, 0));
+            const int q = threadIdx.x < cs ? threadIdx.x : 0;
+            w = join64(sh.get(kNearIdx + q), sh.get(kNearKey + q));
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) {
                 const unsigned long long p = __shfl_xor_sync(0xffffffffu, w, o);
@@ -1192,7 +1309,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
     }
     if (rank == 0 && threadIdx.x == 0) finish(0xffffffffu - (uint32_t)w);
-    sh.sync();  // no CTA leaves while another reads its shared memory
 }
 
 constexpr size_t kMostShared = 200 * 1024;
