@@ -569,34 +569,6 @@ __device__ __forceinline__ void enlist(const Shared &sh, float l, uint32_t idx) 
     }
 }
 
-// The same for the tokens of a piece whose bits are set in `on` (all lanes of
-// the warp take part): one atomic per warp.
-template <int VE>
-__device__ __forceinline__ void enlist_piece(const Shared &sh, const float2 (&v)[VE / 2], uint32_t idx, uint32_t on) {
-    const int lane = threadIdx.x % 32;
-    const uint32_t mine = __popc(on);
-    uint32_t before = 0, total = 0;  // of this lane, and of the warp: bit planes of the counts (at most 8)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t m = __ballot_sync(0xffffffffu, mine >> b & 1);
-        before += __popc(m & ((1u << lane) - 1)) << b;
-        total += __popc(m) << b;
-    }
-    if (total == 0) return;
-    uint32_t at = 0;
-    if (lane == 0) at = sh.add(kListN, total);
-    at = __shfl_sync(0xffffffffu, at, 0) + before;
-#pragma unroll
-    for (int e = 0; e < VE; ++e)
-        if (on >> e & 1) {
-            if (at < kList) {
-                sh.put(kListKey + at, order_bits(e % 2 ? v[e / 2].y : v[e / 2].x));
-                sh.put(kListIdx + at, idx + e);
-            }
-            ++at;
-        }
-}
-
 // Hands this CTA's list to the first CTA, in no order.
 // All CTAs' lists are there once the cluster is in step; then kNearN of the
 // first CTA is their length, or above kNear if they do not fit.
@@ -635,14 +607,15 @@ struct Near {
 // The cut in a list: the first token, in the order (l descending, index
 // ascending), at which the running weight reaches `target`, and with it all
 // before; the last token if the weights do not reach it.  LOW: the key's bits
-// below it say nothing (16-bit logits).  Weights are at most 2^30.  Counters
-// lie over the histogram.
-template <int LOW>
-__device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, const uint32_t (&weight)[kOwn],
-                                        unsigned long long target, int64_t V) {
+// below it say nothing (16-bit logits).  MASS: weights of at most 2^30 (else
+// every token weighs one).  Counters lie over the histogram.
+template <bool MASS, int LOW>
+__device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, int total,
+                                        const uint32_t (&weight)[kOwn], unsigned long long target, int64_t V) {
+    const int own = (total + kThreads - 1) / kThreads;  // tokens of a thread, at most
     uint32_t slot = kCount;
     __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += kThreads) sh.put(kCount + i, i == 1 ? 0xffffffffu : 0);
+    if (threadIdx.x < 128) sh.put(kCount + threadIdx.x, threadIdx.x == 1 ? 0xffffffffu : 0);
     __syncthreads();
     // the range of the keys: its common high bits need no rounds
     uint32_t most = 0, least = 0xffffffffu;
@@ -662,11 +635,19 @@ __device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, cons
     most = sh.get(slot);
     least = sh.get(slot + 1);
     slot += 2;
-    auto sum = [&](auto &&counts) {  // of the weights of the tokens that count
+    auto number = [&](auto &&counts) {  // of the tokens that count
+        int v = __syncthreads_count(near.key[0] && counts(0));
+#pragma unroll
+        for (int j = 1; j < kOwn; ++j)
+            if (j < own) v += __syncthreads_count(near.key[j] && counts(j));
+        return (uint32_t)v;
+    };
+    auto sum = [&](auto &&counts) -> unsigned long long {  // of their weights
+        if constexpr (!MASS) return number(counts);
         unsigned long long v = 0;
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            if (near.key[j] && counts(j)) v += weight[j];
+            if (j < own && near.key[j] && counts(j)) v += weight[j];
         const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7fffu);
         const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 15));
         if (threadIdx.x % 32 == 0) {
@@ -676,14 +657,6 @@ __device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, cons
         __syncthreads();
         v = sh.get(slot) + ((unsigned long long)sh.get(slot + 1) << 15);
         slot += 2;
-        return v;
-    };
-    auto number = [&](auto &&counts) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) v += near.key[j] && counts(j);
-        v = sh.block_add(slot, v);
-        ++slot;
         return v;
     };
     const unsigned long long all = sum([](int) { return true; });
@@ -701,9 +674,11 @@ __device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, cons
     auto equal = [&](int j) { return near.key[j] >> LOW == at >> LOW; };
     const unsigned long long before = sum([&](int j) { return near.key[j] >> LOW > at >> LOW; });
     const uint32_t n_eq = number(equal);
-    const unsigned long long of_eq = sum(equal);
-    const unsigned long long each = of_eq / n_eq;  // (equal logits have equal weights)
-    const unsigned long long want = each > 0 ? (target - before + each - 1) / each : 1;
+    unsigned long long want = target - before;
+    if (MASS) {
+        const unsigned long long each = sum(equal) / n_eq;  // (equal logits have equal weights)
+        want = each > 0 ? (want + each - 1) / each : 1;
+    }
     // 16-bit logits have equal low bits of the key: ones below 0
     const float l = from_order_bits(LOW > 0 && at >> 31 == 0 ? at | ((1u << LOW) - 1) : at);
     if (want >= n_eq) return Cut{l, 0xffffffffu};
@@ -813,28 +788,25 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     if constexpr (PIECES) {
         const float f0 = kMagic + (float)b0, f1 = kMagic + (float)b1;
         float2 sum2 = make_float2(0.f, 0.f);
-        row.each_piece_warp(low, [&](const auto &v, int i0) {
-            bool some = false, ahead = false;  // of the piece is in the bracket, above it
+        row.each_piece(low, [&](const auto &v, int i0) {
+            constexpr int VE = sizeof(v) / sizeof(float);
+            uint32_t on = 0;      // bits of the tokens in the bracket
+            bool ahead = false;   // one is above it
 #pragma unroll
-            for (const float2 &w : v) {
-                const float2 m = in_bins(w);
+            for (int e = 0; e < VE; e += 2) {
+                const float2 m = in_bins(v[e / 2]);
                 if (MASS) {
-                    const float2 e = mass2(w);
-                    sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? e.x : 0.f, m.y < f0 ? e.y : 0.f));
+                    const float2 x = mass2(v[e / 2]);
+                    sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? x.x : 0.f, m.y < f0 ? x.y : 0.f));
                 }
                 ahead = ahead || m.x < f0 || m.y < f0;
-                some = some || (m.x >= f0 && m.x <= f1) || (m.y >= f0 && m.y <= f1);
+                on |= (m.x >= f0 && m.x <= f1 ? 1u << e : 0) | (m.y >= f0 && m.y <= f1 ? 2u << e : 0);
             }
             if (ahead) prefetch(i0);
-            if (__any_sync(0xffffffffu, some)) {
-                constexpr int VE = sizeof(v) / sizeof(float);
-                uint32_t on = 0;
-#pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    const float2 m = in_bins(v[e / 2]);
-                    on |= (m.x >= f0 && m.x <= f1 ? 1u << e : 0) | (m.y >= f0 && m.y <= f1 ? 2u << e : 0);
-                }
-                enlist_piece<VE>(sh, v, row.base + (uint32_t)i0, on);
+            while (on) {
+                const int e = __ffs(on) - 1;
+                on &= on - 1;
+                enlist(sh, row.at(i0 + e), row.base + (uint32_t)(i0 + e));
             }
         });
         above = sum2.x + sum2.y;
@@ -875,7 +847,7 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
                 for (int j = 0; j < kOwn; ++j) weight[j] = 1;
                 want = k - above_count;
             }
-            c = cut_near<LOW>(sh, near, weight, want, V);
+            c = cut_near<MASS, LOW>(sh, near, total, weight, want, V);
         }
         if ((int)threadIdx.x < sh.cs) {
             sh.put(kCutL, (int)threadIdx.x, __float_as_uint(c.l));
@@ -1069,11 +1041,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         if (fabsf(e - min_p) <= 1e-4f * min_p) return exact_e(l) >= min_p;
         return e >= min_p;
     };
-    // the race: a key is worked out in full only if it may be the best
+    // The race.  A key is worked out in full only where the rough one, which is
+    // within a ten-thousandth, may be the best.
+    constexpr float kNearly = 0.9998f;
     float best = -1.f;
     uint32_t best_i = 0xffffffffu;
-    auto behind = [&](float l, float nz, float ahead) { return fast_e(l) < ahead * nz; };
-    auto ahead_now = [&]() { return 0.9999f * fmaxf(best, sh.getf(kRace)); };
+    auto rough = [&](float e, float nz) { return e * rcpf(fmaxf(nz, FLT_MIN)); };
     auto run = [&](float l, uint32_t idx, float nz) {
         const float key = exact_e(l) / fmaxf(nz, FLT_MIN);
         if (l > -INFINITY && (key > best || (key == best && idx < best_i))) {
@@ -1082,25 +1055,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             best_i = idx;
         }
     };
+    // a batch of tokens, all lanes of a warp together; those of rough key -1 do
+    // not take part
+    auto batch = [&](const auto &key, auto &&token) {
+        constexpr int U = sizeof(key) / sizeof(float);
+        float most = key[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) most = fmaxf(most, key[u]);
+        const float ahead = kNearly * sh.getf(kRace);
+        if (!__any_sync(0xffffffffu, most >= ahead)) return;
+        const uint32_t of_warp = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(most, 0.f)));
+        const float least = fmaxf(ahead, kNearly * __uint_as_float(of_warp));
+        if (most >= least)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (key[u] >= least) token(u);
+    };
     // this CTA's winner, as (key, ~index), in every thread
     auto winner = [&]() {
-        unsigned long long w = best < 0.f ? 0ull : join64(0xffffffffu - best_i, __float_as_uint(best));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long p = __shfl_xor_sync(0xffffffffu, w, o);
-            if (p > w) w = p;
-        }
+        uint32_t k = best < 0.f ? 0 : __float_as_uint(best), i = best < 0.f ? 0xffffffffu : best_i;
+        auto warp_best = [&]() {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, k);
+            i = __reduce_min_sync(0xffffffffu, k == top ? i : 0xffffffffu);
+            k = top;
+        };
+        warp_best();
         __syncthreads();
         if (threadIdx.x % 32 == 0) {
-            sh.put(kRed + threadIdx.x / 32, (uint32_t)w);
-            sh.put(kRed2 + threadIdx.x / 32, (uint32_t)(w >> 32));
+            sh.put(kRed + threadIdx.x / 32, k);
+            sh.put(kRed2 + threadIdx.x / 32, i);
         }
         __syncthreads();
-        for (int i = 0; i < kWarps; ++i) {
-            const unsigned long long p = join64(sh.get(kRed + i), sh.get(kRed2 + i));
-            if (p > w) w = p;
-        }
-        return w;
+        k = sh.get(kRed + threadIdx.x % kWarps);
+        i = sh.get(kRed2 + threadIdx.x % kWarps);
+        warp_best();
+        return join64(0xffffffffu - i, k);
     };
 
     Cut cut = no_cut();
@@ -1126,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 uint32_t weight[kOwn];
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) weight[j] = 1;
-                cut = cut_near<LOW>(sh, near, weight, (unsigned long long)top_k, a.V);
+                cut = cut_near<false, LOW>(sh, near, total, weight, (unsigned long long)top_k, a.V);
                 if (use_p) {
                     unsigned long long own = 0;
 #pragma unroll
@@ -1136,10 +1125,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                         weight[j] = near.key[j] ? __float2uint_rn(fast_e(l) * 0x1p30f) : 0;
                         own += weight[j];
                     }
-                    const uint32_t lo = sh.block_add(kCount + 254, (uint32_t)own & 0x7fffu);
-                    const uint32_t hi = sh.block_add(kCount + 255, (uint32_t)(own >> 15));
+                    const uint32_t lo = sh.block_add(kCount + 126, (uint32_t)own & 0x7fffu);
+                    const uint32_t hi = sh.block_add(kCount + 127, (uint32_t)(own >> 15));
                     const double zk = (double)(lo + ((unsigned long long)hi << 15));
-                    cut = cut_near<LOW>(sh, near, weight, __double2ull_ru((double)top_p * zk), a.V);
+                    cut = cut_near<true, LOW>(sh, near, total, weight, __double2ull_ru((double)top_p * zk), a.V);
                 }
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
@@ -1226,38 +1215,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         // neighbouring threads on neighbouring tokens, eight of each in flight
         constexpr int U = 8;
         const float *nb = noise + base;
-        auto some = [&](const float (&l)[U], const float (&nz)[U], int i0) {
-            const float ahead = ahead_now();
-            bool may = false;
+        for (int i0 = threadIdx.x; i0 - (int)threadIdx.x < n; i0 += U * kThreads) {
+            float nz[U], l[U], key[U];
+            if (i0 + (U - 1) * kThreads < n) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) nz[u] = noise_at(nb + i0 + u * kThreads);
+#pragma unroll
+                for (int u = 0; u < U; ++u) l[u] = row.at(i0 + u * kThreads);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = i0 + u * kThreads < n;
+                    nz[u] = in ? noise_at(nb + i0 + u * kThreads) : 1.f;
+                    l[u] = in ? row.at(i0 + u * kThreads) : -INFINITY;
+                }
+            }
 #pragma unroll
             for (int u = 0; u < U; u += 2) {
                 const float2 e = fast_e2(make_float2(l[u], l[u + 1]));
-                may = may || !(e.x < ahead * nz[u]) || !(e.y < ahead * nz[u + 1]);
+                key[u] = l[u] > -INFINITY ? rough(e.x, nz[u]) : -1.f;
+                key[u + 1] = l[u + 1] > -INFINITY ? rough(e.y, nz[u + 1]) : -1.f;
             }
-            if (may)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i0 + u * kThreads < n && !behind(l[u], nz[u], ahead))
-                        run(l[u], (uint32_t)(base + i0 + u * kThreads), nz[u]);
-        };
-        int i0 = threadIdx.x;
-        for (; i0 + (U - 1) * kThreads < n; i0 += U * kThreads) {
-            float nz[U], l[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) nz[u] = noise_at(nb + i0 + u * kThreads);
-#pragma unroll
-            for (int u = 0; u < U; ++u) l[u] = row.at(i0 + u * kThreads);
-            some(l, nz, i0);
-        }
-        if (i0 < n) {
-            float nz[U], l[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = i0 + u * kThreads < n;
-                nz[u] = in ? noise_at(nb + i0 + u * kThreads) : 1.f;
-                l[u] = in ? row.at(i0 + u * kThreads) : -INFINITY;
-            }
-            some(l, nz, i0);
+            batch(key, [&](int u) { run(l[u], (uint32_t)(base + i0 + u * kThreads), nz[u]); });
         }
     } else {
         const float low = use_m ? fmaxf(cut.l, mx + 1.0001f * logf(0.999f * min_p) * temp) : cut.l;
@@ -1265,24 +1244,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         if constexpr (CACHED) {
             // (a masked token is never left, nor is a place outside the slice: no
             // noise is read for either)
-            row.each_piece(low, [&](const auto &v, int i0) {
-                float nz[VE];
-                uint32_t on = 0;
+            row.each_piece_warp(low, [&](const auto &v, int i0) {
+                float nz[VE], key[VE];
                 const float *np = noise + base + i0;
                 const uint32_t idx = row.base + (uint32_t)i0;
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (left(e % 2 ? v[e / 2].y : v[e / 2].x, idx + e)) {
-                        on |= 1u << e;
-                        nz[e] = noise_at(np + e);
-                    }
-                if (!on) return;
-                const float ahead = ahead_now();
-#pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    const float l = e % 2 ? v[e / 2].y : v[e / 2].x;
-                    if ((on >> e & 1) && !behind(l, nz[e], ahead)) run(l, idx + e, nz[e]);
+                    const bool on = left(e % 2 ? v[e / 2].y : v[e / 2].x, idx + e);
+                    nz[e] = on ? noise_at(np + e) : 1.f;
+                    key[e] = on ? 0.f : -1.f;
                 }
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) {
+                    const float2 x = fast_e2(v[e / 2]);
+                    if (key[e] == 0.f) key[e] = rough(x.x, nz[e]);
+                    if (key[e + 1] == 0.f) key[e + 1] = rough(x.y, nz[e + 1]);
+                }
+                batch(key, [&](int e) { run(e % 2 ? v[e / 2].y : v[e / 2].x, idx + e, nz[e]); });
             });
         } else {
             row.each(low, [&](float l, uint32_t idx) {
