@@ -24,8 +24,8 @@
 //     pass sums the mass above the bracket and lists the tokens in it; one
 //     CTA finds the exact token of the list at which the cut lies.
 //   - a list is not sorted either: its tokens lie in the CTA's registers, and
-//     the logit at the cut (then, among equal ones, the index) is found bit by
-//     bit, with one block-wide sum per bit.
+//     the logit at the cut (then, among equal ones, the index) is found by
+//     histograms over eight bits at a time.
 //   - where a list does not fit (many equal logits), histograms over 11 bits
 //     of the logit's ordered key at a time find the value at the cut, and its
 //     tokens are counted in index order.
@@ -148,13 +148,6 @@ struct Shared {
         float s = __shfl_sync(0xffffffffu, v, 0);
         for (int q = 1; q < cs; ++q) s += __shfl_sync(0xffffffffu, v, q);
         return s;
-    }
-    // sum over the CTA's threads, by a counter that is zero before
-    __device__ __forceinline__ uint32_t block_add(uint32_t w, uint32_t v) const {
-        v = __reduce_add_sync(0xffffffffu, v);
-        if (threadIdx.x % 32 == 0) add_only(w, v);
-        __syncthreads();
-        return get(w);
     }
     // the last step of a row in whose words no CTA but the first is still read:
     // that one goes on when all have come, the others do not wait for it
@@ -594,7 +587,9 @@ __device__ __forceinline__ int listed(const Shared &sh) {
 // there is none.
 struct Near {
     uint32_t key[kOwn], idx[kOwn];
+    int own;  // tokens of a thread, at most
     __device__ __forceinline__ void load(const Shared &sh, int total) {
+        own = (total + kThreads - 1) / kThreads;
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
             const int i = threadIdx.x + j * kThreads;
@@ -604,91 +599,172 @@ struct Near {
     }
 };
 
+// A digit's histogram of a list: tokens, and their weight in two words of 15
+// bits and the rest.  Up to seven digits (a key's and an index's) lie over the
+// histograms of the row.
+constexpr uint32_t kDigit = 3 * 256;
+constexpr int kMostDigits = 7;
+static_assert(kMostDigits * kDigit <= 3 * kBins, "layout");
+
+// Where a list's running weight, from the largest value down, reaches
+// `target`: the value, the weight before it, its tokens and their weight.
+struct Place {
+    uint32_t value, count;
+    unsigned long long before, weight;
+    bool reached;
+};
+
+// Finds it by digits of eight bits from bit `top` down to bit `low`, among the
+// tokens that take part; `hist` is the first of the cleared histograms, and
+// moves on.
+template <bool MASS, typename Value, typename On>
+__device__ __forceinline__ Place by_digits(const Shared &sh, int own, const uint32_t (&weight)[kOwn], Value &&value,
+                                           On &&on, int top, int low, unsigned long long target, uint32_t &hist) {
+    const int lane = threadIdx.x % 32;
+    Place p{0, 0, 0, 0, true};
+#pragma unroll 1
+    for (int hi = top + 1; hi > low;) {
+        const int lo = max(hi - 8, low);
+        const uint32_t digits = (1u << (hi - lo)) - 1;
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (j < own && on(j)) {
+                const uint32_t v = value(j);
+                if (hi > top || v >> hi == p.value >> hi) {
+                    const uint32_t at = hist + (v >> lo & digits);
+                    sh.add_only(at, 1);
+                    if (MASS) {
+                        sh.add_only(at + 256, weight[j] & 0x7fffu);
+                        sh.add_only(at + 512, weight[j] >> 15);
+                    }
+                }
+            }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            uint32_t c[8];
+            unsigned long long w[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t at = hist + 255 - (lane * 8 + i);
+                c[i] = sh.get(at);
+                w[i] = MASS ? sh.get(at + 256) + ((unsigned long long)sh.get(at + 512) << 15) : c[i];
+                sum += w[i];
+            }
+            unsigned long long run = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long v = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += v;
+            }
+            const bool none = p.before + __shfl_sync(0xffffffffu, run, 31) < target;
+            if (none && lane == 0) sh.put(kFoundBin, 0xffffffffu);
+            run += p.before - sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (run < target && run + w[i] >= target) {
+                    sh.put(kFoundBin, 255 - (lane * 8 + i));
+                    sh.put(kFoundMassLo, (uint32_t)run);
+                    sh.put(kFoundMassHi, (uint32_t)(run >> 32));
+                    sh.put(kFoundN, c[i]);
+                    sh.put(kFoundWLo, (uint32_t)w[i]);
+                    sh.put(kFoundWHi, (uint32_t)(w[i] >> 32));
+                }
+                run += w[i];
+            }
+        }
+        __syncthreads();
+        const uint32_t digit = sh.get(kFoundBin);
+        if (digit == 0xffffffffu) {
+            p.reached = false;
+            break;
+        }
+        p.value |= digit << lo;
+        p.before = join64(sh.get(kFoundMassLo), sh.get(kFoundMassHi));
+        p.count = sh.get(kFoundN);
+        p.weight = join64(sh.get(kFoundWLo), sh.get(kFoundWHi));
+        hist += kDigit;
+        hi = lo;
+        __syncthreads();
+    }
+    return p;
+}
+
 // The cut in a list: the first token, in the order (l descending, index
-// ascending), at which the running weight reaches `target`, and with it all
-// before; the last token if the weights do not reach it.  LOW: the key's bits
-// below it say nothing (16-bit logits).  MASS: weights of at most 2^30 (else
-// every token weighs one).  Counters lie over the histogram.
-template <bool MASS, int LOW>
-__device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, int total,
-                                        const uint32_t (&weight)[kOwn], unsigned long long target, int64_t V) {
-    const int own = (total + kThreads - 1) / kThreads;  // tokens of a thread, at most
-    uint32_t slot = kCount;
+// ascending), at which the running weight reaches a target (1 or more), and
+// with it all before; the last token if the weights do not reach it.  LOW: the
+// key's bits below it say nothing (16-bit logits).  A token's weight is one,
+// or (MASS) its e in units of 2^-30 of the largest of the list; target_of(all,
+// unit) is in those too, given (with SUM) the sum of all and the unit.
+template <bool MASS, bool SUM, int LOW, typename Mass, typename Target>
+__device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, Mass &&mass, Target &&target_of,
+                                        int64_t V) {
     __syncthreads();
-    if (threadIdx.x < 128) sh.put(kCount + threadIdx.x, threadIdx.x == 1 ? 0xffffffffu : 0);
+    for (int i = threadIdx.x; i < kMostDigits * (int)kDigit; i += kThreads) sh.put(kCount + i, 0);
+    // the largest and the least key: their common high bits need no digits
+    if (threadIdx.x == 0) {
+        sh.put(kRed, 0);
+        sh.put(kRed + 1, 0xffffffffu);
+        sh.put(kRed + 2, 0);
+        sh.put(kRed + 3, 0);
+    }
     __syncthreads();
-    // the range of the keys: its common high bits need no rounds
     uint32_t most = 0, least = 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j)
-        if (near.key[j]) {
+        if (j < near.own && near.key[j]) {
             most = max(most, near.key[j]);
             least = min(least, near.key[j]);
         }
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
     if (threadIdx.x % 32 == 0) {
-        sh.max_only(slot, most);
-        sh.min_only(slot + 1, least);
+        sh.max_only(kRed, most);
+        sh.min_only(kRed + 1, least);
     }
     __syncthreads();
-    most = sh.get(slot);
-    least = sh.get(slot + 1);
-    slot += 2;
-    auto number = [&](auto &&counts) {  // of the tokens that count
-        int v = __syncthreads_count(near.key[0] && counts(0));
+    most = sh.get(kRed);
+    least = sh.get(kRed + 1);
+    uint32_t weight[kOwn];
+    const float largest = MASS ? fmaxf(mass(from_order_bits(most)), FLT_MIN) : 1.f;
 #pragma unroll
-        for (int j = 1; j < kOwn; ++j)
-            if (j < own) v += __syncthreads_count(near.key[j] && counts(j));
-        return (uint32_t)v;
-    };
-    auto sum = [&](auto &&counts) -> unsigned long long {  // of their weights
-        if constexpr (!MASS) return number(counts);
-        unsigned long long v = 0;
+    for (int j = 0; j < kOwn; ++j)
+        weight[j] = !MASS ? 1
+                    : j < near.own && near.key[j]
+                        ? __float2uint_rn(mass(from_order_bits(near.key[j])) / largest * 0x1p30f)
+                        : 0;
+    unsigned long long all = 0;
+    if constexpr (SUM) {
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
-            if (j < own && near.key[j] && counts(j)) v += weight[j];
-        const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7fffu);
-        const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 15));
+            if (j < near.own) all += weight[j];
+        const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)all & 0x7fffu);
+        const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(all >> 15));
         if (threadIdx.x % 32 == 0) {
-            sh.add_only(slot, lo);
-            sh.add_only(slot + 1, hi);
+            sh.add_only(kRed + 2, lo);
+            sh.add_only(kRed + 3, hi);
         }
         __syncthreads();
-        v = sh.get(slot) + ((unsigned long long)sh.get(slot + 1) << 15);
-        slot += 2;
-        return v;
-    };
-    const unsigned long long all = sum([](int) { return true; });
-    if (all < target) return Cut{from_order_bits(least), 0xffffffffu};
-    uint32_t at = least;
-    if (most != least) {
-        const int top = 31 - __clz(most ^ least);
-        at = top == 31 ? 0 : most >> (top + 1) << (top + 1);
-#pragma unroll 1
-        for (int bit = top; bit >= LOW; --bit) {
-            const uint32_t t = at | (1u << bit);
-            if (sum([&](int j) { return near.key[j] >= t; }) >= target) at = t;
-        }
+        all = sh.get(kRed + 2) + ((unsigned long long)sh.get(kRed + 3) << 15);
     }
-    auto equal = [&](int j) { return near.key[j] >> LOW == at >> LOW; };
-    const unsigned long long before = sum([&](int j) { return near.key[j] >> LOW > at >> LOW; });
-    const uint32_t n_eq = number(equal);
-    unsigned long long want = target - before;
-    if (MASS) {
-        const unsigned long long each = sum(equal) / n_eq;  // (equal logits have equal weights)
-        want = each > 0 ? (want + each - 1) / each : 1;
-    }
+    const unsigned long long target = target_of(all, 0x1p30 / (double)largest);
+    uint32_t hist = kCount;
+    const int top = max(LOW, 31 - __clz(most ^ least | 1));
+    const uint32_t low_bits = top == 31 ? 0xffffffffu : (2u << top) - 1;
+    const Place p = by_digits<MASS>(
+        sh, near.own, weight, [&](int j) { return near.key[j] & low_bits; }, [&](int j) { return near.key[j] != 0; },
+        top, LOW, target, hist);
+    if (!p.reached) return Cut{from_order_bits(least), 0xffffffffu};
+    const uint32_t key = (most & ~low_bits) | p.value;
     // 16-bit logits have equal low bits of the key: ones below 0
-    const float l = from_order_bits(LOW > 0 && at >> 31 == 0 ? at | ((1u << LOW) - 1) : at);
-    if (want >= n_eq) return Cut{l, 0xffffffffu};
-    uint32_t end = 0;  // index of the want-th
-#pragma unroll 1
-    for (int bit = 31 - __clz((uint32_t)V); bit >= 0; --bit) {
-        const uint32_t t = end | (1u << bit);
-        if (number([&](int j) { return equal(j) && near.idx[j] < t; }) < want) end = t;
-    }
-    return Cut{l, end + 1};
+    const float l = from_order_bits(LOW > 0 && key >> 31 == 0 ? key | ((1u << LOW) - 1) : key);
+    if (p.count == 1 || p.before + p.weight <= target) return Cut{l, 0xffffffffu};
+    // among equal logits: the index, from the lowest up
+    const int bits = 31 - __clz((uint32_t)V);
+    const uint32_t all_ones = (2u << bits) - 1;
+    const Place q = by_digits<MASS>(
+        sh, near.own, weight, [&](int j) { return all_ones - near.idx[j]; },
+        [&](int j) { return near.key[j] && near.key[j] >> LOW == key >> LOW; }, bits, 0, target - p.before, hist);
+    return Cut{l, q.reached ? all_ones - q.value + 1 : 0xffffffffu};
 }
 
 // The cut at which the running count of tokens reaches `k`, or the running
@@ -831,23 +907,14 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         if (total > 0) {
             Near near;
             near.load(sh, total);
-            uint32_t weight[kOwn];
-            unsigned long long want;
-            if (MASS) {
-                // weights in units of 2^-30 of the bracket's largest mass
-                const float most = mass(mx - ((float)b0 - 0.5f) / scale);
-                const float unit = 0x1p30f / fmaxf(most, FLT_MIN);
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j)
-                    weight[j] = min(__float2uint_rn(mass(from_order_bits(near.key[j])) * unit), 1u << 30);
-                const double left = (target - (double)sh.sum_ctas(kPartAbove)) * (double)unit;
-                want = left > 1 ? __double2ull_ru(left) : 1;
-            } else {
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) weight[j] = 1;
-                want = k - above_count;
-            }
-            c = cut_near<MASS, LOW>(sh, near, total, weight, want, V);
+            const double left = MASS ? target - (double)sh.sum_ctas(kPartAbove) : 0.0;
+            c = cut_near<MASS, false, LOW>(
+                sh, near, mass,
+                [&](unsigned long long, double unit) -> unsigned long long {
+                    if (!MASS) return k - above_count;
+                    return left * unit > 1 ? __double2ull_ru(left * unit) : 1;
+                },
+                V);
         }
         if ((int)threadIdx.x < sh.cs) {
             sh.put(kCutL, (int)threadIdx.x, __float_as_uint(c.l));
@@ -1112,23 +1179,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (rank == 0) {
                 Near near;
                 near.load(sh, total);
-                uint32_t weight[kOwn];
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) weight[j] = 1;
-                cut = cut_near<false, LOW>(sh, near, total, weight, (unsigned long long)top_k, a.V);
+                cut = cut_near<false, false, LOW>(
+                    sh, near, fast_e, [&](unsigned long long, double) { return (unsigned long long)top_k; }, a.V);
                 if (use_p) {
-                    unsigned long long own = 0;
 #pragma unroll
-                    for (int j = 0; j < kOwn; ++j) {
-                        const float l = from_order_bits(near.key[j]);
-                        if (near.key[j] && !cut.keeps(l, near.idx[j])) near.key[j] = 0;
-                        weight[j] = near.key[j] ? __float2uint_rn(fast_e(l) * 0x1p30f) : 0;
-                        own += weight[j];
-                    }
-                    const uint32_t lo = sh.block_add(kCount + 126, (uint32_t)own & 0x7fffu);
-                    const uint32_t hi = sh.block_add(kCount + 127, (uint32_t)(own >> 15));
-                    const double zk = (double)(lo + ((unsigned long long)hi << 15));
-                    cut = cut_near<true, LOW>(sh, near, total, weight, __double2ull_ru((double)top_p * zk), a.V);
+                    for (int j = 0; j < kOwn; ++j)
+                        if (near.key[j] && !cut.keeps(from_order_bits(near.key[j]), near.idx[j])) near.key[j] = 0;
+                    cut = cut_near<true, true, LOW>(
+                        sh, near, fast_e,
+                        [&](unsigned long long all, double) { return __double2ull_ru((double)top_p * (double)all); }, a.V);
                 }
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
