@@ -92,43 +92,55 @@ __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 4 : 2) conv_kernel(cons
         for (int j = 0; j < W - 1; ++j) store_raw<T, VEC>(so + j * a.C, next[j]);
     }
     if (!a.y) return;
-    T *y = static_cast<T *>(a.y) + (b * a.T) * a.C + c;
     // the next batch of steps is on its way while one is worked on
+    int left = (int)(t1 - t0);
+    if (left <= 0) return;
+    const T *px = x + t0 * a.x_st;
+    T *py = static_cast<T *>(a.y) + (b * a.T + t0) * a.C + c;
     RawPiece<T, VEC> raw[BATCH];
-    auto fetch = [&](int64_t t) {
+    auto fetch = [&](int n) {
+        if (n >= BATCH) {
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k)
-            if (t + k < t1) raw[k] = load_raw<T, VEC>(x + (t + k) * a.x_st);
+            for (int k = 0; k < BATCH; ++k) raw[k] = load_raw<T, VEC>(px + k * a.x_st);
+        } else {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k)
+                if (k < n) raw[k] = load_raw<T, VEC>(px + k * a.x_st);
+        }
+        px += BATCH * a.x_st;
     };
-    fetch(t0);
-    for (int64_t t = t0; t < t1; t += BATCH) {
+    auto step = [&](const RawPiece<T, VEC> &now) {
+        float2 in[NP], out[NP];
+        widen2<T, VEC>(in, now);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            float2 s = bias[i];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) s = ffma2(w[j][i], win[j][i], s);
+            s = ffma2(w[W - 1][i], in[i], s);
+            out[i] = a.silu ? silu2(s) : s;
+        }
+        store_piece2<T, VEC>(py, out);
+        py += a.C;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+#pragma unroll
+            for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
+            win[W - 2][i] = in[i];
+        }
+    };
+    fetch(left);
+    for (; left >= BATCH; left -= BATCH) {
         RawPiece<T, VEC> now[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) now[k] = raw[k];
-        fetch(t + BATCH);
+        fetch(left - BATCH);
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) {
-            if (t + k < t1) {
-                float2 in[NP], out[NP];
-                widen2<T, VEC>(in, now[k]);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    float2 s = bias[i];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) s = ffma2(w[j][i], win[j][i], s);
-                    s = ffma2(w[W - 1][i], in[i], s);
-                    out[i] = a.silu ? silu2(s) : s;
-                }
-                store_piece2<T, VEC>(y + (t + k) * a.C, out);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-#pragma unroll
-                    for (int j = 0; j < W - 2; ++j) win[j][i] = win[j + 1][i];
-                    win[W - 2][i] = in[i];
-                }
-            }
-        }
+        for (int k = 0; k < BATCH; ++k) step(now[k]);
     }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+        if (k < left) step(raw[k]);
 }
 
 template <typename T, int VEC, int W>

@@ -37,6 +37,7 @@ struct ScanArgs {
     int64_t x_sb, x_st, dt_sb, dt_st, b_sb, b_st, c_sb, c_st;
     int N;
     bool softplus;
+    bool vec_bc;                        // B and C rows can be read in 16-byte pieces
     bool chunked;                       // the tensor-core form (scan_chunk.cu)
     int segments;                       // parts that the steps are split into
     int64_t seg_steps;                  // steps per part (the last may be shorter)

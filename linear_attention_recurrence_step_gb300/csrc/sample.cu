@@ -956,6 +956,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const float to_log2 = 1.44269504088896341f / temp;
     auto e_below = [&](float l, float top) { return ex2((l - top) * to_log2); };
 
+    if (!only_first && !use_k && !use_p && !use_m) {
+        // all of the noise will be wanted: on its way to L2 with the logits
+        const float *nb = noise + base;
+        for (int i = (int)threadIdx.x * 32; i < n; i += kThreads * 32)
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(nb + i));
+    }
+
     // the slice into shared memory, with each thread's maximum and mass
     Row<T, CACHED> row;
     row.n = n;
@@ -988,24 +995,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const int first = row.mis > 0, end = (row.mis + n) / VE, all = row.count();
         const T *at = src - row.mis;
         constexpr int AHEAD = 4;  // pieces of a thread in flight
-        int j = first + (int)threadIdx.x;
-        for (; j + (AHEAD - 1) * kThreads < end; j += AHEAD * kThreads) {
+        for (int j = first + (int)threadIdx.x; j < end; j += AHEAD * kThreads) {
             RawPiece<T, VE> raw[AHEAD];
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) raw[u].w = row_piece(at + (int64_t)(j + u * kThreads) * VE);
+            for (int u = 0; u < AHEAD; ++u)
+                if (j + u * kThreads < end) raw[u].w = row_piece(at + (int64_t)(j + u * kThreads) * VE);
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const uint4 w = clean(raw[u]);
-                put_piece(row.pieces + 16 * (j + u * kThreads), w);
-                take(w);
-            }
-        }
-        for (; j < end; j += kThreads) {
-            RawPiece<T, VE> raw;
-            raw.w = row_piece(at + (int64_t)j * VE);
-            const uint4 w = clean(raw);
-            put_piece(row.pieces + 16 * j, w);
-            take(w);
+            for (int u = 0; u < AHEAD; ++u)
+                if (j + u * kThreads < end) {
+                    const uint4 w = clean(raw[u]);
+                    put_piece(row.pieces + 16 * (j + u * kThreads), w);
+                    take(w);
+                }
         }
         // (one thread per end; a slice within one piece has one)
         const bool head = threadIdx.x == 0 && first && all > 0, tail = threadIdx.x == 1 && end < all && end >= first;

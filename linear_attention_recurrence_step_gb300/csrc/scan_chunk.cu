@@ -65,15 +65,26 @@ __host__ __device__ constexpr size_t chunk_smem(int N, int warps) {
            (y_over_c(N, warps) ? 0 : (size_t)warps * kL * 16 * 2);
 }
 
-__device__ __forceinline__ void stsm_x4_t(void *row, const uint32_t (&r)[4]) {
-    const unsigned a = static_cast<unsigned>(__cvta_generic_to_shared(row));
+// (Shared memory goes by 32-bit addresses here: a generic pointer per ldmatrix
+// costs more instructions than the product it feeds.)
+__device__ __forceinline__ void stsm_x4_t(uint32_t a, const uint32_t (&r)[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
+__device__ __forceinline__ void put_pair(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint4 get_piece(uint32_t a) {
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(a)
+                 : "memory");
+    return w;
+}
 // 16 bytes, or zeros.
-__device__ __forceinline__ void cp_async16_or_zero(void *smem, const void *gmem, bool on) {
-    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t s, const void *gmem, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(s), "l"(gmem), "r"(on ? 16 : 0) : "memory");
 }
 // (x0, x1) ~ hi + mid + lo in packed bf16 pairs: all 24 bits of the f32 values.
@@ -92,14 +103,15 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int XP = x_pitch(warps);
-    const size_t stage = stage_bytes(N, warps);
-    T *const sW = reinterpret_cast<T *>(smem_raw + 2 * stage);          // hi, then lo
-    T *const sWlo = sW + kL * kWPitch;
-    ChunkDecay *const sdec = reinterpret_cast<ChunkDecay *>(smem_raw + 2 * stage + 2 * kL * kWPitch * 2);
-    T *const sYown = reinterpret_cast<T *>(sdec + 2);
-    auto sx = [&](int b) { return reinterpret_cast<T *>(smem_raw + b * stage); };
-    auto sB = [&](int b) { return sx(b) + kL * XP; };
-    auto sC = [&](int b) { return sB(b) + kL * BP; };
+    const uint32_t stage = (uint32_t)stage_bytes(N, warps);
+    const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+    const uint32_t sW = smem + 2 * stage;                               // hi, then lo
+    constexpr uint32_t kWBytes = kL * kWPitch * 2;
+    ChunkDecay *const sdec = reinterpret_cast<ChunkDecay *>(smem_raw + 2 * stage + 2 * kWBytes);
+    const uint32_t sYown = sW + 2 * kWBytes + 2 * (uint32_t)sizeof(ChunkDecay);
+    auto sx = [&](int b) { return smem + b * stage; };
+    auto sB = [&](int b) { return sx(b) + kL * XP * 2; };
+    auto sC = [&](int b) { return sB(b) + kL * BP * 2; };
     pdl_trigger();
     pdl_wait();
 
@@ -141,14 +153,14 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
 #pragma unroll
             for (int i = 0; i < kL / 16; ++i) {
                 const bool on = q < rows && t + 16 * i < n;
-                cp_async16_or_zero(sx(buf) + (t + 16 * i) * XP + q, on ? src + 16 * i * a.x_st : x, on);
+                cp_async16_or_zero(sx(buf) + ((t + 16 * i) * XP + q) * 2, on ? src + 16 * i * a.x_st : x, on);
             }
         }
         for (int i = threadIdx.x; i < kL * (N / 8); i += blockDim.x) {
             const int t = i / (N / 8), q = i % (N / 8);
             const bool on = t < n;
-            cp_async16_or_zero(sB(buf) + t * BP + q * 8, on ? Bp + (t0 + t) * a.b_st + q * 8 : Bp, on);
-            if (OUT) cp_async16_or_zero(sC(buf) + t * BP + q * 8, on ? Cp + (t0 + t) * a.c_st + q * 8 : Cp, on);
+            cp_async16_or_zero(sB(buf) + (t * BP + q * 8) * 2, on ? Bp + (t0 + t) * a.b_st + q * 8 : Bp, on);
+            if (OUT) cp_async16_or_zero(sC(buf) + (t * BP + q * 8) * 2, on ? Cp + (t0 + t) * a.c_st + q * 8 : Cp, on);
         }
         cp_async_commit();
     };
@@ -217,20 +229,28 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
             if (warp == (c + 1) % warps) decays(c + 1);
         }
         const ChunkDecay &d = sdec[buf];
-        const T *xs = sx(buf), *Bs = sB(buf), *Cs = sC(buf);
+        // where this lane's ldmatrix rows start: plain tiles of B and C (rows
+        // across matrices 0-1 or 2-3), and transposed ones of x and B
+        const uint32_t Bs = sB(buf), Cs = sC(buf);
+        const uint32_t c_rows = Cs + ((lr + 8 * (lm & 1)) * BP + 8 * (lm >> 1)) * 2;   // left operand
+        const uint32_t c_cols = Cs + ((lr + 8 * (lm >> 1)) * BP + 8 * (lm & 1)) * 2;   // right operand
+        const uint32_t w_cols = sW + ((lr + 8 * (lm >> 1)) * kWPitch + 8 * (lm & 1)) * 2;
+        const uint32_t x_t = sx(buf) + ((lr + 8 * (lm >> 1)) * XP + warp * 16 + 8 * (lm & 1)) * 2;
+        const uint32_t b_t = Bs + ((lr + 8 * (lm & 1)) * BP + 8 * (lm >> 1)) * 2;
         float Y[kL / 8][4];
         if constexpr (OUT) {
             // W by tiles of 16 rows t and 8 columns s, those below the diagonal
             for (int job = warp; job < 6; job += warps) {
                 const int ti = job < 4 ? 1 : 0, sb = job < 4 ? job : job - 4;
                 float G[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint32_t b_row = Bs + ((sb * 8 + lr) * BP + 8 * lm) * 2, c_row = c_rows + ti * 16 * BP * 2;
 #pragma unroll
                 for (int kk = 0; kk < N / 16; kk += 2) {
                     uint32_t ca[4], bb[4];
-                    ldsm_x4(bb, Bs + (sb * 8 + lr) * BP + kk * 16 + 8 * lm);
-                    ldsm_x4(ca, Cs + (ti * 16 + lr + 8 * (lm & 1)) * BP + kk * 16 + 8 * (lm >> 1));
+                    ldsm_x4_a(bb, b_row + kk * 32);
+                    ldsm_x4_a(ca, c_row + kk * 32);
                     mma_bf16_16816(G, ca, bb[0], bb[1]);
-                    ldsm_x4(ca, Cs + (ti * 16 + lr + 8 * (lm & 1)) * BP + kk * 16 + 16 + 8 * (lm >> 1));
+                    ldsm_x4_a(ca, c_row + kk * 32 + 32);
                     mma_bf16_16816(G, ca, bb[2], bb[3]);
                 }
                 const int t0 = ti * 16 + gr, s0 = sb * 8 + tq * 2;
@@ -247,8 +267,8 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
                     const float2 ct = d.c[t];
                     uint32_t hi, lo;
                     split_bf16x2(wt(G[2 * r], ct, cs0, dl0, t, s0), wt(G[2 * r + 1], ct, cs1, dl1, t, s0 + 1), hi, lo);
-                    *reinterpret_cast<uint32_t *>(sW + t * kWPitch + s0) = hi;
-                    *reinterpret_cast<uint32_t *>(sWlo + t * kWPitch + s0) = lo;
+                    put_pair(sW + (t * kWPitch + s0) * 2, hi);
+                    put_pair(sW + kWBytes + (t * kWPitch + s0) * 2, lo);
                 }
             }
             // S C^T: the state's accumulators are the left operand
@@ -266,7 +286,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
 #pragma unroll
                 for (int j = 0; j < kL / 8; j += 2) {
                     uint32_t cb[4];
-                    ldsm_x4(cb, Cs + ((j + (lm >> 1)) * 8 + lr) * BP + kk * 16 + 8 * (lm & 1));
+                    ldsm_x4_a(cb, c_cols + (j * 8 * BP + kk * 16) * 2);
                     mma_bf16_16816(Y[j], hi, cb[0], cb[1]);
                     mma_bf16_16816(Y[j + 1], hi, cb[2], cb[3]);
                     mma_bf16_16816(Y[j], lo, cb[0], cb[1]);
@@ -295,15 +315,15 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         for (int ks = 0; ks < kL / 16; ++ks) {
             // x^T, rows p of this warp, 16 steps
             uint32_t xa[4];
-            ldsm_x4_t(xa, xs + (ks * 16 + lr + 8 * (lm >> 1)) * XP + warp * 16 + 8 * (lm & 1));
+            ldsm_x4_t_a(xa, x_t + ks * 16 * XP * 2);
             if constexpr (OUT) {
 #pragma unroll
                 for (int j = 2 * ks; j < kL / 8; j += 2) {
                     uint32_t wb[4];
-                    ldsm_x4(wb, sW + ((j + (lm >> 1)) * 8 + lr) * kWPitch + ks * 16 + 8 * (lm & 1));
+                    ldsm_x4_a(wb, w_cols + (j * 8 * kWPitch + ks * 16) * 2);
                     mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
                     mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
-                    ldsm_x4(wb, sWlo + ((j + (lm >> 1)) * 8 + lr) * kWPitch + ks * 16 + 8 * (lm & 1));
+                    ldsm_x4_a(wb, w_cols + kWBytes + (j * 8 * kWPitch + ks * 16) * 2);
                     mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
                     mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
                 }
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
 #pragma unroll
             for (int j = 0; j < NT; j += 2) {
                 uint32_t bb[4];
-                ldsm_x4_t(bb, Bs + (ks * 16 + lr + 8 * (lm & 1)) * BP + (j + (lm >> 1)) * 8);
+                ldsm_x4_t_a(bb, b_t + (ks * 16 * BP + j * 8) * 2);
                 if (TERMS == 3) {
                     mma_bf16_16816(S[j], lo, bb[0], bb[1]);
                     mma_bf16_16816(S[j + 1], lo, bb[2], bb[3]);
@@ -335,7 +355,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         if constexpr (OUT) {
             // y: the warp's 16 rows turned into 64 rows of 16 (32 bytes; the two
             // 16-byte halves swap places every fourth row against bank conflicts)
-            T *ys = (y_over_c(N, warps) ? sC(buf) : sYown) + warp * kL * 16;
+            const uint32_t ys = (y_over_c(N, warps) ? Cs : sYown) + warp * kL * 32;
 #pragma unroll
             for (int j = 0; j < kL / 8; j += 2) {
                 uint32_t r[4];
@@ -344,7 +364,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
                 r[2] = pack2<T>(Y[j + 1][0], Y[j + 1][1]);
                 r[3] = pack2<T>(Y[j + 1][2], Y[j + 1][3]);
                 const int t = (j + (lm >> 1)) * 8 + lr;
-                stsm_x4_t(ys + t * 16 + (((lm & 1) ^ ((t >> 2) & 1)) * 8), r);
+                stsm_x4_t(ys + t * 32 + ((lm & 1) ^ ((t >> 2) & 1)) * 16, r);
             }
             __syncwarp();
             const int64_t t0 = t_begin + (int64_t)c * kL;
@@ -356,7 +376,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
                 const int t = i * 16 + (lane >> 1);
                 if (t < n && warp * 16 + q * 8 < rows)
                     *reinterpret_cast<uint4 *>(y + (int64_t)t * a.H * a.P) =
-                        *reinterpret_cast<const uint4 *>(ys + t * 16 + ((q ^ ((t >> 2) & 1)) * 8));
+                        get_piece(ys + t * 32 + (q ^ ((t >> 2) & 1)) * 16);
             }
         }
     }

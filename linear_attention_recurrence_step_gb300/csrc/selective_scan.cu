@@ -23,19 +23,23 @@ namespace {
 constexpr int kStage = 16;      // steps staged in shared memory at a time
 constexpr int kScanWarps = 4;   // most warps per CTA
 
-template <int N> struct ScanShape {
+// SHORT (2 to 16 steps): half of the rows per lane, for more CTAs per SM while
+// a CTA waits for its step's sums (16 sequences of 8 steps, 64 heads of 64 x
+// 128: 19.5 us, 23.3 us without); one step alone has no such wait and is
+// better off with the larger tile (32 sequences: 25.8 us, 26.5 us).
+template <int N, bool SHORT> struct ScanShape {
     static constexpr int LR = N >= 32 ? 8 : 4;        // lanes per row
     static constexpr int VPL = N / LR;                // entries per lane and row
-    static constexpr int RPL = N >= 256 ? 2 : 4;      // rows per lane
+    static constexpr int RPL = (N >= 256 ? 2 : 4) / (SHORT && N >= 128 ? 2 : 1);  // rows per lane
     static constexpr int RW = 32 / LR;                // rows side by side in a warp
     static constexpr int kWarpRows = RW * RPL;
 };
 
 // workspace: end states [segments][B][H][P][N], then decays [segments][B][H]
-template <typename T, int N, int phase>
+template <typename T, int N, int phase, bool SHORT>
 __global__ void __launch_bounds__(kScanWarps * 32)
 scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
-    using S = ScanShape<N>;
+    using S = ScanShape<N, SHORT>;
     constexpr int LR = S::LR, VPL = S::VPL, RPL = S::RPL, RW = S::RW, WR = S::kWarpRows;
     constexpr int NV4 = VPL / 4;  // float4 groups per lane and row: entries j*4*LR + lane*4
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -110,10 +114,30 @@ scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
     for (int64_t t0 = t_begin; t0 < t_end; t0 += kStage) {
         const int n = (int)(t_end - t0 < kStage ? t_end - t0 : kStage);
         __syncthreads();
-        for (int i = threadIdx.x; i < n * N; i += blockDim.x) {
-            const int t = i / N, c = i % N;
-            sB[i] = ld_f32(Bp + (t0 + t) * a.b_st + c);
-            if (out) sC[i] = ld_f32(Cp + (t0 + t) * a.c_st + c);
+        if (a.vec_bc) {
+            constexpr int VE = 16 / sizeof(T), PR = N / VE;  // pieces of a row
+            for (int i = threadIdx.x; i < n * PR; i += blockDim.x) {
+                const int t = i / PR, c = i % PR * VE;
+                const RawPiece<T, VE> rB = load_raw<T, VE>(Bp + (t0 + t) * a.b_st + c);
+                float v[VE];
+                if (out) {
+                    const RawPiece<T, VE> rC = load_raw<T, VE>(Cp + (t0 + t) * a.c_st + c);
+                    widen<T, VE>(v, rC);
+#pragma unroll
+                    for (int e = 0; e < VE; e += 4)
+                        *reinterpret_cast<float4 *>(sC + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+                widen<T, VE>(v, rB);
+#pragma unroll
+                for (int e = 0; e < VE; e += 4)
+                    *reinterpret_cast<float4 *>(sB + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+        } else {
+            for (int i = threadIdx.x; i < n * N; i += blockDim.x) {
+                const int t = i / N, c = i % N;
+                sB[i] = ld_f32(Bp + (t0 + t) * a.b_st + c);
+                if (out) sC[i] = ld_f32(Cp + (t0 + t) * a.c_st + c);
+            }
         }
         for (int i = threadIdx.x; i < n * rows_cta; i += blockDim.x) {
             const int t = i / rows_cta, p = i % rows_cta;
@@ -229,27 +253,31 @@ __global__ void __launch_bounds__(256) scan_join_kernel(float *ws, float *state_
     if (state_out) *reinterpret_cast<float4 *>(state_out + i) = v;
 }
 
-template <int N> int64_t scan_warps(int64_t P, int64_t *row_blocks) {
-    const int64_t w = (P + ScanShape<N>::kWarpRows - 1) / ScanShape<N>::kWarpRows;
+template <int N, bool SHORT> int64_t scan_warps(int64_t P, int64_t *row_blocks) {
+    constexpr int WR = ScanShape<N, SHORT>::kWarpRows;
+    const int64_t w = (P + WR - 1) / WR;
     *row_blocks = (w + kScanWarps - 1) / kScanWarps;
     return (w + *row_blocks - 1) / *row_blocks;
 }
 
+template <typename T, int N, int PHASE, bool SHORT>
+cudaError_t launch_phase(const ScanArgs &a, cudaStream_t s) {
+    int64_t row_blocks;
+    const int warps = (int)scan_warps<N, SHORT>(a.P, &row_blocks);
+    const size_t smem = (size_t)kStage * (2 * N + warps * ScanShape<N, SHORT>::kWarpRows + 2) * 4;
+    const int64_t ctas = a.B * a.H * row_blocks * a.segments;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_dependent(scan_step_kernel<T, N, PHASE, SHORT>, (unsigned)ctas, warps * 32, smem, s, a, row_blocks);
+}
+
 template <typename T, int N>
 cudaError_t launch_n(const ScanArgs &a, cudaStream_t s) {
-    int64_t row_blocks;
-    const int warps = (int)scan_warps<N>(a.P, &row_blocks);
-    const size_t smem = (size_t)kStage * (2 * N + warps * ScanShape<N>::kWarpRows + 2) * 4;
-    const int64_t tiles = a.B * a.H * row_blocks;
-    if (tiles * a.segments > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (a.segments == 1)
-        return launch_dependent(scan_step_kernel<T, N, kScanWhole>, (unsigned)tiles, warps * 32, smem, s, a, row_blocks);
-    cudaError_t e = launch_dependent(scan_step_kernel<T, N, kScanFold>, (unsigned)(tiles * a.segments), warps * 32, smem,
-                                     s, a, row_blocks);
+        return a.T > 1 && a.T <= kStage ? launch_phase<T, N, kScanWhole, true>(a, s) : launch_phase<T, N, kScanWhole, false>(a, s);
+    cudaError_t e = launch_phase<T, N, kScanFold, false>(a, s);
     if (e == cudaSuccess) e = launch_scan_join(a, s);
     if (e != cudaSuccess || !a.y) return e;
-    return launch_dependent(scan_step_kernel<T, N, kScanOutput>, (unsigned)(tiles * a.segments), warps * 32, smem, s, a,
-                            row_blocks);
+    return launch_phase<T, N, kScanOutput, false>(a, s);
 }
 
 template <typename T>
@@ -289,14 +317,14 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
         // sixteen warps per SM
         target = 152.0 * (16 / scan_chunk_warps(P, &row_blocks));
         least = 256;
-        unit = 64;
+        unit = 32;
     } else {
         switch (N) {
-        case 16: scan_warps<16>(P, &row_blocks); break;
-        case 32: scan_warps<32>(P, &row_blocks); break;
-        case 64: scan_warps<64>(P, &row_blocks); break;
-        case 128: scan_warps<128>(P, &row_blocks); break;
-        case 256: scan_warps<256>(P, &row_blocks); break;
+        case 16: scan_warps<16, false>(P, &row_blocks); break;
+        case 32: scan_warps<32, false>(P, &row_blocks); break;
+        case 64: scan_warps<64, false>(P, &row_blocks); break;
+        case 128: scan_warps<128, false>(P, &row_blocks); break;
+        case 256: scan_warps<256, false>(P, &row_blocks); break;
         }
     }
     const double ctas = (double)B * (double)H * (double)row_blocks;
