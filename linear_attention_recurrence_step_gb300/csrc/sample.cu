@@ -80,8 +80,9 @@ constexpr uint32_t kPartMax = kWords, kPartZ = kWords + 1, kPartLeast = kWords +
                    kPartAbove = kWords + 4, kListN = kWords + 5, kTies = kWords + 6, kFoundBin = kWords + 9, kFoundLast = kWords + 10, kFoundCount = kWords + 11,
                    kFoundN = kWords + 12, kFoundMassLo = kWords + 13, kFoundMassHi = kWords + 14,
                    kFoundWLo = kWords + 15, kFoundWHi = kWords + 16, kLimit = kWords + 17, kCutL = kWords + 18,
-                   kCutEnd = kWords + 19, kRace = kWords + 20, kNearN = kWords + 21, kNearAt = kWords + 22;
-constexpr uint32_t kSharedBytes = (kWords + 24) * 4;
+                   kCutEnd = kWords + 19, kRace = kWords + 20, kNearN = kWords + 21, kNearAt = kWords + 22, kPartIn = kWords + 23,
+                   kTightBin = kWords + 24, kTightLast = kWords + 25;
+constexpr uint32_t kSharedBytes = (kWords + 28) * 4;
 static_assert(kCountBins <= kHi && 2 * kList <= kBins && kSharedBytes % 16 == 0, "layout");
 
 // Word accesses at a CTA's own shared memory, and at that of another CTA of
@@ -794,6 +795,8 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     if (threadIdx.x == 0) {
         sh.put(kFoundBin, kCountBins - 1);
         sh.put(kFoundLast, kCountBins - 1);
+        sh.put(kTightBin, kCountBins - 1);
+        sh.put(kTightLast, kCountBins - 1);
         sh.put(kFoundCount, 0);
         sh.put(kListN, 0);
         sh.put(kNearN, 0);
@@ -846,6 +849,11 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     // counts are exact in f32 up to 2^24; masses have room for the roundings
     const float first = MASS ? (float)target * 0.9999f : (float)k;
     const float last = MASS ? (float)target * 1.0001f * expf(width) : (float)k;
+    // mid-bin masses are a good guess, within a sixth of a bin's width but for
+    // rows whose mass lies in a few tokens: a bracket of about a third of a bin's
+    // width of mass, instead of one of a whole, with the certain one behind it
+    const float middle = MASS ? (float)target * expf(0.5f * width) : 0.f;
+    const float first_tight = middle * (1.f - width / 6.f), last_tight = middle * (1.f + width / 6.f);
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
         const int bin = threadIdx.x * PB + j;
@@ -855,53 +863,73 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
             sh.put(kFoundCount, (uint32_t)run);
         }
         if (run < last && next >= last) sh.put(kFoundLast, bin);
+        if (MASS && run < first_tight && next >= first_tight) sh.put(kTightBin, bin);
+        if (MASS && run < last_tight && next >= last_tight) sh.put(kTightLast, bin);
         run = next;
     }
     __syncthreads();
-    const uint32_t b0 = sh.get(kFoundBin), b1 = sh.get(kFoundLast);
     const uint32_t above_count = sh.get(kFoundCount);
-    float above = 0.f;
-    if constexpr (PIECES) {
-        const float f0 = kMagic + (float)b0, f1 = kMagic + (float)b1;
-        float2 sum2 = make_float2(0.f, 0.f);
-        row.each_piece(low, [&](const auto &v, int i0) {
-            constexpr int VE = sizeof(v) / sizeof(float);
-            uint32_t on = 0;      // bits of the tokens in the bracket
-            bool ahead = false;   // one is above it
+    int total;
+    for (bool tight = MASS;; tight = false) {
+        const uint32_t b0 = sh.get(tight ? kTightBin : kFoundBin), b1 = sh.get(tight ? kTightLast : kFoundLast);
+        float above = 0.f, inside = 0.f;  // masses
+        if constexpr (PIECES) {
+            const float f0 = kMagic + (float)b0, f1 = kMagic + (float)b1;
+            float2 sum2 = make_float2(0.f, 0.f);
+            row.each_piece(low, [&](const auto &v, int i0) {
+                constexpr int VE = sizeof(v) / sizeof(float);
+                uint32_t on = 0;      // bits of the tokens in the bracket
+                bool ahead = false;   // one is above it
 #pragma unroll
-            for (int e = 0; e < VE; e += 2) {
-                const float2 m = in_bins(v[e / 2]);
-                if (MASS) {
-                    const float2 x = mass2(v[e / 2]);
-                    sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? x.x : 0.f, m.y < f0 ? x.y : 0.f));
+                for (int e = 0; e < VE; e += 2) {
+                    const float2 m = in_bins(v[e / 2]);
+                    if (MASS) {
+                        const float2 x = mass2(v[e / 2]);
+                        sum2 = __fadd2_rn(sum2, make_float2(m.x < f0 ? x.x : 0.f, m.y < f0 ? x.y : 0.f));
+                    }
+                    ahead = ahead || m.x < f0 || m.y < f0;
+                    on |= (m.x >= f0 && m.x <= f1 ? 1u << e : 0) | (m.y >= f0 && m.y <= f1 ? 2u << e : 0);
                 }
-                ahead = ahead || m.x < f0 || m.y < f0;
-                on |= (m.x >= f0 && m.x <= f1 ? 1u << e : 0) | (m.y >= f0 && m.y <= f1 ? 2u << e : 0);
+                if (ahead) prefetch(i0);
+                while (on) {
+                    const int e = __ffs(on) - 1;
+                    on &= on - 1;
+                    const float l = row.at(i0 + e);
+                    enlist(sh, l, row.base + (uint32_t)(i0 + e));
+                    if (MASS) inside += mass(l);
+                }
+            });
+            above = sum2.x + sum2.y;
+        } else {
+            row.each(low, [&](float l, uint32_t idx) {
+                const uint32_t bin = clamped(l);
+                if (bin > b1 || !in(l, idx)) return;
+                if (bin >= b0) enlist(sh, l, idx);
+                if (MASS) (bin >= b0 ? inside : above) += mass(l);
+            });
+        }
+        if (MASS) {
+            above = block_sum(above, sh);
+            inside = block_sum(inside, sh);
+            if (threadIdx.x == 0) {
+                sh.putf(kPartAbove, above);
+                sh.putf(kPartIn, inside);
             }
-            if (ahead) prefetch(i0);
-            while (on) {
-                const int e = __ffs(on) - 1;
-                on &= on - 1;
-                enlist(sh, row.at(i0 + e), row.base + (uint32_t)(i0 + e));
-            }
-        });
-        above = sum2.x + sum2.y;
-    } else {
-        row.each(low, [&](float l, uint32_t idx) {
-            const uint32_t bin = clamped(l);
-            if (bin > b1 || !in(l, idx)) return;
-            if (bin >= b0) enlist(sh, l, idx);
-            else if (MASS) above += mass(l);
-        });
+        }
+        send_list(sh);
+        sh.sync();
+        total = listed(sh);
+        if (total < 0) return false;
+        if (!tight) break;
+        const float all_above = sh.sum_ctas(kPartAbove);
+        if (all_above < (float)target && all_above + sh.sum_ctas(kPartIn) >= (float)target) break;
+        sh.sync();
+        if (threadIdx.x == 0) {
+            sh.put(kListN, 0);
+            sh.put(kNearN, 0);
+        }
+        sh.sync();
     }
-    if (MASS) {
-        above = block_sum(above, sh);
-        if (threadIdx.x == 0) sh.putf(kPartAbove, above);
-    }
-    send_list(sh);
-    sh.sync();
-    const int total = listed(sh);
-    if (total < 0) return false;
     if (rank == 0) {
         Cut c = no_cut();
         if (total > 0) {
