@@ -38,6 +38,7 @@ struct ScanArgs {
     int N;
     bool softplus;
     bool vec_bc;                        // B and C rows can be read in 16-byte pieces
+    bool vec_x;                         // and x rows
     bool chunked;                       // the tensor-core form (scan_chunk.cu)
     int segments;                       // parts that the steps are split into
     int64_t seg_steps;                  // steps per part (the last may be shorter)

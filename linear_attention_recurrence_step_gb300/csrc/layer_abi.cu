@@ -186,6 +186,8 @@ gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, con
     a.softplus = softplus != 0;
     a.vec_bc = aligned(Bm, 16) && aligned(Cm, 16) && (T == 1 || (st.B_t * eb % 16 == 0 && st.C_t * eb % 16 == 0)) &&
                (B == 1 || (st.B_b * eb % 16 == 0 && st.C_b * eb % 16 == 0));
+    a.vec_x = aligned(x, 16) && P * eb % 16 == 0 && (T == 1 || st.x_t * eb % 16 == 0) &&
+              (B == 1 || st.x_b * eb % 16 == 0);
     a.chunked = chunked;
     a.segments = plan.segments;
     a.seg_steps = plan.seg_steps;

@@ -15,6 +15,7 @@
 // third one runs the segments from those.
 #include "layer.h"
 #include "pieces.cuh"
+#include "tile.cuh"
 
 namespace gdn {
 
@@ -35,6 +36,9 @@ template <int N, bool SHORT> struct ScanShape {
     static constexpr int kWarpRows = RW * RPL;
 };
 
+// Whether a kernel has room to copy a stage ahead.
+__host__ __device__ constexpr bool scan_ahead(int N, bool SHORT) { return !SHORT && N <= 128; }
+
 // workspace: end states [segments][B][H][P][N], then decays [segments][B][H]
 template <typename T, int N, int phase, bool SHORT>
 __global__ void __launch_bounds__(kScanWarps * 32)
@@ -42,6 +46,7 @@ scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
     using S = ScanShape<N, SHORT>;
     constexpr int LR = S::LR, VPL = S::VPL, RPL = S::RPL, RW = S::RW, WR = S::kWarpRows;
     constexpr int NV4 = VPL / 4;  // float4 groups per lane and row: entries j*4*LR + lane*4
+    constexpr bool AHEAD = scan_ahead(N, SHORT);
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const int warps = blockDim.x / 32, rows_cta = warps * WR;
     float *sB = reinterpret_cast<float *>(smem_raw);      // [kStage][N]
@@ -111,53 +116,108 @@ scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
     const bool out = phase != kScanFold && a.y != nullptr;
     float decay = 1.f;
 
+    // The next stage's rows are copied while this one is worked on, where whole
+    // pieces can be (`ahead`); the step sizes go by a register.
+    constexpr int VE = 16 / sizeof(T);
+    const bool ahead = AHEAD && a.T > kStage && a.vec_bc && a.vec_x;
+    T *const rB = reinterpret_cast<T *>(sd + kStage), *const rC = rB + kStage * N, *const rx = rC + kStage * N;
+    float next_dt = 0.f;
+    auto fetch = [&](int64_t t0) {
+        const int n = (int)(t_end - t0 < kStage ? t_end - t0 : kStage);
+        constexpr int PR = N / VE;
+        for (int i = threadIdx.x; i < n * PR; i += blockDim.x) {
+            const int t = i / PR, c = i % PR * VE;
+            cp_async16(rB + t * N + c, Bp + (t0 + t) * a.b_st + c);
+            if (out) cp_async16(rC + t * N + c, Cp + (t0 + t) * a.c_st + c);
+        }
+        const int px = rows_cta / VE;
+        for (int i = threadIdx.x; i < n * px; i += blockDim.x) {
+            const int t = i / px, p = i % px * VE;
+            if (rb * rows_cta + p < a.P)
+                cp_async16(rx + t * rows_cta + p, x + (t0 + t) * a.x_st + rb * rows_cta + p);
+        }
+        cp_async_commit();
+        if (threadIdx.x < n) next_dt = ld_f32(dtp + (t0 + threadIdx.x) * a.dt_st);
+    };
+    if (ahead && t_begin < t_end) fetch(t_begin);
+
     for (int64_t t0 = t_begin; t0 < t_end; t0 += kStage) {
         const int n = (int)(t_end - t0 < kStage ? t_end - t0 : kStage);
+        if (ahead) cp_async_wait_all();
         __syncthreads();
-        if (a.vec_bc) {
-            constexpr int VE = 16 / sizeof(T), PR = N / VE;  // pieces of a row
-            for (int i = threadIdx.x; i < n * PR; i += blockDim.x) {
-                const int t = i / PR, c = i % PR * VE;
-                const RawPiece<T, VE> rB = load_raw<T, VE>(Bp + (t0 + t) * a.b_st + c);
+        float dt_now = next_dt;
+        if (ahead) {
+            for (int i = threadIdx.x * VE; i < n * N; i += blockDim.x * VE) {
                 float v[VE];
-                if (out) {
-                    const RawPiece<T, VE> rC = load_raw<T, VE>(Cp + (t0 + t) * a.c_st + c);
-                    widen<T, VE>(v, rC);
-#pragma unroll
-                    for (int e = 0; e < VE; e += 4)
-                        *reinterpret_cast<float4 *>(sC + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                }
-                widen<T, VE>(v, rB);
+                load_piece<T, VE>(v, rB + i);
 #pragma unroll
                 for (int e = 0; e < VE; e += 4)
-                    *reinterpret_cast<float4 *>(sB + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    *reinterpret_cast<float4 *>(sB + i + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                if (out) {
+                    load_piece<T, VE>(v, rC + i);
+#pragma unroll
+                    for (int e = 0; e < VE; e += 4)
+                        *reinterpret_cast<float4 *>(sC + i + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+            for (int i = threadIdx.x * VE; i < n * rows_cta; i += blockDim.x * VE) {
+                float v[VE];
+                load_piece<T, VE>(v, rx + i);
+                const bool in = rb * rows_cta + i % rows_cta < a.P;
+#pragma unroll
+                for (int e = 0; e < VE; e += 4)
+                    *reinterpret_cast<float4 *>(sx + i + e) =
+                        in ? make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         } else {
-            for (int i = threadIdx.x; i < n * N; i += blockDim.x) {
-                const int t = i / N, c = i % N;
-                sB[i] = ld_f32(Bp + (t0 + t) * a.b_st + c);
-                if (out) sC[i] = ld_f32(Cp + (t0 + t) * a.c_st + c);
+            if (a.vec_bc) {
+                constexpr int PR = N / VE;  // pieces of a row
+                for (int i = threadIdx.x; i < n * PR; i += blockDim.x) {
+                    const int t = i / PR, c = i % PR * VE;
+                    const RawPiece<T, VE> rB = load_raw<T, VE>(Bp + (t0 + t) * a.b_st + c);
+                    float v[VE];
+                    if (out) {
+                        const RawPiece<T, VE> rC = load_raw<T, VE>(Cp + (t0 + t) * a.c_st + c);
+                        widen<T, VE>(v, rC);
+#pragma unroll
+                        for (int e = 0; e < VE; e += 4)
+                            *reinterpret_cast<float4 *>(sC + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                    widen<T, VE>(v, rB);
+#pragma unroll
+                    for (int e = 0; e < VE; e += 4)
+                        *reinterpret_cast<float4 *>(sB + t * N + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            } else {
+                for (int i = threadIdx.x; i < n * N; i += blockDim.x) {
+                    const int t = i / N, c = i % N;
+                    sB[i] = ld_f32(Bp + (t0 + t) * a.b_st + c);
+                    if (out) sC[i] = ld_f32(Cp + (t0 + t) * a.c_st + c);
+                }
             }
-        }
-        for (int i = threadIdx.x; i < n * rows_cta; i += blockDim.x) {
-            const int t = i / rows_cta, p = i % rows_cta;
-            sx[i] = rb * rows_cta + p < a.P ? ld_f32(x + (t0 + t) * a.x_st + rb * rows_cta + p) : 0.f;
+            for (int i = threadIdx.x; i < n * rows_cta; i += blockDim.x) {
+                const int t = i / rows_cta, p = i % rows_cta;
+                sx[i] = rb * rows_cta + p < a.P ? ld_f32(x + (t0 + t) * a.x_st + rb * rows_cta + p) : 0.f;
+            }
+            if (threadIdx.x < n) dt_now = ld_f32(dtp + (t0 + threadIdx.x) * a.dt_st);
         }
         if (threadIdx.x < n) {
-            float d = ld_f32(dtp + (t0 + threadIdx.x) * a.dt_st) + bias;
+            float d = dt_now + bias;
             if (a.softplus) d = fmaxf(d, 0.f) + log1pf(expf(-fabsf(d)));
             sd[threadIdx.x] = d;
             sg[threadIdx.x] = expf(d * Ah);
         }
         __syncthreads();
+        if (ahead && t0 + kStage < t_end) fetch(t0 + kStage);
         for (int t = 0; t < n; ++t) {
             const float gt = sg[t], dl = sd[t];
             decay *= gt;
-            float xv[RPL], acc[RPL];
+            float xv[RPL];
+            float2 acc2[RPL];
 #pragma unroll
             for (int r = 0; r < RPL; ++r) {
-                xv[r] = sx[t * rows_cta + warp * WR + grp + r * RW];
-                acc[r] = 0.f;
+                xv[r] = dl * sx[t * rows_cta + warp * WR + grp + r * RW];
+                acc2[r] = make_float2(0.f, 0.f);
             }
 #pragma unroll
             for (int j = 0; j < NV4; ++j) {
@@ -166,21 +226,19 @@ scan_step_kernel(const ScanArgs a, const int64_t row_blocks) {
                 if (out) Cv = *reinterpret_cast<const float4 *>(sC + t * N + j * 4 * LR + sub * 4);
 #pragma unroll
                 for (int r = 0; r < RPL; ++r) {
-                    const float dx = dl * xv[r];
-                    const float2 dx2 = make_float2(dx, dx), g2 = make_float2(gt, gt);
+                    const float2 dx2 = make_float2(xv[r], xv[r]), g2 = make_float2(gt, gt);
                     const float2 lo = ffma2(g2, lo2(s[r][j]), fmul2(dx2, lo2(Bv)));
                     const float2 hi = ffma2(g2, hi2(s[r][j]), fmul2(dx2, hi2(Bv)));
                     s[r][j] = cat4(lo, hi);
-                    if (out) {
-                        float2 z = fmul2(lo, lo2(Cv));
-                        z = ffma2(hi, hi2(Cv), z);
-                        acc[r] += z.x + z.y;
-                    }
+                    if (out) acc2[r] = ffma2(hi, hi2(Cv), ffma2(lo, lo2(Cv), acc2[r]));
                 }
             }
             if (out) {
                 // the lanes of a row share its sum out: half of the rows go to
                 // each side until a lane holds one row, then plain exchanges
+                float acc[RPL];
+#pragma unroll
+                for (int r = 0; r < RPL; ++r) acc[r] = acc2[r].x + acc2[r].y;
                 int row = 0, left = RPL;
 #pragma unroll
                 for (int o = LR / 2; o > 0; o >>= 1) {
@@ -264,7 +322,8 @@ template <typename T, int N, int PHASE, bool SHORT>
 cudaError_t launch_phase(const ScanArgs &a, cudaStream_t s) {
     int64_t row_blocks;
     const int warps = (int)scan_warps<N, SHORT>(a.P, &row_blocks);
-    const size_t smem = (size_t)kStage * (2 * N + warps * ScanShape<N, SHORT>::kWarpRows + 2) * 4;
+    const size_t row = 2 * N + warps * ScanShape<N, SHORT>::kWarpRows;  // of B, C and x
+    const size_t smem = kStage * ((row + 2) * 4 + (scan_ahead(N, SHORT) ? row * sizeof(T) : 0));
     const int64_t ctas = a.B * a.H * row_blocks * a.segments;
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     return launch_dependent(scan_step_kernel<T, N, PHASE, SHORT>, (unsigned)ctas, warps * 32, smem, s, a, row_blocks);
@@ -316,7 +375,7 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
     if (chunked) {
         // sixteen warps per SM
         target = 152.0 * (16 / scan_chunk_warps(P, &row_blocks));
-        least = 256;
+        least = 64;
         unit = 32;
     } else {
         switch (N) {
