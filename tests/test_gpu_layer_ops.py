@@ -168,6 +168,40 @@ def test_scan(dev, B, T, H, P, G, N, dtype, state, lengths, pad, D, bias, softpl
         assert torch.equal(st, so) and torch.equal(y2.nan_to_num(7), y.nan_to_num(7)), "in place"
 
 
+# the tensor-core form (bf16, N of 64 or 128, whole 16-byte rows): chunks of 32,
+# one segment and several, rows of every warp count, two blocks of rows
+CHUNKED = [  # B, T, H, P, G, N, lengths, D, bias
+    (1, 32, 1, 8, 1, 64, None, True, True),
+    (2, 33, 2, 16, 1, 128, "ragged", False, True),
+    (1, 1000, 2, 64, 1, 64, None, True, True),
+    (3, 700, 2, 72, 2, 128, "ragged", True, True),
+    (1, 2080, 1, 128, 1, 128, None, True, False),
+    (2, 130, 3, 200, 1, 64, "ragged", True, True),
+    (40, 40, 8, 64, 4, 128, "ragged", True, True),
+]
+
+
+@pytest.mark.parametrize("B,T,H,P,G,N,lengths,D,bias", CHUNKED)
+def test_scan_chunked(dev, B, T, H, P, G, N, lengths, D, bias):
+    test_scan(dev, B, T, H, P, G, N, "bf16", True, lengths, 0, D, bias, True)
+
+
+def test_scan_forms_agree(dev):
+    """The same call on rows that are whole 16-byte pieces (the tensor-core
+    form) and on rows that are not (the step form)."""
+    rng = np.random.default_rng(12)
+    (x, dt, A, Bm, Cm, st, Dt, bt), _ = scan_inputs(rng, 2, 300, 4, 64, 2, 128, "bf16", dev, True, 0, True, True)
+    (xs, _, _, Bs, Cs, _, _, _), _ = scan_inputs(rng, 2, 300, 4, 64, 2, 128, "bf16", dev, True, 1, True, True)
+    for a, b in ((xs, x), (Bs, Bm), (Cs, Cm)):
+        a.copy_(b)
+    lens = torch.tensor([300, 171], dtype=torch.int32, device=dev)
+    a = gdn.gdn_selective_scan(x, dt, A, Bm, Cm, st, D=Dt, dt_bias=bt, lengths=lens)
+    b = gdn.gdn_selective_scan(xs, dt, A, Bs, Cs, st, D=Dt, dt_bias=bt, lengths=lens)
+    assert float((a.state_out - b.state_out).abs().max()) < 1e-5 * float(b.state_out.abs().max())
+    on = torch.arange(300, device=dev) < lens[:, None]
+    assert float((a.y.float() - b.y.float())[on].abs().max()) < 2.0 ** -7 * float(b.y.float()[on].abs().max())
+
+
 def test_scan_rolls_back(dev):
     """Draft steps, then the accepted prefix again from the snapshot: the state
     that a call over just those steps gives."""
@@ -213,6 +247,18 @@ NORM = [  # lead shape, D, dtype, gate, residual, weight per head, pad
     ((300, 8), 64, "f32", "after", False, True, 0),
     ((2, 2), 2056, "bf16", "none", True, False, 0),
     ((11, 1), 24, "bf16", "after", False, False, 0),
+    # enough rows for several per thread
+    ((5000, 8), 128, "bf16", "after", False, False, 0),
+    ((5001, 8), 120, "f16", "first", True, True, 8),
+    ((1250, 32), 256, "bf16", "after", True, False, 0),
+    ((40000, 1), 64, "f32", "after", False, False, 0),
+    ((9750, 4), 512, "bf16", "none", False, True, 0),
+    # wide rows, whole and cut across 16-byte boundaries
+    ((3, 1), 5120, "f32", "none", True, False, 0),
+    ((5, 1), 10237, "f16", "after", True, False, 0),
+    ((4, 1), 1031, "f32", "first", True, False, 0),
+    ((6, 1), 77, "bf16", "after", True, False, 0),
+    ((2, 3), 16001, "bf16", "after", True, True, 0),
 ]
 
 
@@ -345,6 +391,32 @@ def test_sample_cut_is_exact(dev, dtype, V, levels):
     out = gdn.gdn_sample(l, torch.from_numpy(noise).to(dev),
                          **{k: torch.from_numpy(v).to(dev) for k, v in settings.items()})
     hold_sample(out, l64, noise, settings, 6)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_sample_sweep(dev, seed):
+    """Rows of every shape of distribution, each with settings of its own: large
+    top-k with top-p, nuclei of a handful and of most tokens, lists that do not
+    fit, one CTA and clusters."""
+    rng = np.random.default_rng(700 + seed)
+    V = int(rng.choice([257, 4096, 9001, 33000, 70001, 131072]))
+    R = int(rng.integers(2, 9))
+    dtype = ["bf16", "f32", "f16"][seed % 3]
+    sigma = rng.choice([0.05, 0.7, 1.5, 4.0, 12.0], R)
+    logits = sigma[:, None] * rng.standard_normal((R, V)) + rng.choice([0.0, 30.0, -200.0], R)[:, None]
+    logits[:, rng.integers(0, V, 5)] += sigma[:, None] * rng.uniform(0, 6, 5)
+    logits[rng.random((R, V)) < 0.05] = -np.inf
+    l, l64 = put(logits, dtype, dev)
+    noise = rng.standard_exponential((R, V)).astype(np.float32)
+    s = dict(temperature=rng.uniform(0.3, 2, R).astype(np.float32),
+             top_k=rng.choice([0, 0, 5, 256, 257, V // 3, V], R).astype(np.int32),
+             top_p=rng.choice([0.1, 0.5, 0.9, 0.999, 1.0], R).astype(np.float32),
+             min_p=rng.choice([0.0, 0.0, 0.001, 0.2], R).astype(np.float32))
+    out = gdn.gdn_sample(l, torch.from_numpy(noise).to(dev), **{k: torch.from_numpy(v).to(dev) for k, v in s.items()})
+    hold_sample(out, l64, noise, s, R)
+    again = gdn.gdn_sample(l, torch.from_numpy(noise).to(dev),
+                           **{k: torch.from_numpy(v).to(dev) for k, v in s.items()})
+    assert torch.equal(again.token, out.token) and torch.equal(again.logprob, out.logprob)
 
 
 def test_sample_masks(dev):
