@@ -164,13 +164,23 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         }
         cp_async_commit();
     };
-    // the decays of a chunk, by one warp, a step per lane
+    // the decays of a chunk, by one warp, a step per lane: the last two warps in
+    // turn, which have the least to do for W; each has read its next steps'
+    // sizes by then
+    auto step_size = [&](int c) {
+        const int64_t t = t_begin + (int64_t)c * kL + lane;
+        return t < t_end ? ld_f32(dtp + t * a.dt_st) : 0.f;
+    };
+    auto decay_warp = [&](int c) { return warps > 1 ? warps - 1 - (c & 1) : 0; };
+    float next_size = 0.f;
     auto decays = [&](int c) {
         const int64_t t = t_begin + (int64_t)c * kL + lane;
         ChunkDecay &d = sdec[c & 1];
         float dl = 0.f;
+        const float size = next_size;
+        next_size = step_size(c + (warps > 1 ? 2 : 1));
         if (t < t_end) {
-            const float v = ld_f32(dtp + t * a.dt_st) + bias;
+            const float v = size + bias;
             dl = a.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
         }
         // a decay below 2^-256 is zero in f32
@@ -218,7 +228,12 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
     const int lr = lane & 7, lm = lane >> 3;            // ldmatrix: row and matrix of this lane's address
     if (chunks > 0) {
         fetch(0);
-        if (warp == 0) decays(0);
+        if (warp == decay_warp(0)) {
+            next_size = step_size(0);
+            decays(0);
+        } else if (warp == decay_warp(1)) {
+            next_size = step_size(1);
+        }
     }
     for (int c = 0; c < chunks; ++c) {
         const int buf = c & 1;
@@ -226,7 +241,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
         __syncthreads();
         if (c + 1 < chunks) {
             fetch(c + 1);
-            if (warp == (c + 1) % warps) decays(c + 1);
+            if (warp == decay_warp(c + 1)) decays(c + 1);
         }
         const ChunkDecay &d = sdec[buf];
         // where this lane's ldmatrix rows start: plain tiles of B and C (rows

@@ -371,7 +371,7 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
     int64_t row_blocks = 1;
     // CTAs that fill 152 SMs, and the fewest steps of a segment
     double target = 608.0;
-    int64_t least = 32, unit = kStage;
+    int64_t least = 64, unit = kStage;
     if (chunked) {
         // sixteen warps per SM
         target = 152.0 * (16 / scan_chunk_warps(P, &row_blocks));
