@@ -8,6 +8,11 @@
 // channels and a run of consecutive steps; the window of W-1 earlier inputs
 // stays in its registers, so a run re-reads only the W-1 steps before it.
 // Sums are f32 and rounded once.
+//
+// Measured (4096 steps of 8192 bf16 channels, width 4): 29.6 us, 4.5 TB/s of
+// the bytes it cannot do without; the inputs read again at the start of a run
+// come from L2.  16 x 8 steps: 4.6 us, one step of 32 sequences: 3.5 us, which
+// are a launch and two dependent loads.
 #include "pieces.cuh"
 #include "layer.h"
 
@@ -146,9 +151,11 @@ __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 4 : 2) conv_kernel(cons
 template <typename T, int VEC, int W>
 cudaError_t launch_w(const ConvArgs &a, int sm_count, cudaStream_t s) {
     const int64_t cblocks = (a.C + (int64_t)kConvThreads * VEC - 1) / ((int64_t)kConvThreads * VEC);
-    // steps per thread: up to 32, fewer while there are not four blocks per SM
+    // Steps per thread: up to 32, fewer while there are not three blocks per SM.
+    // 32 at 4096 steps of 8192 channels: 29.5 us, 8 steps there: 40.9 us; at 512
+    // steps 9.6 and 5.7 us, at four sequences of 512 16.8 and 23.4 us.
     int run = 32;
-    const int64_t want = 4 * (int64_t)(sm_count > 0 ? sm_count : 152);
+    const int64_t want = 3 * (int64_t)(sm_count > 0 ? sm_count : 152);
     if (!a.y || a.T <= 8) run = 8;
     while (run > 8 && a.B * cblocks * ((a.T + run - 1) / run) < want) run /= 2;
     const int64_t runs = a.y ? (a.T + run - 1) / run : 1;
