@@ -9,7 +9,7 @@
 // stays in its registers, so a run re-reads only the W-1 steps before it.
 // Sums are f32 and rounded once.
 //
-// Measured (4096 steps of 8192 bf16 channels, width 4): 29.6 us, 4.5 TB/s of
+// Measured (4096 steps of 8192 bf16 channels, width 4): 27.4 us, 4.9 TB/s of
 // the bytes it cannot do without; the inputs read again at the start of a run
 // come from L2.  16 x 8 steps: 4.6 us, one step of 32 sequences: 3.5 us, which
 // are a launch and two dependent loads.
@@ -151,10 +151,10 @@ __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 4 : 2) conv_kernel(cons
 template <typename T, int VEC, int W>
 cudaError_t launch_w(const ConvArgs &a, int sm_count, cudaStream_t s) {
     const int64_t cblocks = (a.C + (int64_t)kConvThreads * VEC - 1) / ((int64_t)kConvThreads * VEC);
-    // Steps per thread: up to 32, fewer while there are not three blocks per SM.
-    // 32 at 4096 steps of 8192 channels: 29.5 us, 8 steps there: 40.9 us; at 512
-    // steps 9.6 and 5.7 us, at four sequences of 512 16.8 and 23.4 us.
-    int run = 32;
+    // Steps per thread: up to 64, fewer while there are not three blocks per SM.
+    // 4096 steps of 8192 channels: 27.4 us by 64, 29.5 by 32, 34.0 by 16, 40.9 by
+    // 8; 512 steps: 9.6 us by 32, 5.7 by 8.
+    int run = 64;
     const int64_t want = 3 * (int64_t)(sm_count > 0 ? sm_count : 152);
     if (!a.y || a.T <= 8) run = 8;
     while (run > 8 && a.B * cblocks * ((a.T + run - 1) / run) < want) run /= 2;
