@@ -1300,6 +1300,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         if (!done)
             cut = narrow<true, ROUNDS>(row, sh, rank, cut, 0, (double)top_p * zk * 0x1p40, low, in, fast_e);
+        // the cuts above are exact among the tokens that top-k left, and may end
+        // past the last of them: what top-k removed stays out
+        if (cut.l < k_cut.l) cut = k_cut;
+        else if (cut.l == k_cut.l) cut.end = min(cut.end, k_cut.end);
     }
 
     if (only_first) {
