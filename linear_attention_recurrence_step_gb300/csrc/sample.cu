@@ -782,7 +782,7 @@ __device__ __forceinline__ Cut cut_near(const Shared &sh, const Near &near, Mass
 // holds it; `width` is a bin's in units of log(e).  ALL: every token of
 // logit `low` or more takes part, and the bins cover all of those; else those
 // of which `in(l, idx)` holds, the last bin taking what lies below.  False:
-// the list does not fit.
+// the list does not fit, or does not hold the cut.
 template <bool MASS, bool ALL, bool CACHED, int LOW, typename RowT, typename In, typename Mass, typename Mass2,
           typename Prefetch>
 __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, int rank, Cut &cut, uint32_t k,
@@ -851,9 +851,12 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
     }
     if (lane == 31) sh.putf(kRed + warp, incl);
     __syncthreads();
+    // (a thread's last bin ends at the very value from which the next thread
+    // goes on, so that no value lies between two bins)
     float run = 0.f;
     for (int i = 0; i < warp; ++i) run += sh.getf(kRed + i);
-    run += incl - sum;
+    const float end = run + incl, before = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane > 0) run += before;
     // counts are exact in f32 up to 2^24; masses have room for the roundings
     const float first = MASS ? (float)target * 0.9999f : (float)k;
     const float last = MASS ? (float)target * 1.0001f * expf(width) : (float)k;
@@ -865,14 +868,15 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
 #pragma unroll
     for (int j = 0; j < PB; ++j) {
         const int bin = threadIdx.x * PB + j;
-        const float next = run + part[j];
+        const float next = j + 1 < PB ? run + part[j] : end;
+        // (rounded masses may pass a value twice: the first bin counts)
         if (run < first && next >= first) {
-            sh.put(kFoundBin, bin);
-            sh.put(kFoundCount, (uint32_t)run);
+            sh.min_only(kFoundBin, bin);
+            if (!MASS) sh.put(kFoundCount, (uint32_t)run);
         }
-        if (run < last && next >= last) sh.put(kFoundLast, bin);
-        if (MASS && run < first_tight && next >= first_tight) sh.put(kTightBin, bin);
-        if (MASS && run < last_tight && next >= last_tight) sh.put(kTightLast, bin);
+        if (run < last && next >= last) sh.min_only(kFoundLast, bin);
+        if (MASS && run < first_tight && next >= first_tight) sh.min_only(kTightBin, bin);
+        if (MASS && run < last_tight && next >= last_tight) sh.min_only(kTightLast, bin);
         run = next;
     }
     __syncthreads();
@@ -928,9 +932,10 @@ __device__ __forceinline__ bool cut_by_list(const RowT &row, const Shared &sh, i
         sh.sync();
         total = listed(sh);
         if (total < 0) return false;
-        if (!tight) break;
+        if (!MASS) break;
         const float all_above = sh.sum_ctas(kPartAbove);
         if (all_above < (float)target && all_above + sh.sum_ctas(kPartIn) >= (float)target) break;
+        if (!tight) return false;  // (a target within roundings of the whole mass)
         sh.sync();
         if (threadIdx.x == 0) {
             sh.put(kListN, 0);

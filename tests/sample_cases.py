@@ -53,3 +53,28 @@ def tied_cut(name, seed=0):
     noise[order[-1]] = 1e-10
     noise[full[k:]] = 1e-25
     return l, s, noise
+
+
+def bracket_edge(seed):
+    """(logits [V] f64 of float32 values, top_p near which a nucleus ends where
+    the kernel's bracket for it begins).  The kernel counts tokens in 4096 bins
+    over the range that can matter and bounds the mass above each bin by the
+    bins' upper edges; it looks for the nucleus' end from the bin on in which
+    that bound passes top_p times the mass (less a ten-thousandth).  Here 1500
+    tokens lie just below such edges, so that the bound is tight, then one
+    alone in its bin, in which the nucleus ends, then 1500 more; the bound
+    passes exactly between the first 1500 and the one."""
+    V, rng = 50000, np.random.default_rng(seed)
+    bins = np.sort(rng.integers(770, 900, 1500))
+    late = np.concatenate([[1000], rng.integers(1002, 1015, 1500)])
+    p = 0.7
+    for _ in range(100):
+        z = 25.0
+        for _ in range(300):
+            width = -np.log(0.5 * (1 - p) * z / V) / 4096
+            d, d_late = (bins - 0.47) * width, (late - 0.45) * width
+            z = 1 + np.exp(-d).sum() + np.exp(-d_late).sum()
+        p = (np.exp(0.5 * width) + np.exp(-(bins - 0.5) * width).sum()) / (0.9999 * z)
+    l = np.full(V, -np.inf)
+    l[:3002] = np.concatenate([[0.0], -d, -d_late])
+    return np.random.default_rng(seed).permutation(l.astype(np.float32)).astype(np.float64), np.float32(p)

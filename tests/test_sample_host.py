@@ -11,7 +11,7 @@ import pytest
 
 import host_cuda
 import layer_reference as ref
-from sample_cases import TIED_CUTS, tied_cut
+from sample_cases import TIED_CUTS, bracket_edge, tied_cut
 
 torch = pytest.importorskip("torch")
 
@@ -105,3 +105,36 @@ def test_top_p_stays_inside_top_k(lib, name, sms):
     for dtype in ("bf16", "f32") if sms != 4 else ("f16",):
         l, s, noise = tied_cut(name)
         hold(lib, l[None], noise[None], dtype, sms, **s)
+
+
+@pytest.mark.parametrize("seed", [2, 3, 7, 15, 22, 23, 30])
+def test_nucleus_at_the_edge_of_its_bracket(lib, seed):
+    """Rows whose running masses pass the bracket's first value in the rounding
+    between one thread's sum and the next one's: the cut is found all the same
+    (noise lets every token past it win, were it left)."""
+    l, p = bracket_edge(seed)
+    ps = (p.view(np.int32) + np.arange(-2, 3, dtype=np.int32)).view(np.float32)
+    full = np.argsort(-l, kind="stable")
+    noise = np.ones((5, len(l)), np.float32)
+    for r in range(5):
+        n = len(ref.kept_order(l, 1.0, 0, ps[r], 0.0)[0])
+        assert 1490 < n < 1510
+        noise[r, full[n:]] = 1e-25
+        noise[r, full[n - 1]] = 1e-10
+    hold(lib, np.repeat(l[None], 5, 0), noise, "f32", 1, top_p=ps)
+
+
+@pytest.mark.parametrize("sms", [1, 152], ids=["one block", "cluster"])
+def test_extreme_settings(lib, sms):
+    """Temperatures at both ends, nuclei of next to nothing and next to all."""
+    rng = np.random.default_rng(3)
+    R, V = 12, 5001
+    logits = 3 * rng.standard_normal((R, V))
+    logits[:, ::7] = -np.inf
+    logits[8:, 3:] = -np.inf
+    noise = rng.standard_exponential((R, V))
+    hold(lib, logits, noise, "f32", sms,
+         temperature=[3e38, 3e38, 1e30, 1e-30, 1e-45, 1, 1, 1, 3e38, 1e-30, 1, 1],
+         top_k=[0, 300, 20, 0, 0, 0, 0, 2000, 0, 0, 300, 2],
+         top_p=[.4, .4, .9, .9, 1, 1e-30, .9999999, .9999999, .6, .6, .9999999, .9],
+         min_p=[0, 0, .5, 0, 1e-30, 0, 0, 0, 1, 0, 0, 1e-40])
