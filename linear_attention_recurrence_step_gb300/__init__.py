@@ -2,7 +2,9 @@
 
 A thin ctypes binding over ``libgdn.so`` (C ABI: ``include/gdn.h``).  The
 functions below only check tensor metadata, allocate missing outputs with
-PyTorch and forward raw device pointers plus the current CUDA stream; every
+PyTorch and forward raw device pointers plus the current CUDA stream, or the
+one given as ``stream`` (a stream object or a raw handle): then what a call
+allocates belongs to that stream, as it does under ``torch.cuda.stream``.  Every
 step of the computation runs in the library's sm_103a kernels.  There is no
 CPU or PyTorch fallback: if the library has not been built (``build()``) or
 cannot be loaded, every call raises ``GdnError``.
@@ -191,6 +193,22 @@ def _stream(device: torch.device, stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty in the memory of the stream that a call runs on (None: the
+    current one).  The caching allocator hands a freed block to the next
+    allocation of its own stream, so a workspace that dies with the call is
+    reused behind the call's kernels, and an output's block is free of earlier
+    work when they write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)  # 0 and 1 both name the default stream
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t: torch.Tensor, name: str, shape, dtype, device) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -231,16 +249,16 @@ def gdn_step_record(q, k, v, g, beta, state_in, mask=None, *, y=None, state_out=
     if mask is not None:
         _need(mask, "mask", (B, T), torch.int32 if mask.dtype == torch.int32 else torch.uint32, dev)
     if y is None:
-        y = torch.empty((B, T, Hv, Dv), dtype=dt, device=dev)
+        y = _empty((B, T, Hv, Dv), dt, dev, stream)
     if state_out is None:
-        state_out = torch.empty_like(state_in)
+        state_out = _empty(state_in.shape, state_in.dtype, dev, stream)
     if delta_log is None:
-        delta_log = torch.empty((B, T, Hv, Dv), dtype=dt, device=dev)
+        delta_log = _empty((B, T, Hv, Dv), dt, dev, stream)
     if capture_tape:
         if k_log is None:
-            k_log = torch.empty((B, T, Hv, Dk), dtype=dt, device=dev)
+            k_log = _empty((B, T, Hv, Dk), dt, dev, stream)
         if g_log is None:
-            g_log = torch.empty((B, T, Hv), dtype=dt, device=dev)
+            g_log = _empty((B, T, Hv), dt, dev, stream)
     _need(y, "y", (B, T, Hv, Dv), dt, dev)
     _need(state_out, "state_out", (B, Hv, Dv, Dk), state_in.dtype, dev)
     _need(delta_log, "delta_log", (B, T, Hv, Dv), dt, dev)
@@ -302,16 +320,16 @@ def gdn_chunk_prefill(q, k, v, g, beta, state_in, mask=None, *, y=None, state_ou
     if mask is not None:
         _need(mask, "mask", (B, T), torch.int32 if mask.dtype == torch.int32 else torch.uint32, dev)
     if y is None:
-        y = torch.empty((B, T, Hv, Dv), dtype=dt, device=dev)
+        y = _empty((B, T, Hv, Dv), dt, dev, stream)
     if state_out is None:
-        state_out = torch.empty_like(state_in)
+        state_out = _empty(state_in.shape, state_in.dtype, dev, stream)
     if delta_log is None and write_delta:
-        delta_log = torch.empty((B, T, Hv, Dv), dtype=dt, device=dev)
+        delta_log = _empty((B, T, Hv, Dv), dt, dev, stream)
     if capture_tape:
         if k_log is None:
-            k_log = torch.empty((B, T, Hv, Dk), dtype=dt, device=dev)
+            k_log = _empty((B, T, Hv, Dk), dt, dev, stream)
         if g_log is None:
-            g_log = torch.empty((B, T, Hv), dtype=dt, device=dev)
+            g_log = _empty((B, T, Hv), dt, dev, stream)
     _need(y, "y", (B, T, Hv, Dv), dt, dev)
     _need(state_out, "state_out", (B, Hv, Dv, Dk), torch.float32, dev)
     if delta_log is not None:
@@ -331,7 +349,7 @@ def gdn_chunk_prefill(q, k, v, g, beta, state_in, mask=None, *, y=None, state_ou
         return RecordOutputs(y, state_out, delta_log, k_log, g_log)
     need = gdn_chunk_prefill_workspace_size(B, T, Hv)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     st = load().gdn_chunk_prefill(
@@ -372,7 +390,7 @@ def gdn_state_replay(delta_log, k_log, g_log, state_in, mask=None, *, accepted,
     if mask is not None:
         _need(mask, "mask", (B, T), torch.int32 if mask.dtype == torch.int32 else torch.uint32, dev)
     if state_out is None:
-        state_out = torch.empty_like(state_in)
+        state_out = _empty(state_in.shape, state_in.dtype, dev, stream)
     _need(state_out, "state_out", (B, Hv, Dv, Dk), state_in.dtype, dev)
     ptrs = (_ptr(delta_log), _ptr(k_log), _ptr(g_log), _ptr(state_in), _ptr(mask),
             _ptr(state_out), B, T, Hv, Dk, Dv)
@@ -417,7 +435,7 @@ def gdn_chunk_replay(delta_log, k_log, g_log, state_in, mask=None, *, accepted,
     if mask is not None:
         _need(mask, "mask", (B, T), torch.int32 if mask.dtype == torch.int32 else torch.uint32, dev)
     if state_out is None:
-        state_out = torch.empty_like(state_in)
+        state_out = _empty(state_in.shape, state_in.dtype, dev, stream)
     _need(state_out, "state_out", (B, Hv, Dv, Dk), torch.float32, dev)
     per_seq = None
     if isinstance(accepted, torch.Tensor):
@@ -425,7 +443,7 @@ def gdn_chunk_replay(delta_log, k_log, g_log, state_in, mask=None, *, accepted,
         per_seq, accepted = accepted, 0
     need = gdn_chunk_replay_workspace_size(B, T, Hv, Dk, Dv)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(need, torch.uint8, dev, stream)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     st = load().gdn_chunk_replay(
@@ -453,7 +471,7 @@ def gqa_repeat_tiled(src, h: int, *, dst=None, stream=None) -> torch.Tensor:
     if not src.is_contiguous():
         raise ValueError("src must be contiguous")
     if dst is None:
-        dst = torch.empty((seq, h, kd), dtype=dt, device=dev)
+        dst = _empty((seq, h, kd), dt, dev, stream)
     _need(dst, "dst", (seq, h, kd), dt, dev)
     st = load().gqa_repeat_tiled(_ptr(src), _ptr(dst), seq, hg, h, kd, DTYPE_CODES[dt],
                                  src.numel() * src.element_size(),

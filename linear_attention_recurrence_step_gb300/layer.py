@@ -5,7 +5,8 @@ recurrence over the tokens (``gdn_step_record`` or ``gdn_selective_scan``) and
 normalises the result with ``gdn_gated_norm``; ``gdn_sample`` draws tokens,
 and the count of those that match a draft is the ``accepted`` of the replay
 calls.  As with the other calls, these functions check tensor metadata,
-allocate missing outputs and forward pointers and the current stream.
+allocate missing outputs and forward pointers and the current stream (or
+``stream``, to which the allocations then belong).
 
 ``lengths`` is an int32 device tensor [B]: the steps that each sequence has
 (clamped to 0..T).  ``y`` is not written at or past it.  A sequence is rolled
@@ -22,7 +23,7 @@ import torch
 
 import linear_attention_recurrence_step_gb300 as _pkg
 
-from . import DTYPE_CODES, _check, _need, load
+from . import DTYPE_CODES, _check, _empty, _need, load
 
 ConvOutputs = namedtuple("ConvOutputs", "y state_out")
 ScanOutputs = namedtuple("ScanOutputs", "y state_out")
@@ -138,11 +139,11 @@ def gdn_causal_conv(x, weight, state_in=None, *, bias=None, lengths=None, activa
     sb, st = _strided(x, "x", (B, T, C), dt, dev)
     if write_y:
         if y is None:
-            y = torch.empty((B, T, C), dtype=dt, device=x.device)
+            y = _empty((B, T, C), dt, x.device, stream)
     elif y is not None:
         raise ValueError("y is given but write_y is False")
     if state_out is None:
-        state_out = torch.empty((B, W - 1, C), dtype=dt, device=x.device)
+        state_out = _empty((B, W - 1, C), dt, x.device, stream)
     status = _lib().gdn_causal_conv(
         x.data_ptr(), _dense(weight, "weight", (C, W), dt, dev), _dense(bias, "bias", (C,), dt, dev),
         _dense(state_in, "state_in", (B, W - 1, C), dt, dev), _dense(lengths, "lengths", (B,), torch.int32, dev),
@@ -183,16 +184,16 @@ def gdn_selective_scan(x, dt, A, B, C, state_in=None, *, D=None, dt_bias=None, s
                            *_strided(B, "B", (nb, T, G, N), et, dev), *_strided(C, "C", (nb, T, G, N), et, dev))
     if write_y:
         if y is None:
-            y = torch.empty((nb, T, H, P), dtype=et, device=x.device)
+            y = _empty((nb, T, H, P), et, x.device, stream)
     elif y is not None:
         raise ValueError("y is given but write_y is False")
     shape = (nb, H, P, N)
     if state_out is None:
-        state_out = torch.empty(shape, dtype=torch.float32, device=x.device)
+        state_out = _empty(shape, torch.float32, x.device, stream)
     if workspace is None:
         need = _scan_workspace(nb, T, H, P, N)
         if need > 16:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _empty(need, torch.uint8, x.device, stream)
     elif workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     f32 = torch.float32
@@ -238,9 +239,9 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
         gs = xs if gate is None else _rows(gate, "gate", 2)
     M = x.numel() // (K * D) if x.numel() else 0
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=x.device)
+        y = _empty(shape, dt, x.device, stream)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=dt, device=x.device)
+        residual_out = _empty(shape, dt, x.device, stream)
     elif residual is None and residual_out is not None:
         raise ValueError("residual_out is given but residual is not")
     status = _lib().gdn_gated_norm(
@@ -279,9 +280,9 @@ def gdn_sample(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
         _need(noise, "noise", shape, torch.float32, logits.device)
     ns = _rows(noise, "noise", 1)
     if token is None:
-        token = torch.empty(lead, dtype=torch.int32, device=logits.device)
+        token = _empty(lead, torch.int32, logits.device, stream)
     if logprob is None:
-        logprob = torch.empty(lead, dtype=torch.float32, device=logits.device)
+        logprob = _empty(lead, torch.float32, logits.device, stream)
     f32 = torch.float32
     tp, tv = _setting(temperature, "temperature", lead, f32, dev, float)
     kp, kv = _setting(top_k, "top_k", lead, torch.int32, dev, int)

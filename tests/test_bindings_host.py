@@ -1,0 +1,126 @@
+"""The bindings without a GPU: CPU tensors that say they are on a CUDA device,
+and a library that records what it is called with."""
+from __future__ import annotations
+
+import contextlib
+
+import pytest
+
+import linear_attention_recurrence_step_gb300 as gdn
+from linear_attention_recurrence_step_gb300 import layer
+
+torch = pytest.importorskip("torch")
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that reports a CUDA device."""
+    index = 0
+    device = property(lambda self: torch.device("cuda", self.index))
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.index
+
+
+def cuda(*shape, dtype=torch.float32, index=0):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+    t.index = index
+    return t
+
+
+class Side:
+    """A stream object."""
+    cuda_stream = 0x7000
+
+
+class Library:
+    """Takes every call, with the sizes that the workspace calls are to give."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("workspace_size"):
+                return 1 << 12
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    """The recorded calls; `lib.made` holds the stream of every allocation (None:
+    the current one)."""
+    lib, inside = Library(), []
+    lib.made = []
+    real = torch.empty
+
+    @contextlib.contextmanager
+    def stream(s):
+        inside.append(s)
+        try:
+            yield
+        finally:
+            inside.pop()
+
+    def empty(*shape, dtype=None, device=None, **kw):
+        lib.made.append(inside[-1].cuda_stream if inside else None)
+        t = real(*shape, dtype=dtype).as_subclass(OnDevice)
+        t.index = torch.device(device).index or 0
+        return t
+
+    class External:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    monkeypatch.setattr(gdn, "_lib", lib)
+    monkeypatch.setattr(layer, "_raw_stream", lambda dev: 0x5000)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type("S", (), {"cuda_stream": 0x5000}))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: External(0))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch, "empty_like", lambda t: empty(t.shape, dtype=t.dtype, device=t.device))
+    layer._scan_workspace.cache_clear()
+    yield lib
+    layer._scan_workspace.cache_clear()
+
+
+def _calls():
+    """name -> (the call, how many outputs and workspaces it allocates)."""
+    B, T, Hk, Hv, D = 2, 20, 1, 2, 64
+    q, v, g, st = cuda(B, T, Hk, D), cuda(B, T, Hv, D), cuda(B, T, Hv), cuda(B, Hv, D, D)
+    tape = (v, cuda(B, T, Hv, D), g, st)
+    acc = cuda(B, dtype=torch.int32)
+    x, w = cuda(B, T, 64), cuda(64, 4)
+    bc = cuda(B, T, 1, 64)
+    return {
+        "step_record": (lambda **kw: gdn.gdn_step_record(q, q, v, g, g, st, capture_tape=True, **kw), 5),
+        "step_record_mapped": (lambda **kw: gdn.gdn_step_record_mapped(q, q, v, g, g, st, mapping="tiled", **kw), 3),
+        "chunk_prefill": (lambda **kw: gdn.gdn_chunk_prefill(q, q, v, g, g, st, capture_tape=True, **kw), 6),
+        "chunk_prefill_noalloc": (lambda **kw: gdn.gdn_chunk_prefill_noalloc(q, q, v, g, g, st, **kw), 3),
+        "state_replay": (lambda **kw: gdn.gdn_state_replay(*tape, accepted=3, **kw), 1),
+        "state_replay_per_seq": (lambda **kw: gdn.gdn_state_replay_per_seq(*tape, accepted=acc, **kw), 1),
+        "chunk_replay": (lambda **kw: gdn.gdn_chunk_replay(*tape, accepted=3, **kw), 2),
+        "repeat_tiled": (lambda **kw: gdn.gqa_repeat_tiled(v.reshape(B * T, Hv, D), 4, **kw), 1),
+        "causal_conv": (lambda **kw: gdn.gdn_causal_conv(x, w, **kw), 2),
+        "selective_scan": (lambda **kw: gdn.gdn_selective_scan(v, g, cuda(Hv), bc, bc, **kw), 3),
+        "gated_norm": (lambda **kw: gdn.gdn_gated_norm(x, cuda(64), residual=x, **kw), 2),
+        "sample": (lambda **kw: gdn.gdn_sample(x, x, **kw), 2),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_allocations_belong_to_the_calls_stream(lib, name):
+    """Outputs and workspaces that a call allocates come from the memory of the
+    stream that its kernels run on: a workspace is free again when the call
+    returns, and only work behind it in that stream may then have it."""
+    call, count = _calls()[name]
+    for given, handle, owner in ((None, 0x5000, None), (Side(), 0x7000, 0x7000), (0x7100, 0x7100, 0x7100),
+                                 (0, 0, 0), (1, 1, 0)):
+        lib.made.clear()
+        lib.calls.clear()
+        call(stream=given)
+        assert lib.made == [owner] * count
+        assert [args[-1] for _, args in lib.calls] == [handle]
