@@ -187,7 +187,25 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_current_device = torch._C._cuda_getDevice
+_one_device: Optional[bool] = None  # whether there is only one (asking for the current one takes a microsecond)
+
+
+def _is_current(index: int) -> bool:
+    global _one_device
+    if _one_device is None:
+        _one_device = torch.cuda.device_count() == 1
+    return _one_device or index == _current_device()
+
+
+def _other_device(index: int) -> ValueError:
+    return ValueError(f"the tensors are on cuda:{index}, but the current device is cuda:{_current_device()} "
+                      "(a call runs on the current device: see torch.cuda.device)")
+
+
 def _stream(device: torch.device, stream) -> int:
+    if device.type == "cuda" and not _is_current(device.index):
+        raise _other_device(device.index)
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)

@@ -61,10 +61,13 @@ def _dense(t, name, shape, dtype, dev):
 
 
 def _device_of(t, name):
-    """The CUDA device index of a floating tensor."""
+    """The CUDA device index of a floating tensor, the current one."""
     try:
         if t.dtype in DTYPE_CODES and t.is_cuda:
-            return t.get_device()
+            dev = t.get_device()
+            if _pkg._is_current(dev):
+                return dev
+            raise _pkg._other_device(dev)
     except AttributeError:
         raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype not in DTYPE_CODES:

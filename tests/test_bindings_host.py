@@ -53,7 +53,7 @@ def lib(monkeypatch):
     """The recorded calls; `lib.made` holds the stream of every allocation (None:
     the current one)."""
     lib, inside = Library(), []
-    lib.made = []
+    lib.made, lib.current = [], 0
     real = torch.empty
 
     @contextlib.contextmanager
@@ -77,6 +77,8 @@ def lib(monkeypatch):
     monkeypatch.setattr(gdn, "_lib", lib)
     monkeypatch.setattr(layer, "_raw_stream", lambda dev: 0x5000)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type("S", (), {"cuda_stream": 0x5000}))
+    monkeypatch.setattr(gdn, "_one_device", False)
+    monkeypatch.setattr(gdn, "_current_device", lambda: lib.current)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: External(0))
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", External)
@@ -124,3 +126,17 @@ def test_allocations_belong_to_the_calls_stream(lib, name):
         call(stream=given)
         assert lib.made == [owner] * count
         assert [args[-1] for _, args in lib.calls] == [handle]
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_another_device_is_refused(lib, name):
+    """Kernels run on the current device: tensors of another one are refused
+    before the library is called."""
+    call, _ = _calls()[name]
+    lib.current = 1
+    with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+        call()
+    assert not lib.calls
+    lib.current = 0
+    call()
+    assert len(lib.calls) == 1
