@@ -3,6 +3,7 @@
 // the host, before any CUDA call, under the rules of abi.cu.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "abi_util.h"
 #include "layer.h"
@@ -60,8 +61,11 @@ gdn_status gdn_causal_conv(const void *x, const void *weight, const void *bias, 
     if (state_in && state_out && state_in != state_out && overlap(state_in, s_b, state_out, s_b))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: state_out overlaps state_in without being the same buffer", fn);
     if (over(y, y_b, x, x_b) || over(y, y_b, state_in, s_b) || over(y, y_b, state_out, s_b) ||
-        over(state_out, s_b, x, x_b) || over(y, y_b, weight, w_b) || over(state_out, s_b, weight, w_b))
+        over(state_out, s_b, x, x_b))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps another tensor", fn);
+    for (const auto &[o, o_b] : {std::pair<const void *, int64_t>(y, y_b), {state_out, s_b}})
+        if (over(o, o_b, weight, w_b) || over(o, o_b, bias, C * eb) || over(o, o_b, lengths, B * 4))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps weight, bias or lengths", fn);
 
     if (take_forced_failure()) return forced_failure(fn);
     cudaError_t e;
@@ -147,6 +151,9 @@ gdn_status gdn_selective_scan(const void *x, const void *dt, const float *A, con
         if (over(outs[i], out_b[i], x, x_b) || over(outs[i], out_b[i], dt, dt_b) || over(outs[i], out_b[i], Bm, b_b) ||
             over(outs[i], out_b[i], Cm, c_b) || (i != 1 && over(outs[i], out_b[i], state_in, st_b)))
             return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps an input", fn);
+        if (over(outs[i], out_b[i], A, H * 4) || over(outs[i], out_b[i], D, H * 4) ||
+            over(outs[i], out_b[i], dt_bias, H * 4) || over(outs[i], out_b[i], lengths, B * 4))
+            return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps A, D, dt_bias or lengths", fn);
         for (int j = 0; j < i; ++j)
             if (over(outs[i], out_b[i], outs[j], out_b[j]))
                 return fail(GDN_ERR_INVALID_ARGUMENT, "%s: two outputs overlap", fn);

@@ -1,0 +1,39 @@
+"""Further refusals of the operators around the recurrence, and calls that
+they have to take (fake addresses: nothing reaches a device)."""
+from __future__ import annotations
+
+import pytest
+
+import linear_attention_recurrence_step_gb300 as gdn
+from test_layer_ops_host import CUDA, INVALID, OK, P, conv, lib, scan  # noqa: F401 (lib: fixture)
+
+torch = pytest.importorskip("torch")
+
+# outputs that lie on a small input (at its first byte, and just at its last)
+ON_SMALL = {
+    conv: [dict(y=P(2)), dict(state_out=P(2)), dict(y=P(4)), dict(state_out=P(4)),
+           dict(y=P(2) + 126), dict(state_out=P(4) + 6)],
+    scan: [dict(y=P(2)), dict(state_out=P(2)), dict(y=P(5)), dict(state_out=P(5)), dict(y=P(6)), dict(state_out=P(6)),
+           dict(y=P(8)), dict(state_out=P(8)), dict(y=P(2) + 14), dict(y=P(8) + 6),
+           *(dict(T=4096, B=1, ws=P(i), ws_bytes=1 << 30, y=P(40), state_out=P(80), x=P(100), Bm=P(120), Cm=P(140),
+                  dt=P(160)) for i in (2, 5, 6, 8))],
+}
+
+
+@pytest.mark.parametrize("call,kw", [(c, kw) for c in ON_SMALL for kw in ON_SMALL[c]],
+                         ids=lambda v: v.__name__ if callable(v) else "-".join(v))
+def test_an_output_on_a_small_input(lib, call, kw):  # noqa: F811
+    assert call(lib, **kw) == INVALID
+    assert b"overlap" in lib.gdn_last_error()
+
+
+def test_outputs_beside_small_inputs(lib):  # noqa: F811
+    """One element past the end is another tensor's."""
+    calls = [(conv, dict(y=P(2) + 128)), (conv, dict(y=P(4) + 8)), (scan, dict(y=P(2) + 16)),
+             (scan, dict(state_out=P(8) + 16))]
+    try:
+        assert lib.gdn_force_launch_failures(len(calls)) == OK
+        for call, kw in calls:
+            assert call(lib, **kw) == CUDA  # accepted: it got as far as the launch
+    finally:
+        assert lib.gdn_force_launch_failures(0) == OK
