@@ -99,8 +99,9 @@ def _strided(t, name, shape, dtype, dev):
     return (st[0] if shape[0] > 1 else step * shape[1]), step
 
 
-def _rows(t, name, inner_dims):
-    """Row stride of a tensor [..., inner] whose leading dimensions collapse into one."""
+def _rows(t, name, inner_dims, must=True):
+    """Row stride of a tensor [..., inner] whose leading dimensions collapse into
+    one; of another, the error (or None, unless it `must`)."""
     shape = t.shape
     lead = len(shape) - inner_dims
     dense = 1
@@ -111,6 +112,8 @@ def _rows(t, name, inner_dims):
     st = t.stride()
     for i in range(len(shape) - 1, lead - 1, -1):
         if st[i] != dense and shape[i] != 1:
+            if not must:
+                return None
             raise ValueError(f"{name}'s last dimension(s) must be dense (strides {st})")
         dense *= shape[i]
     row, count = None, 1
@@ -120,6 +123,8 @@ def _rows(t, name, inner_dims):
         if row is None:
             row = st[i]
         elif st[i] != row * count:
+            if not must:
+                return None
             raise ValueError(f"{name}'s leading dimensions must collapse into one (strides {st})")
         count *= shape[i]
     return dense if row is None else row
@@ -223,7 +228,7 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
     multiplies by silu(gate) after the norm, or before it with
     ``gate_first``.  With ``residual`` the norm is of ``residual +
     residual_scale * x``, which is also returned.  x and gate may be slices
-    of wider tokens [..., K, D]."""
+    of wider rows [..., D] or of wider tokens [..., K, D]."""
     dev = _device_of(x, "x")
     dt, shape = x.dtype, x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
@@ -232,9 +237,11 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
     per_head = weight.dim() == 2
     if gate is not None and (gate.shape != shape or gate.dtype is not dt or gate.get_device() != dev):
         _need(gate.contiguous() if gate.device == x.device else gate, "gate", shape, dt, x.device)
-    if not per_head and x.is_contiguous() and (gate is None or gate.is_contiguous()):
-        K, xs, gs = 1, D, D
-    else:
+    # a shared weight: rows [..., D], if x and gate are both that; else tokens of
+    # K heads each [..., K, D]
+    K, xs = 1, None if per_head else _rows(x, "x", 1, len(shape) < 2)
+    gs = xs if gate is None or xs is None else _rows(gate, "gate", 1, len(shape) < 2)
+    if gs is None:
         if len(shape) < 2:
             raise ValueError("x must be [..., K, D]")
         K = shape[-2]

@@ -140,3 +140,44 @@ def test_another_device_is_refused(lib, name):
     lib.current = 0
     call()
     assert len(lib.calls) == 1
+
+
+# a call of the norm, and the M, K, D and token strides of x and gate that the library gets
+def _norms():
+    kv = cuda(6, 576)                                  # a fused projection
+    seq = cuda(2, 5, 200)
+    heads = cuda(4, 3 * 64 + 8)
+    w = lambda *s: cuda(*s)  # noqa: E731
+    return {
+        "rows of a projection": (lambda **kw: gdn.gdn_gated_norm(kv[:, :512], w(512), **kw), (6, 1, 512, 576, 576)),
+        "three dimensions": (lambda **kw: gdn.gdn_gated_norm(seq[..., 8:72], w(64), **kw), (10, 1, 64, 200, 200)),
+        "one row": (lambda **kw: gdn.gdn_gated_norm(kv[0, 3:35], w(32), **kw), (1, 1, 32, 32, 32)),
+        "one of many": (lambda **kw: gdn.gdn_gated_norm(kv[2:3, :512], w(512), **kw), (1, 1, 512, 512, 512)),
+        "a sliced gate": (lambda **kw: gdn.gdn_gated_norm(cuda(6, 512), w(512), gate=kv[:, 64:], **kw), (6, 1, 512, 512, 576)),
+        "a sliced x": (lambda **kw: gdn.gdn_gated_norm(kv[:, 64:], w(512), gate=cuda(6, 512), **kw), (6, 1, 512, 576, 512)),
+        "heads of a projection": (lambda **kw: gdn.gdn_gated_norm(heads[:, :192].unflatten(-1, (3, 64)), w(64), **kw),
+                                  (4, 3, 64, 200, 200)),
+        "heads, x whole": (lambda **kw: gdn.gdn_gated_norm(cuda(4, 3, 64), w(64), gate=heads[:, 8:].unflatten(-1, (3, 64)), **kw),
+                           (4, 3, 64, 192, 200)),
+        "a weight per head": (lambda **kw: gdn.gdn_gated_norm(heads[:, :192].unflatten(-1, (3, 64)), w(3, 64), **kw),
+                              (4, 3, 64, 200, 200)),
+        "whole": (lambda **kw: gdn.gdn_gated_norm(cuda(4, 3, 64), w(64), **kw), (12, 1, 64, 64, 64)),
+    }
+
+
+@pytest.mark.parametrize("name", list(_norms()))
+def test_norm_takes_slices(lib, name):
+    """Rows, and tokens of several heads, of a wider tensor, x and gate each."""
+    call, want = _norms()[name]
+    call()
+    (_, args), = lib.calls
+    assert args[6:11] == want
+
+
+def test_norm_refuses_what_is_not_rows(lib):
+    for x in (cuda(64, 6).t(), cuda(4, 5, 64).transpose(0, 1), cuda(4, 64).expand(4, 64)[:, ::2]):
+        with pytest.raises(ValueError, match="x's"):
+            gdn.gdn_gated_norm(x, cuda(x.shape[-1]))
+    with pytest.raises(ValueError, match="gate's"):
+        gdn.gdn_gated_norm(cuda(6, 64), cuda(64), gate=cuda(64, 6).t())
+    assert not lib.calls
