@@ -394,8 +394,8 @@ gdn_status gqa_repeat_tiled(const void *src, void *dst,
  * a draft are the `accepted` counts of the replay calls.  The conventions
  * above hold, and:
  *   - Inputs that a layer has as slices of a wider projection may have
- *     strides (in elements) on their outer dimensions; the inner dimensions
- *     are dense.  A stride below the inner size is
+ *     strides (in elements) on their outer dimensions, in either order; the
+ *     inner dimensions are dense.  Strides that let rows overlap are
  *     GDN_ERR_INVALID_ARGUMENT.
  *   - `lengths` ([B] int32, DEVICE memory, or NULL for T) is the number of
  *     steps that a sequence has; an entry < 0 acts as 0, an entry > T as T.

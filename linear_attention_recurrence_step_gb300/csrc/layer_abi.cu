@@ -13,15 +13,16 @@ using namespace gdn::abi;
 namespace {
 
 // Elements from the first to the last of a [n0,n1,inner] tensor whose first
-// two strides are given (inner dense), or -1: a stride below what keeps its
-// rows apart, or an overflow.
+// two strides are given (inner dense; either of them may be the outer one), or
+// -1: strides that do not keep its rows apart, or an overflow.
 int64_t extent(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t inner) {
-    if ((n1 > 1 && s1 < inner) || s1 < 0 || s0 < 0) return -1;
+    if (s1 < 0 || s0 < 0) return -1;
     int64_t e0, e1, e;
     if (!mul_ok(n0 - 1, s0, &e0) || !mul_ok(n1 - 1, s1, &e1)) return -1;
     if (__builtin_add_overflow(e0, e1, &e) || __builtin_add_overflow(e, inner, &e)) return -1;
-    if (n0 > 1 && s0 < e1 + inner) return -1;
-    return e;
+    const bool first_outer = (n0 == 1 || s0 >= e1 + inner) && (n1 == 1 || s1 >= inner);
+    const bool second_outer = (n0 == 1 || s0 >= inner) && (n1 == 1 || s1 >= e0 + inner);
+    return first_outer || second_outer ? e : -1;
 }
 
 bool over(const void *a, int64_t na, const void *b, int64_t nb) { return a && b && overlap(a, na, b, nb); }

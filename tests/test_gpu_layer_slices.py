@@ -40,3 +40,21 @@ def test_norm_rows_of_a_projection(dev, dtype, lead, D, wide, first):
                 assert torch.equal(got.residual_out, want.residual_out)
             if not (D * x.element_size() % 16 or wide * x.element_size() % 16 or first * x.element_size() % 16):
                 assert torch.equal(got.y, want.y)
+
+
+@pytest.mark.parametrize("T,C,dtype", [(1, 64, "bf16"), (9, 96, "f32"), (70, 33, "f16"), (300, 256, "bf16")])
+def test_steps_before_sequences(dev, T, C, dtype):
+    """x, dt, B and C laid out [T,B,...]: the convolution and both forms of the
+    scan."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    B = 3
+    mk = lambda *inner: torch.randn(T, B, *inner, generator=gen, device=dev).to(torch_dtype(dtype)).transpose(0, 1)  # noqa: E731
+    lens = torch.tensor([T, T // 2, 0], dtype=torch.int32, device=dev)
+    x, w = mk(C), torch.randn(C, 4, generator=gen, device=dev).to(torch_dtype(dtype))
+    a, b = (gdn.gdn_causal_conv(t, w, lengths=lens) for t in (x, x.contiguous()))
+    on = torch.arange(T, device=dev) < lens[:, None]
+    assert torch.equal(a.y[on], b.y[on]) and torch.equal(a.state_out, b.state_out)
+    H, P, N = 2, 64, 64
+    ins = (mk(H, P), mk(H), -torch.rand(H, generator=gen, device=dev), mk(1, N), mk(1, N))
+    a, b = (gdn.gdn_selective_scan(*(t.contiguous() if dense else t for t in ins), lengths=lens) for dense in (False, True))
+    assert torch.equal(a.y[on], b.y[on]) and torch.equal(a.state_out, b.state_out)

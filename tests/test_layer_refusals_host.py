@@ -37,3 +37,27 @@ def test_outputs_beside_small_inputs(lib):  # noqa: F811
             assert call(lib, **kw) == CUDA  # accepted: it got as far as the launch
     finally:
         assert lib.gdn_force_launch_failures(0) == OK
+
+
+# strides of tensors that hold the steps of all sequences together, [T,B,...]
+TIME_MAJOR = [(conv, dict(sb=64, st=128)), (conv, dict(sb=100, st=264)),
+              (scan, dict(strides=(256, 512, 4, 8, 256, 512, 256, 512))),
+              (scan, dict(strides=(256, 512, 12, 4, 768, 256, 256, 512))),
+              (conv, dict(B=1, sb=0)), (conv, dict(T=1, st=0, sb=64))]
+
+
+def test_steps_may_be_the_outer_dimension(lib):  # noqa: F811
+    try:
+        assert lib.gdn_force_launch_failures(len(TIME_MAJOR)) == OK
+        for call, kw in TIME_MAJOR:
+            assert call(lib, **kw) == CUDA, kw
+    finally:
+        assert lib.gdn_force_launch_failures(0) == OK
+
+
+@pytest.mark.parametrize("kw", [dict(sb=63, st=128), dict(sb=64, st=127), dict(sb=128, st=64), dict(sb=0, st=128),
+                                dict(sb=64, st=0), dict(sb=1 << 62, st=64, B=4), dict(sb=64, st=1 << 62)],
+                         ids=lambda kw: f"{kw['sb']}-{kw['st']}")
+def test_rows_that_overlap_are_refused(lib, kw):  # noqa: F811
+    assert conv(lib, **kw) == INVALID
+    assert b"strides" in lib.gdn_last_error()
