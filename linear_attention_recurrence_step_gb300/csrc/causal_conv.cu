@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kConvThreads, W <= 4 ? 4 : 2) conv_kernel(cons
     }
     if (!a.y) return;
     // the next batch of steps is on its way while one is worked on
-    int left = (int)(t1 - t0);
-    if (left <= 0) return;
+    if (t1 <= t0) return;
+    int left = (int)(t1 - t0);  // run at most
     const T *px = x + t0 * a.x_st;
     T *py = static_cast<T *>(a.y) + (b * a.T + t0) * a.C + c;
     RawPiece<T, VEC> raw[BATCH];

@@ -432,6 +432,11 @@ cudaError_t cudaLaunchKernelEx(const cudaLaunchConfig_t *cfg, void (*kernel)(K..
 
 // what common.cuh gives the kernels
 namespace gdn {
+template <typename... K, typename... A>
+cudaError_t launch_dependent(void (*kernel)(K...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A &&...args) {
+    cudaLaunchConfig_t cfg{dim3(grid), dim3(block), smem, st, nullptr, 0};
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 inline void pdl_wait() {}
 inline void pdl_trigger() {}
 template <typename T> struct Elem;
