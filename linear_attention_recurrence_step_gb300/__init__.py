@@ -240,6 +240,13 @@ def _need(t: torch.Tensor, name: str, shape, dtype, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+def _need_workspace(t, device) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+
+
 def gdn_step_record(q, k, v, g, beta, state_in, mask=None, *, y=None, state_out=None,
                     delta_log=None, k_log=None, g_log=None, capture_tape: bool = False,
                     gqa: str = "block", stream=None) -> RecordOutputs:
@@ -368,8 +375,7 @@ def gdn_chunk_prefill(q, k, v, g, beta, state_in, mask=None, *, y=None, state_ou
     need = gdn_chunk_prefill_workspace_size(B, T, Hv)
     if workspace is None:
         workspace = _empty(need, torch.uint8, dev, stream)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    _need_workspace(workspace, dev)
     st = load().gdn_chunk_prefill(
         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_in), _ptr(mask), _ptr(y),
         _ptr(state_out), _ptr(delta_log), _ptr(k_log), _ptr(g_log), B, T, Hk, Hv, Dk, Dv,
@@ -462,8 +468,7 @@ def gdn_chunk_replay(delta_log, k_log, g_log, state_in, mask=None, *, accepted,
     need = gdn_chunk_replay_workspace_size(B, T, Hv, Dk, Dv)
     if workspace is None:
         workspace = _empty(need, torch.uint8, dev, stream)
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    _need_workspace(workspace, dev)
     st = load().gdn_chunk_replay(
         _ptr(delta_log), _ptr(k_log), _ptr(g_log), _ptr(state_in), _ptr(mask), _ptr(state_out),
         B, T, Hv, Dk, Dv, int(accepted), _ptr(per_seq), _ptr(workspace),

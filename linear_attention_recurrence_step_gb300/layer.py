@@ -23,7 +23,7 @@ import torch
 
 import linear_attention_recurrence_step_gb300 as _pkg
 
-from . import DTYPE_CODES, _check, _empty, _need, load
+from . import DTYPE_CODES, _check, _empty, _need, _need_workspace, load
 
 ConvOutputs = namedtuple("ConvOutputs", "y state_out")
 ScanOutputs = namedtuple("ScanOutputs", "y state_out")
@@ -65,7 +65,7 @@ def _device_of(t, name):
     try:
         if t.dtype in DTYPE_CODES and t.is_cuda:
             dev = t.get_device()
-            if _pkg._is_current(dev):
+            if _pkg._one_device or _pkg._is_current(dev):
                 return dev
             raise _pkg._other_device(dev)
     except AttributeError:
@@ -73,6 +73,15 @@ def _device_of(t, name):
     if t.dtype not in DTYPE_CODES:
         raise ValueError(f"unsupported dtype {t.dtype}")
     raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
+
+
+def _shape(t, name, dims, what):
+    """The shape of a tensor of `dims` dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {what} (shape {tuple(t.shape)})")
+    return t.shape
 
 
 def _strided(t, name, shape, dtype, dev):
@@ -142,8 +151,12 @@ def gdn_causal_conv(x, weight, state_in=None, *, bias=None, lengths=None, activa
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(map(str, ACTIVATIONS))}")
     dt = x.dtype
-    B, T, C = x.shape
-    W = weight.shape[1]
+    try:
+        B, T, C = x.shape
+        _, W = weight.shape
+    except (AttributeError, ValueError):
+        B, T, C = _shape(x, "x", 3, "[B,T,C]")
+        W = _shape(weight, "weight", 2, "[C,W]")[1]
     sb, st = _strided(x, "x", (B, T, C), dt, dev)
     if write_y:
         if y is None:
@@ -186,8 +199,12 @@ def gdn_selective_scan(x, dt, A, B, C, state_in=None, *, D=None, dt_bias=None, s
     allocated when not given."""
     dev = _device_of(x, "x")
     et = x.dtype
-    nb, T, H, P = x.shape
-    G, N = B.shape[2], B.shape[3]
+    try:
+        nb, T, H, P = x.shape
+        _, _, G, N = B.shape
+    except (AttributeError, ValueError):
+        nb, T, H, P = _shape(x, "x", 4, "[B,T,H,P]")
+        _, _, G, N = _shape(B, "B", 4, "[B,T,G,N]")
     strides = _ScanStrides(*_strided(x, "x", (nb, T, H, P), et, dev), *_strided(dt, "dt", (nb, T, H), et, dev),
                            *_strided(B, "B", (nb, T, G, N), et, dev), *_strided(C, "C", (nb, T, G, N), et, dev))
     if write_y:
@@ -202,8 +219,8 @@ def gdn_selective_scan(x, dt, A, B, C, state_in=None, *, D=None, dt_bias=None, s
         need = _scan_workspace(nb, T, H, P, N)
         if need > 16:
             workspace = _empty(need, torch.uint8, x.device, stream)
-    elif workspace.device != x.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    else:
+        _need_workspace(workspace, x.device)
     f32 = torch.float32
     status = _lib().gdn_selective_scan(
         x.data_ptr(), dt.data_ptr(), _dense(A, "A", (H,), f32, dev), B.data_ptr(), C.data_ptr(),
@@ -233,20 +250,27 @@ def gdn_gated_norm(x, weight, *, gate=None, gate_first: bool = False, residual=N
     dt, shape = x.dtype, x.shape
     if not isinstance(weight, torch.Tensor) or weight.dim() not in (1, 2):
         raise ValueError("weight must be a tensor [D] or [K,D]")
+    if not shape:
+        raise ValueError("x must be [..., D]")
     D = shape[-1]
     per_head = weight.dim() == 2
-    if gate is not None and (gate.shape != shape or gate.dtype is not dt or gate.get_device() != dev):
-        _need(gate.contiguous() if gate.device == x.device else gate, "gate", shape, dt, x.device)
+    if gate is not None and (not isinstance(gate, torch.Tensor) or gate.shape != shape or gate.dtype is not dt
+                             or gate.get_device() != dev):
+        _need(gate.contiguous() if isinstance(gate, torch.Tensor) and gate.device == x.device else gate, "gate", shape,
+              dt, x.device)
     # a shared weight: rows [..., D], if x and gate are both that; else tokens of
     # K heads each [..., K, D]
-    K, xs = 1, None if per_head else _rows(x, "x", 1, len(shape) < 2)
-    gs = xs if gate is None or xs is None else _rows(gate, "gate", 1, len(shape) < 2)
-    if gs is None:
-        if len(shape) < 2:
-            raise ValueError("x must be [..., K, D]")
-        K = shape[-2]
-        xs = _rows(x, "x", 2)
-        gs = xs if gate is None else _rows(gate, "gate", 2)
+    if not per_head and x.is_contiguous() and (gate is None or gate.is_contiguous()):
+        K, xs, gs = 1, D, D
+    else:
+        K, xs = 1, None if per_head else _rows(x, "x", 1, len(shape) < 2)
+        gs = xs if gate is None or xs is None else _rows(gate, "gate", 1, len(shape) < 2)
+        if gs is None:
+            if len(shape) < 2:
+                raise ValueError("x must be [..., K, D]")
+            K = shape[-2]
+            xs = _rows(x, "x", 2)
+            gs = xs if gate is None else _rows(gate, "gate", 2)
     M = x.numel() // (K * D) if x.numel() else 0
     if y is None:
         y = _empty(shape, dt, x.device, stream)
@@ -283,6 +307,8 @@ def gdn_sample(logits, noise, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     probability under the softmax at the row's temperature, before the cuts."""
     dev = _device_of(logits, "logits")
     dt, shape = logits.dtype, logits.shape
+    if not shape:
+        raise ValueError("logits must be [..., V]")
     V, lead = shape[-1], shape[:-1]
     ls = _rows(logits, "logits", 1)
     if not isinstance(noise, torch.Tensor) or noise.shape != shape or noise.dtype is not torch.float32 \

@@ -181,3 +181,36 @@ def test_norm_refuses_what_is_not_rows(lib):
     with pytest.raises(ValueError, match="gate's"):
         gdn.gdn_gated_norm(cuda(6, 64), cuda(64), gate=cuda(64, 6).t())
     assert not lib.calls
+
+
+def _wrong_arguments():
+    x, w, v, g = cuda(2, 20, 64), cuda(64, 4), cuda(2, 20, 2, 64), cuda(2, 20, 2)
+    bc, A = cuda(2, 20, 1, 64), cuda(2)
+    conv, scan, norm, sample = gdn.gdn_causal_conv, gdn.gdn_selective_scan, gdn.gdn_gated_norm, gdn.gdn_sample
+    calls = {
+        "conv x list": lambda: conv([1.0], w), "conv x flat": lambda: conv(x[0], w),
+        "conv weight list": lambda: conv(x, [1.0]), "conv weight flat": lambda: conv(x, w[:, 0]),
+        "conv weight none": lambda: conv(x, None), "conv bias list": lambda: conv(x, w, bias=[0.0]),
+        "conv lengths list": lambda: conv(x, w, lengths=[1, 2]), "conv state list": lambda: conv(x, w, [0.0]),
+        "scan x flat": lambda: scan(x, g, A, bc, bc), "scan dt none": lambda: scan(v, None, A, bc, bc),
+        "scan B none": lambda: scan(v, g, A, None, bc), "scan B flat": lambda: scan(v, g, A, x, x),
+        "scan C list": lambda: scan(v, g, A, bc, [1]), "scan A list": lambda: scan(v, g, [1.0, 2.0], bc, bc),
+        "scan D number": lambda: scan(v, g, A, bc, bc, D=1.0), "scan workspace": lambda: scan(v, g, A, bc, bc, workspace=4096),
+        "norm x number": lambda: norm(cuda()[()], cuda(1)), "norm weight list": lambda: norm(x, [1.0]),
+        "norm gate list": lambda: norm(x, cuda(64), gate=[1.0]), "norm gate number": lambda: norm(x, cuda(64), gate=2.0),
+        "norm residual list": lambda: norm(x, cuda(64), residual=[0.0]),
+        "norm residual_out": lambda: norm(x, cuda(64), residual=x, residual_out=1),
+        "sample logits number": lambda: sample(cuda()[()], cuda()), "sample noise list": lambda: sample(x, [1.0]),
+        "sample top_k list": lambda: sample(x, x, top_k=[1]), "sample temperature none": lambda: sample(x, x, temperature=None),
+        "sample token list": lambda: sample(x, x, token=[0]),
+        "prefill workspace": lambda: gdn.gdn_chunk_prefill(v, v, v, g, g, cuda(2, 2, 64, 64), workspace=4096),
+        "replay workspace": lambda: gdn.gdn_chunk_replay(v, v, g, cuda(2, 2, 64, 64), accepted=1, workspace=[0]),
+    }
+    return calls
+
+
+@pytest.mark.parametrize("name", list(_wrong_arguments()))
+def test_wrong_arguments_are_type_or_value_errors(lib, name):
+    with pytest.raises((TypeError, ValueError)):
+        _wrong_arguments()[name]()
+    assert not lib.calls
