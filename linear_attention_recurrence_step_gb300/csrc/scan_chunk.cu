@@ -181,15 +181,16 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
     auto decays = [&](int c) {
         const int64_t t = t_begin + (int64_t)c * kL + lane;
         ChunkDecay &d = sdec[c & 1];
-        float dl = 0.f;
+        // (steps past the end have no size, and no decay whatever the rate)
+        float dl = 0.f, l2 = 0.f;
         const float size = next_size;
         next_size = step_size(c + (warps > 1 ? 2 : 1));
         if (t < t_end) {
             const float v = size + bias;
             dl = a.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+            l2 = dl * A2;
         }
         // a decay below 2^-256 is zero in f32
-        const float l2 = dl * A2;
         double ct = l2 < -256.f ? -256.0 : (double)l2;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
