@@ -457,9 +457,10 @@ gdn_status gdn_causal_conv(const void *x, const void *weight, const void *bias,
  * The state and all sums are float32 and results do not change from run to
  * run.  bf16 calls of 32 steps or more with N of 64 or 128, P a multiple of 8
  * and 16-byte aligned rows take 32 steps at a time on the tensor cores: the
- * state stays as accurate as float32, the state's and the decay products' part
- * of y is off by 2^-18 of its terms at most before y is rounded, and an
- * infinity or NaN among a sequence's inputs may show in y from the start of its
+ * state stays as accurate as float32, the part of y that comes through the
+ * state from before those steps is off by 2^-17 of its terms at most before y
+ * is rounded (2^-16 in a call that is split along its steps), and an infinity
+ * or NaN among a sequence's inputs may show in y from the start of its
  * 32 steps on.  One kernel, or three where a long call is split along its
  * steps.
  */

@@ -18,19 +18,22 @@
 //
 // Precision: x, B and C enter as they are (bf16).  The weighted x, which goes
 // into the state, enters as three bf16 terms (24 significant bits: f32's own),
-// and the state is only ever scaled and added to in f32 (two terms where the
-// state goes into y alone, in a second pass).  The state and W as
-// operands of y enter as two terms (16 bits): their products carry a relative
-// error of at most 2^-18, a thousandth of what rounding y to bf16 costs.  c_t
-// is summed in f64 and kept as two f32 terms, so that exp(c_t - c_s) loses
-// nothing to a chunk's large |c|.
+// and the state is only ever scaled and added to in f32; W enters as three
+// terms too.  Two terms are taken where it costs most and only y sees it: the
+// state as an operand of y (its third term would cost 12 us of the 134 below),
+// and the weighted x in the second pass over a split call (8 us).  Two terms
+// are off by 2^-17 of a value at most, so the part of y that comes through the
+// state is off by 2^-17 of its terms, 2^-16 in a split call, where rounding y
+// to bf16 costs 2^-9.  (W in two terms saved 3 us and moved one y in 1700 to
+// its neighbour.)  c_t is summed in f64 and kept as two f32 terms, so that
+// exp(c_t - c_s) loses nothing to a chunk's large |c|.
 //
 // A call with few heads is split along the steps as in selective_scan.cu: a
 // first pass forms the segments' end states (the last product alone), and the
 // output pass starts every segment from the state after the one before it.
 //
-// Measured (one sequence of 4096 steps, 32 heads of 128 x 128): 130.5 us, of
-// which the first pass takes 50, the join 9 and the output pass 72; the step
+// Measured (one sequence of 4096 steps, 32 heads of 128 x 128): 134 us, of
+// which the first pass takes 50, the join 9 and the output pass 75; the step
 // form takes 614 us on f32 inputs of that size.  Chunks of 64 steps, one CTA
 // per SM, took 139 us: more of the products lies above the diagonal and nothing
 // else runs while a CTA waits for its W.  What bounds it: the warps' issue of
@@ -59,14 +62,14 @@ struct ChunkDecay {
 __host__ __device__ constexpr int bc_pitch(int N) { return N + 8; }
 __host__ __device__ constexpr int x_pitch(int warps) { return warps * 16 + 8; }
 
-// Shared memory (bytes): two stages of x, B, C; W (hi, lo); two decay blocks;
+// Shared memory (bytes): two stages of x, B, C; W (hi, mid, lo); two decay blocks;
 // y tiles, unless they fit over a stage's C
 __host__ __device__ constexpr size_t stage_bytes(int N, int warps) {
     return (size_t)kL * (x_pitch(warps) + 2 * bc_pitch(N)) * 2;
 }
 __host__ __device__ constexpr bool y_over_c(int N, int warps) { return warps * kL * 16 <= kL * bc_pitch(N); }
 __host__ __device__ constexpr size_t chunk_smem(int N, int warps) {
-    return 2 * stage_bytes(N, warps) + 2 * (size_t)kL * kWPitch * 2 + 2 * sizeof(ChunkDecay) +
+    return 2 * stage_bytes(N, warps) + 3 * (size_t)kL * kWPitch * 2 + 2 * sizeof(ChunkDecay) +
            (y_over_c(N, warps) ? 0 : (size_t)warps * kL * 16 * 2);
 }
 
@@ -110,10 +113,10 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
     const int XP = x_pitch(warps);
     const uint32_t stage = (uint32_t)stage_bytes(N, warps);
     const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
-    const uint32_t sW = smem + 2 * stage;                               // hi, then lo
+    const uint32_t sW = smem + 2 * stage;                               // hi, mid, lo
     constexpr uint32_t kWBytes = kL * kWPitch * 2;
-    ChunkDecay *const sdec = reinterpret_cast<ChunkDecay *>(smem_raw + 2 * stage + 2 * kWBytes);
-    const uint32_t sYown = sW + 2 * kWBytes + 2 * (uint32_t)sizeof(ChunkDecay);
+    ChunkDecay *const sdec = reinterpret_cast<ChunkDecay *>(smem_raw + 2 * stage + 3 * kWBytes);
+    const uint32_t sYown = sW + 3 * kWBytes + 2 * (uint32_t)sizeof(ChunkDecay);
     auto sx = [&](int b) { return smem + b * stage; };
     auto sB = [&](int b) { return sx(b) + kL * XP * 2; };
     auto sC = [&](int b) { return sB(b) + kL * BP * 2; };
@@ -286,10 +289,12 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
                 for (int r = 0; r < 2; ++r) {
                     const int t = t0 + 8 * r;
                     const float2 ct = d.c[t];
-                    uint32_t hi, lo;
-                    split_bf16x2(wt(G[2 * r], ct, cs0, dl0, t, s0), wt(G[2 * r + 1], ct, cs1, dl1, t, s0 + 1), hi, lo);
+                    uint32_t hi, mid, lo;
+                    split3(wt(G[2 * r], ct, cs0, dl0, t, s0), wt(G[2 * r + 1], ct, cs1, dl1, t, s0 + 1), hi, mid,
+                           lo);
                     put_pair(sW + (t * kWPitch + s0) * 2, hi);
-                    put_pair(sW + kWBytes + (t * kWPitch + s0) * 2, lo);
+                    put_pair(sW + kWBytes + (t * kWPitch + s0) * 2, mid);
+                    put_pair(sW + 2 * kWBytes + (t * kWPitch + s0) * 2, lo);
                 }
             }
             // S C^T: the state's accumulators are the left operand
@@ -341,12 +346,12 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
 #pragma unroll
                 for (int j = 2 * ks; j < kL / 8; j += 2) {
                     uint32_t wb[4];
-                    ldsm_x4_a(wb, w_cols + (j * 8 * kWPitch + ks * 16) * 2);
-                    mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
-                    mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
-                    ldsm_x4_a(wb, w_cols + kWBytes + (j * 8 * kWPitch + ks * 16) * 2);
-                    mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
-                    mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k) {  // lo first
+                        ldsm_x4_a(wb, w_cols + k * kWBytes + (j * 8 * kWPitch + ks * 16) * 2);
+                        mma_bf16_16816(Y[j], xa, wb[0], wb[1]);
+                        mma_bf16_16816(Y[j + 1], xa, wb[2], wb[3]);
+                    }
                 }
             }
             // weighted by w_t
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(256, 2) scan_chunk_kernel(const ScanArgs a, co
             }
         }
         if constexpr (OUT) {
-            // y: the warp's 16 rows turned into 64 rows of 16 (32 bytes; the two
+            // y: the warp's 16 rows turned into 32 rows of 16 (32 bytes; the two
             // 16-byte halves swap places every fourth row against bank conflicts)
             const uint32_t ys = (y_over_c(N, warps) ? Cs : sYown) + warp * kL * 32;
 #pragma unroll
