@@ -406,6 +406,11 @@ gdn_status gqa_repeat_tiled(const void *src, void *dst,
  *   - Pointers need the alignment of their element type unless 16 bytes are
  *     asked for; 16-byte aligned rows take the vector paths.
  *   - An output must not overlap an input, except where a call says so.
+ *   - silu, the decays of the scan's tensor-core form and sampling's
+ *     exponentials use the hardware's approximate float32 functions: silu(v) is
+ *     within 8 + 2 |v| units (2^-24) of its value, a logprob within 2e-5 and 4
+ *     units of its own.  The cut by min_p and the race compare exact float32
+ *     exponentials.
  */
 typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
 

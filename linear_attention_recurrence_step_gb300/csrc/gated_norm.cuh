@@ -9,9 +9,9 @@
 // behind, so what is known at launch (gate, residual, dense rows) is known to
 // the compiler, and pairs of elements share packed instructions.
 //
-// Measured: 4096 x 32 rows of 128 in bf16 with a gate 18.7 us (5.4 TB/s),
-// 1000 rows of 5001 in f32 with a residual 16.9 us (4.7 TB/s; rows that
-// straddle 16-byte boundaries), 16 x 32 rows 1.9 us.
+// Measured: 4096 x 32 rows of 128 in bf16 with a gate 18.4 us (5.5 TB/s),
+// 1000 rows of 5001 in f32 with a residual 16.6 us (4.8 TB/s; rows that
+// straddle 16-byte boundaries), 16 x 32 rows 1.7 us.
 //
 // A row stays in registers between its sum and its scaling.  TPR threads share
 // a row: eight of them a head of 128, a block a wide row; each holds NV pieces
@@ -256,6 +256,9 @@ cudaError_t launch_rows(const NormArgs &a, int sm_count, cudaStream_t s) {
         if (n <= 2048) return launch_cfg<T, ROWS, GATE, RES, 256, 8>(a, s);
         if (n <= 8192) return launch_cfg<T, ROWS, GATE, RES, 1024, 8>(a, s);
     } else {
+        // (up to 1344 pieces by 448 threads: 4096 bf16 rows of 8192 with a gate take
+        // 40.2 us so, 62.7 us by 512 threads of four pieces, and 43.0 and 42.2 us with
+        // a residual instead; 1000 f32 rows of 5001 16.7 and 16.9 us)
         if (n <= 768) return launch_cfg<T, ROWS, GATE, RES, 256, 3>(a, s);
         if (n <= 1344) return launch_cfg<T, ROWS, GATE, RES, 448, 3>(a, s);
         if (n <= 2048) return launch_cfg<T, ROWS, GATE, RES, 512, 4>(a, s);

@@ -34,9 +34,9 @@
 // looked at: results do not change from run to run.  The noise is read
 // only for tokens that are left.
 //
-// What bounds it: one row of 32000 f32 with top-k 50 takes 11.7 us, about ten
+// What bounds it: one row of 32000 f32 with top-k 50 takes 11.6 us, about ten
 // exchanges over the block and two over the cluster one after another.  128
-// rows of 131072 bf16 with the three cuts take 81 us (a tenth of the copy
+// rows of 131072 bf16 with the three cuts take 79 us (a tenth of the copy
 // rate): passes over shared memory, the list and the race of the rows with a
 // top-p cut.  256 rows of 100003 uncut take 58 us (2.6 TB/s): two passes, the
 // race waiting for the row's maximum.  A single pass over logits and noise in
@@ -1428,8 +1428,8 @@ cudaError_t launch_t(const SampleArgs &a, int sm_count, cudaStream_t s) {
     auto bytes_of = [&](int cs) { return kSharedBytes + (size_t)(slice_of(cs) + VE) * sizeof(T); };
     // A row over as few CTAs as leave room for two of them on an SM, so that
     // one loads while another computes; over more while SMs would stay idle.
-    // 128 x 131072 bf16 with the three cuts over slices of up to 112 KB: 81 us;
-    // 200 KB: 102 us, 60 KB: 94 us; 256 x 100003 uncut 58, 75 and 79 us.  One row
+    // 128 x 131072 bf16 with the three cuts over slices of up to 112 KB: 79 us;
+    // 200 KB: 98 us, 60 KB: 94 us; 256 x 100003 uncut 58, 75 and 79 us.  One row
     // of 32000 f32 with top-p over slices down to 4096: 19.3 us, to 16384:
     // 25.3 us, to 2048: no change.
     int cs = 1;

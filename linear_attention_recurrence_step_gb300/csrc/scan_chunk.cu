@@ -21,7 +21,7 @@
 // and the state is only ever scaled and added to in f32; W enters as three
 // terms too.  Two terms are taken where it costs most and only y sees it: the
 // state as an operand of y (its third term would cost 12 us of the 134 below),
-// and the weighted x in the second pass over a split call (8 us).  Two terms
+// and the weighted x in the second pass over a split call (11 us).  Two terms
 // are off by 2^-17 of a value at most, so the part of y that comes through the
 // state is off by 2^-17 of its terms, 2^-16 in a split call, where rounding y
 // to bf16 costs 2^-9.  (W in two terms saved 3 us and moved one y in 1700 to
@@ -37,8 +37,9 @@
 // form takes 614 us on f32 inputs of that size.  Chunks of 64 steps, one CTA
 // per SM, took 139 us: more of the products lies above the diagonal and nothing
 // else runs while a CTA waits for its W.  What bounds it: the warps' issue of
-// about 190 mma.sync and their operand loads per chunk (tensor pipe 45 % of
-// its cycles, issue slots 42 %), between the barriers around W and the decays.
+// about 150 mma.sync (190 in a call that is not split) and their operand loads
+// per chunk (tensor pipe 45 % of its cycles, issue slots 44 %), between the
+// barriers around W and the decays.
 #include "layer.h"
 #include "pieces.cuh"
 #include "record_mma.cuh"

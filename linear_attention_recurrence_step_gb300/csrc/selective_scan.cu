@@ -365,7 +365,7 @@ cudaError_t launch_scan_join(const ScanArgs &a, cudaStream_t s) {
 bool scan_supported_n(int64_t N) { return N == 16 || N == 32 || N == 64 || N == 128 || N == 256; }
 
 // From one whole chunk on: 16 sequences of 32 steps, 32 heads of 128 x 128, take
-// 27.6 us in chunks, 48.5 us by steps; one sequence 8.6 and 13.9 us.
+// 27.0 us in chunks, 48.2 us by steps; one sequence 8.4 and 13.6 us.
 bool scan_chunk_sizes(DType dt, int64_t T, int64_t P, int64_t N) {
     return dt == DType::BF16 && (N == 64 || N == 128) && P % 8 == 0 && T >= 32;
 }
@@ -374,8 +374,8 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
     ScanPlan plan{1, T, 0};
     int64_t row_blocks = 1;
     // CTAs that fill 152 SMs, and the fewest steps of a segment (128 instead of
-    // 64 at 512 steps of 32 heads of 128 x 128: 47 us instead of 34 in the chunk
-    // form, 162 instead of 96 by steps)
+    // 64 at 512 steps of 32 heads of 128 x 128: 49 us instead of 35 in the chunk
+    // form, 161 instead of 93 by steps)
     double target = 608.0;
     const int64_t least = 64;
     int64_t unit = kStage;
@@ -396,8 +396,8 @@ ScanPlan scan_plan(int64_t B, int64_t T, int64_t H, int64_t P, int64_t N, bool c
     int64_t want = ctas >= target ? 1 : (int64_t)(target / ctas);
     if (want > T / least) want = T / least;
     // Three kernels instead of one pay for themselves from 256 steps on in the
-    // chunk form (one sequence, 32 heads of 128 x 128: 31 us split in four, 32 us
-    // whole; 27 and 18.5 us at 128 steps, 34 and 58 us at 512).
+    // chunk form (one sequence, 32 heads of 128 x 128: 31.3 us split in four, 31.8 us
+    // whole; 26 and 18.4 us at 128 steps, 35 and 59 us at 512).
     if (chunked && T < 256) want = 1;
     if (want > 64) want = 64;
     if (want > 1) {
