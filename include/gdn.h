@@ -549,6 +549,181 @@ gdn_status gdn_sample(const void *logits, const float *noise,
                       int64_t logits_stride, int64_t noise_stride,
                       gdn_dtype dtype, gdn_stream_t stream);
 
+/*
+ * The operators of an attention layer.  A hybrid model puts attention layers
+ * between its recurrent ones; their keys and values stay in pages of 4-bit
+ * values.  In a serving step gdn_page_slots finds the pages and places of the
+ * new tokens from the requests' lengths, gdn_rotary turns queries and keys,
+ * gdn_kv_append writes keys and values to their places and gdn_kv_attention
+ * reads them; gdn_kv_read gives them back.  The conventions above hold, and
+ * those of the operators around the recurrence on strides, alignment and
+ * overlap.
+ *
+ * The cache is [pages, H, page, 9 D/8] bytes for H key heads of D channels (D
+ * of 64, 128 or 256; page, the tokens of a page, of 16, 32, 64 or 128), 16-byte
+ * aligned.  Page and head make one block: the keys' codes [page, D/2] (element
+ * 2i in the low half of byte i), the keys' scales [page, D/16], the values'
+ * codes and the values' scales.  16 neighbouring channels of a token share a
+ * scale s, an e4m3 byte; a code is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and, in bit
+ * 3, the sign), and an element's value is head scale * s * code, where the
+ * float32 head scales k_scale[H] and v_scale[H] (finite, > 0; NULL: 1) keep s in
+ * its range.  The cache holds finite values: an infinity is written as the
+ * largest value (2688 head scales), a NaN as zero.
+ *
+ * Token j of sequence b stands in place j % page of page block_table[b, j /
+ * page]; its slot is that page * page + j % page, an int32 (so pages * page
+ * < 2^31).  A slot below 0 or past the last page is no slot: its token is not
+ * written and not read.
+ */
+
+/*
+ * gdn_page_slots -- block tables and slots of a step's tokens, from lengths.
+ * Sequence b holds lengths[b] tokens in held[b] pages (more than it needs after
+ * a rollback: to roll back, shorten its length), the first held[b] entries of
+ * its row of block_table, and gets add[b] more:
+ *     need[b] = max(0, ceil((lengths[b] + add[b]) / page) - held[b])
+ * It is served if its row has room for them and need[b] is 0, or need[0] + ... +
+ * need[b] (over sequences whose rows have room) is at most the number of free
+ * pages; then granted[b] = add[b], and 0 if not.  add[b] < 0 ends the sequence:
+ * its pages are free from the next call on, and its length is 0.
+ *
+ * Free pages stand in a ring of `pages` places, ring_state[1] of them from place
+ * ring_state[0] on; pages are taken there in the order of the batch, and those
+ * of ended sequences put behind the last one.
+ *
+ *   lengths, held   [B] int32         add        [B] int32 or NULL (T for each);
+ *                                                above T counts as T
+ *   ring_state      [2] int32         ring       [pages] int32, changed in place
+ *   block_table     [B,width] int32, changed in place: entries held[b] on are
+ *                   filled, no other is written
+ *   slots           [B,T] int32: slot of token lengths[b] + t, -1 for t >=
+ *                   granted[b] (and of an entry that names no page)
+ *   positions       [B,T] int32: lengths[b] + t, -1 for t >= granted[b]
+ *   granted         [B] int32: the `lengths` of the recurrent layers' calls, the
+ *                   `fresh` of gdn_kv_attention
+ *   lengths_out, held_out [B], ring_state_out [2]: after the call; each may be
+ *                   its input's own buffer.  With other buffers a repeated call
+ *                   gives the same results.
+ * Counts that are negative or too large act as the nearest that is possible.
+ * One kernel, two for more than 8192 slots.
+ */
+gdn_status gdn_page_slots(const int32_t *lengths, const int32_t *add,
+                          const int32_t *held, const int32_t *ring_state,
+                          int32_t *block_table, int32_t *ring, int32_t *slots,
+                          int32_t *positions, int32_t *granted,
+                          int32_t *lengths_out, int32_t *held_out,
+                          int32_t *ring_state_out, int64_t B, int64_t T,
+                          int64_t width, int64_t pages, int64_t page,
+                          gdn_stream_t stream);
+
+/* Which channels make a pair, i from 0 to R/2 - 1. */
+typedef enum gdn_rotary_layout {
+    GDN_ROTARY_HALF = 0,       /* i and i + R/2  */
+    GDN_ROTARY_INTERLEAVED = 1 /* 2i and 2i + 1  */
+} gdn_rotary_layout;
+
+/* Batch and step strides, in elements. */
+typedef struct gdn_rotary_strides {
+    int64_t q_b, q_t, k_b, k_t, q_out_b, q_out_t, k_out_b, k_out_t;
+} gdn_rotary_strides;
+
+/*
+ * gdn_rotary -- rotary positions of queries and keys: each pair (x, y) of the
+ * first R channels of every head becomes
+ *     scale * (x cos - y sin,  x sin + y cos),  angle = positions[b,t] * inv_freq[i]
+ * and the channels from R on are copied.  `inverse` turns by minus the angles
+ * (what a gradient takes).
+ *
+ *   q          [B,T,Hq,D] dtype      k  [B,T,Hk,D] dtype or NULL
+ *   positions  [B,T] int32; a token with a negative one is left out: nothing of
+ *              it is written
+ *   inv_freq   [R/2] float32, R even, at most D and 8192 (above:
+ *              GDN_ERR_UNSUPPORTED); frequencies stretched for long contexts
+ *              are simply others, with their factor as `scale`
+ *   q_out, k_out  like q and k; each may be its input's own rows (same pointer
+ *              and strides)
+ *   strides    of the four, or NULL (dense)
+ * An angle's fraction of a turn is exact to 2^-32 and 2^-53 of inv_freq per
+ * step for every position; sines and products are float32, rounded once.  One
+ * kernel.
+ */
+gdn_status gdn_rotary(const void *q, const void *k, const int32_t *positions,
+                      const float *inv_freq, void *q_out, void *k_out,
+                      int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                      int64_t R, const gdn_rotary_strides *strides,
+                      gdn_rotary_layout layout, float scale, int inverse,
+                      gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * gdn_kv_append -- writes keys and values to their slots of the cache.  With
+ * u = x / head scale (rounded to float32), each 16 channels get the scale s, the
+ * nearest e4m3 of max|u| / 6 (at most 448), and each of them the nearest e2m1 of
+ * u / s (at most 6); both of the exact quotient, ties to even.
+ *
+ *   k, v     [B,T,H,D] dtype, batch and step strides given
+ *   slots    [B,T] int32; a slot may stand there once (of two tokens with the
+ *            same slot, parts of either may be written)
+ *   cache    in out; only the slots' bytes are written
+ * One kernel.
+ */
+gdn_status gdn_kv_append(const void *k, const void *v, const int32_t *slots,
+                         void *cache, const float *k_scale,
+                         const float *v_scale, int64_t B, int64_t T, int64_t H,
+                         int64_t D, int64_t page, int64_t pages,
+                         int64_t k_stride_b, int64_t k_stride_t,
+                         int64_t v_stride_b, int64_t v_stride_t,
+                         gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * gdn_kv_read -- the keys and values of N slots ([N] int32), as dense [N,H,D]
+ * dtype, rounded to nearest-even.  The rows of a slot that is none are not
+ * written.  One kernel.
+ */
+gdn_status gdn_kv_read(const void *cache, const int32_t *slots,
+                       const float *k_scale, const float *v_scale, void *k,
+                       void *v, int64_t N, int64_t H, int64_t D, int64_t page,
+                       int64_t pages, gdn_dtype dtype, gdn_stream_t stream);
+
+/*
+ * gdn_kv_attention -- attention of new tokens over the cache.  Query token t of
+ * sequence b (t < n, n = fresh[b]) stands at position p = lengths[b] - n + t and
+ * sees the tokens j <= p with j > p - window (window 0: all of them):
+ *     y[b,t,hq] = sum_j softmax_j(scale q . k_j) v_j,  key head hq / (Hq/H)
+ *     lse[b,t,hq] = log sum_j exp(scale q . k_j)
+ * A token that sees nothing (its position is below 0) has y = 0 and lse = -inf.
+ *
+ *   q            [B,T,Hq,D] dtype, batch and step strides given
+ *   block_table  [B,width] int32; an entry that names no page takes its tokens
+ *                out of sight
+ *   lengths      [B] int32: the tokens in the cache, the new ones among them; at
+ *                most width * page count
+ *   fresh        [B] int32 or NULL (T): an entry < 0 acts as 0, > T as T.  y and
+ *                lse are not written at or past it
+ *   y            [B,T,Hq,D] dtype    lse [B,T,Hq] float32 or NULL
+ *   workspace    at least gdn_kv_attention_workspace_size bytes, 16-byte
+ *                aligned, one per call in flight; not looked at when that call
+ *                gives 16
+ * Sums, maxima and outputs are float32, rounded once; the products take the
+ * cache's values exactly, the queries to 2^-23 of their row's largest channel
+ * and the probabilities rounded to f16 (two f16 terms for float32 calls).  A
+ * query row that holds an infinity or a NaN has NaN for y.  What stands in
+ * places that no token sees does not matter.  Results do not change from run to
+ * run.  One kernel, or two where a call's tokens are shared out among blocks.
+ */
+size_t gdn_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq,
+                                       int64_t H, int64_t D);
+
+gdn_status gdn_kv_attention(const void *q, const void *cache,
+                            const int32_t *block_table, const int32_t *lengths,
+                            const int32_t *fresh, const float *k_scale,
+                            const float *v_scale, void *y, float *lse,
+                            int64_t B, int64_t T, int64_t Hq, int64_t H,
+                            int64_t D, int64_t width, int64_t page,
+                            int64_t pages, int64_t q_stride_b,
+                            int64_t q_stride_t, float scale, int64_t window,
+                            void *workspace, size_t workspace_bytes,
+                            gdn_dtype dtype, gdn_stream_t stream);
+
 /* Static name of a status code ("GDN_OK", ...); never NULL. */
 const char *gdn_status_string(gdn_status status);
 

@@ -42,6 +42,17 @@ The operators around the recurrence (``layer.py``, re-exported here):
 * ``gdn_gated_norm`` -- root-mean-square norm with gate and residual sum.
 * ``gdn_sample`` -- temperature, top-k, top-p and min-p sampling from given
   noise.
+
+The operators of an attention layer (``attention.py``, re-exported here):
+
+* ``gdn_page_slots`` -- block tables and slots of a step's tokens from the
+  requests' lengths.
+* ``gdn_rotary`` -- rotary positions of queries and keys;
+  ``rotary_frequencies`` makes their frequencies, also for long contexts.
+* ``gdn_kv_cache``, ``gdn_kv_append``, ``gdn_kv_read`` -- a paged cache of 4-bit
+  keys and values, writing to it and reading it.
+* ``gdn_kv_attention`` -- attention over that cache, for single tokens, drafts
+  and prompts.
 """
 from __future__ import annotations
 
@@ -62,6 +73,9 @@ __all__ = ["GdnError", "build", "load", "lib_path", "gdn_step_record", "gdn_step
            "gdn_state_replay", "gdn_state_replay_per_seq", "gqa_repeat_tiled", "RecordOutputs",
            "gdn_causal_conv", "gdn_selective_scan", "gdn_selective_scan_workspace_size",
            "gdn_gated_norm", "gdn_sample", "ConvOutputs", "ScanOutputs", "NormOutputs", "SampleOutputs",
+           "gdn_page_slots", "gdn_rotary", "rotary_frequencies", "gdn_kv_cache", "gdn_kv_append", "gdn_kv_read",
+           "gdn_kv_attention", "gdn_kv_attention_workspace_size", "SlotOutputs", "RotaryOutputs", "KvOutputs",
+           "AttentionOutputs",
            "STATUS_NAMES", "DTYPE_CODES", "GQA_MAPPINGS"]
 
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -74,7 +88,8 @@ EXPORTED = ("gdn_step_record", "gdn_step_record_mapped", "gdn_chunk_prefill",
             "gdn_state_replay_tstate", "gdn_state_replay",
             "gdn_state_replay_per_seq", "gqa_repeat_tiled", "gdn_causal_conv",
             "gdn_selective_scan_workspace_size", "gdn_selective_scan", "gdn_gated_norm",
-            "gdn_sample", "gdn_status_string",
+            "gdn_sample", "gdn_page_slots", "gdn_rotary", "gdn_kv_append", "gdn_kv_read",
+            "gdn_kv_attention_workspace_size", "gdn_kv_attention", "gdn_status_string",
             "gdn_last_error", "gdn_abi_version", "gdn_wait_status", "gdn_set_wait_bound",
             "gdn_inject_wait_expiry", "gdn_force_launch_failures")
 
@@ -143,6 +158,18 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.gdn_sample.argtypes = [_P] * 6 + [ctypes.c_float, ctypes.c_int32, ctypes.c_float, ctypes.c_float] + \
         [_P] * 2 + [_I] * 4 + [ctypes.c_int, _P]
     lib.gdn_sample.restype = ctypes.c_int
+    lib.gdn_page_slots.argtypes = [_P] * 12 + [_I] * 5 + [_P]
+    lib.gdn_page_slots.restype = ctypes.c_int
+    lib.gdn_rotary.argtypes = [_P] * 6 + [_I] * 6 + [_P, ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_int, _P]
+    lib.gdn_rotary.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [_P] * 6 + [_I] * 10 + [ctypes.c_int, _P]
+    lib.gdn_kv_append.restype = ctypes.c_int
+    lib.gdn_kv_read.argtypes = [_P] * 6 + [_I] * 5 + [ctypes.c_int, _P]
+    lib.gdn_kv_read.restype = ctypes.c_int
+    lib.gdn_kv_attention_workspace_size.argtypes = [_I] * 5
+    lib.gdn_kv_attention_workspace_size.restype = ctypes.c_size_t
+    lib.gdn_kv_attention.argtypes = [_P] * 9 + [_I] * 10 + [ctypes.c_float, _I, _P, ctypes.c_size_t, ctypes.c_int, _P]
+    lib.gdn_kv_attention.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -534,3 +561,6 @@ def force_launch_failures(n: int) -> None:
 
 from .layer import (ConvOutputs, NormOutputs, SampleOutputs, ScanOutputs, gdn_causal_conv,  # noqa: E402
                     gdn_gated_norm, gdn_sample, gdn_selective_scan, gdn_selective_scan_workspace_size)
+from .attention import (AttentionOutputs, KvOutputs, RotaryOutputs, SlotOutputs, gdn_kv_append,  # noqa: E402
+                        gdn_kv_attention, gdn_kv_attention_workspace_size, gdn_kv_cache, gdn_kv_read, gdn_page_slots,
+                        gdn_rotary, rotary_frequencies)

@@ -1,0 +1,178 @@
+// kv_cache.cu -- writing tokens to the 4-bit paged cache and reading them.
+//
+// A group of 16 elements u = x / head scale is held as s * e2m1(u / s) with
+// s = e4m3(max|u| / 6).  Both roundings are to the nearest of the exact
+// quotient: a float32 quotient can fall on a border between two codes only
+// where its remainder says on which side of it the exact one lies.
+//
+// Bound by memory (a read or write of 16 elements and one of 9 bytes); one
+// thread per group, neighbouring threads on neighbouring groups.
+#include "attend.h"
+#include "fp4.cuh"
+#include "pieces.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kKvThreads = 256;
+
+// A quotient a/b >= 0 from its float32 rounding q, moved off q if a/b is not q
+// itself: on the same side of every border that q is not on.
+__device__ __forceinline__ float beside(float q, float a, float b) {
+    const float r = fmaf(-q, b, a);
+    return r > 0.f ? __uint_as_float(__float_as_uint(q) + 1u)
+                   : r < 0.f ? __uint_as_float(__float_as_uint(q) - 1u) : q;
+}
+
+// Where a (token, kv, head, group) of the flat index lies.
+struct Place {
+    int64_t token;
+    int head, group;
+    bool value;
+};
+__device__ __forceinline__ Place place_of(int64_t i, int H, int groups) {
+    Place p;
+    const int per = 2 * H * groups;
+    p.token = i / per;
+    int r = (int)(i - p.token * per);
+    p.value = r >= H * groups;
+    if (p.value) r -= H * groups;
+    p.head = r / groups;
+    p.group = r - p.head * groups;
+    return p;
+}
+// The group's codes and scale in the cache (the slot is valid).
+__device__ __forceinline__ unsigned char *codes_of(const KvArgs &a, int slot, const Place &p, unsigned char **scale) {
+    const int page = 1 << a.page_shift, half = page * a.D / 2;
+    const int64_t block = ((int64_t)(slot >> a.page_shift) * a.H + p.head) * kv_block_bytes(page, a.D);
+    unsigned char *base = a.cache + block + (p.value ? half + page * (a.D / 16) : 0);
+    const int row = slot & (page - 1);
+    *scale = base + half + row * (a.D / 16) + p.group;
+    return base + row * (a.D / 2) + p.group * 8;
+}
+
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvArgs a, int64_t total) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
+    if (i >= total) return;
+    const Place p = place_of(i, a.H, a.D / 16);
+    const int slot = a.slots[p.token];
+    if (slot < 0 || (slot >> a.page_shift) >= a.pages) return;
+    const int64_t b = p.token / a.T, t = p.token - b * a.T;
+    const T *src = static_cast<const T *>(p.value ? a.v_in : a.k_in) + b * (p.value ? a.v_sb : a.k_sb) +
+                   t * (p.value ? a.v_st : a.k_st) + (int64_t)p.head * a.D + p.group * 16;
+    constexpr int VEC = VECTOR ? 16 / (int)sizeof(T) : 1;
+    float u[16];
+#pragma unroll
+    for (int e = 0; e < 16; e += VEC) {
+        float v[VEC];
+        load_piece<T, VEC>(v, src + e);
+#pragma unroll
+        for (int f = 0; f < VEC; ++f) u[e + f] = v[f];
+    }
+    const float *hs = p.value ? a.v_scale : a.k_scale;
+    const float g = hs ? hs[p.head] : 1.f;
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        u[e] = hs ? u[e] / g : u[e];
+        // finite from here on: a NaN is a zero, infinities are the largest value
+        u[e] = u[e] == u[e] ? fminf(fmaxf(u[e], -3.4e38f), 3.4e38f) : 0.f;
+        top = fmaxf(top, fabsf(u[e]));
+    }
+    const uint32_t sb = f32_to_e4m3(beside(top / 6.f, top, 6.f));
+    const float s = f16_lo(e4m3x2_to_f16(sb));
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    uint32_t word[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        float q[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const float m = fabsf(u[e + f]);
+            float x = m * inv;
+            x = fmaf(fmaf(-x, s, m), inv, x);  // the quotient's nearest float
+            if (s > 0.f && sizeof(T) == 4) x = beside(x, m, s);
+            q[f] = copysignf(x, u[e + f]);
+        }
+        word[e / 8] |= f32_to_e2m1x2(q[0], q[1]) << (4 * (e % 8));
+    }
+    unsigned char *scale, *codes = codes_of(a, slot, p, &scale);
+    *reinterpret_cast<uint2 *>(codes) = make_uint2(word[0], word[1]);
+    *scale = (unsigned char)sb;
+}
+
+template <typename T, bool VECTOR>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvArgs a, int64_t total) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
+    if (i >= total) return;
+    const Place p = place_of(i, a.H, a.D / 16);
+    const int slot = a.slots[p.token];
+    if (slot < 0 || (slot >> a.page_shift) >= a.pages) return;
+    unsigned char *scale;
+    const uint2 w = *reinterpret_cast<const uint2 *>(codes_of(a, slot, p, &scale));
+    const float *hs = p.value ? a.v_scale : a.k_scale;
+    const float s = f16_lo(e4m3x2_to_f16(*scale)), g = hs ? hs[p.head] : 1.f;
+    float u[16];
+    const uint32_t word[2] = {w.x, w.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h[4];
+        e2m1x8_to_f16(word[j], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            u[8 * j + 2 * e] = f16_lo(h[e]) * s * g;
+            u[8 * j + 2 * e + 1] = f16_hi(h[e]) * s * g;
+        }
+    }
+    T *dst = static_cast<T *>(p.value ? a.v_out : a.k_out) + (p.token * a.H + p.head) * a.D + p.group * 16;
+    constexpr int VEC = VECTOR ? 16 / (int)sizeof(T) : 1;
+#pragma unroll
+    for (int e = 0; e < 16; e += VEC) {
+        float v[VEC];
+#pragma unroll
+        for (int f = 0; f < VEC; ++f) v[f] = u[e + f];
+        store_piece<T, VEC>(dst + e, v);
+    }
+}
+
+template <typename T>
+cudaError_t launch_append_t(const KvArgs &a, cudaStream_t s) {
+    const int64_t total = a.B * a.T * 2 * a.H * (a.D / 16), blocks = (total + kKvThreads - 1) / kKvThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return a.vec ? launch_dependent(kv_append_kernel<T, true>, (unsigned)blocks, kKvThreads, 0, s, a, total)
+                 : launch_dependent(kv_append_kernel<T, false>, (unsigned)blocks, kKvThreads, 0, s, a, total);
+}
+template <typename T>
+cudaError_t launch_read_t(const KvArgs &a, cudaStream_t s) {
+    const int64_t total = a.B * a.T * 2 * a.H * (a.D / 16), blocks = (total + kKvThreads - 1) / kKvThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return a.vec ? launch_dependent(kv_read_kernel<T, true>, (unsigned)blocks, kKvThreads, 0, s, a, total)
+                 : launch_dependent(kv_read_kernel<T, false>, (unsigned)blocks, kKvThreads, 0, s, a, total);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(DType dt, const KvArgs &a, cudaStream_t s) {
+    switch (dt) {
+    case DType::F32: return launch_append_t<float>(a, s);
+    case DType::BF16: return launch_append_t<__nv_bfloat16>(a, s);
+    case DType::F16: return launch_append_t<__half>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+cudaError_t launch_kv_read(DType dt, const KvArgs &a, cudaStream_t s) {
+    switch (dt) {
+    case DType::F32: return launch_read_t<float>(a, s);
+    case DType::BF16: return launch_read_t<__nv_bfloat16>(a, s);
+    case DType::F16: return launch_read_t<__half>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gdn
