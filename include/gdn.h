@@ -560,8 +560,8 @@ gdn_status gdn_sample(const void *logits, const float *noise,
  * overlap.
  *
  * The cache is [pages, H, page, 9 D/8] bytes for H key heads of D channels (D
- * of 64, 128 or 256; page, the tokens of a page, of 16, 32, 64 or 128), 16-byte
- * aligned.  Page and head make one block: the keys' codes [page, D/2] (element
+ * of 64, 128 or 256, H at most 65535; page, the tokens of a page, of 16, 32, 64
+ * or 128), 16-byte aligned.  Page and head make one block: the keys' codes [page, D/2] (element
  * 2i in the low half of byte i), the keys' scales [page, D/16], the values'
  * codes and the values' scales.  16 neighbouring channels of a token share a
  * scale s, an e4m3 byte; a code is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and, in bit

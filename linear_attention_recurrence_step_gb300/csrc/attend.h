@@ -65,9 +65,12 @@ struct AttendArgs {
     int Hq, H, D, width, page_shift;
     float scale;
     int window;                         // 0: none
+    bool vec_y;                         // y is 16-byte aligned
 };
-constexpr int kAttendRows = 16;         // query rows of a unit
 int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D);
-cudaError_t launch_kv_attend(DType dt, const AttendArgs &a, cudaStream_t s);
+// One translation unit per element type.
+cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_f16(const AttendArgs &a, cudaStream_t s);
 
 }  // namespace gdn

@@ -41,7 +41,7 @@ bool head_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 // The sizes of a cache that slots of int32 can name, in bytes, or -1.
 int64_t cache_bytes(int64_t pages, int64_t H, int64_t page, int64_t D) {
     int64_t slots;
-    if (!mul_ok(pages, page, &slots) || slots > INT32_MAX) return -1;
+    if (!mul_ok(pages, page, &slots) || slots > INT32_MAX || H > 65535) return -1;
     return nbytes({pages, H}, gdn::kv_block_bytes(page, D));
 }
 
@@ -62,8 +62,8 @@ gdn_status check_kv(const char *fn, const void *cache, const int32_t *slots, con
         return fail(GDN_ERR_UNSUPPORTED, "%s: page (%lld) must be 16, 32, 64 or 128", fn, (long long)page);
     if (!cache || !slots) return fail(GDN_ERR_INVALID_ARGUMENT, "%s: cache and slots must be non-NULL", fn);
     *bytes = cache_bytes(pages, H, page, D);
-    if (*bytes < 0 || H > INT32_MAX / (2 * D / 16))
-        return fail(GDN_ERR_INVALID_ARGUMENT, "%s: the cache's sizes overflow (at most 2^31 - 1 slots)", fn);
+    if (*bytes < 0)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "%s: the cache's sizes overflow (2^31 - 1 slots, 65535 heads)", fn);
     if (!aligned(cache, 16)) return fail(GDN_ERR_MISALIGNED, "%s: cache must be 16-byte aligned", fn);
     if (!aligned(slots, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
         return fail(GDN_ERR_MISALIGNED, "%s: slots, k_scale and v_scale must be 4-byte aligned", fn);
@@ -341,7 +341,7 @@ gdn_status gdn_kv_attention(const void *q, const void *cache, const int32_t *blo
     if (y_b < 0 || l_b < 0 || t_b < 0 || c_b < 0 || !mul_ok(width, page, &row_all) || row_all > INT32_MAX ||
         B > INT32_MAX || gdn::attend_workspace_bytes(B, T, Hq, H, D) < 0)
         return fail(GDN_ERR_INVALID_ARGUMENT,
-                    "%s: sizes overflow (pages * page, width * page and the query rows fit int32)", fn);
+                    "%s: sizes overflow (pages * page, width * page and the query rows fit int32, H 16 bits)", fn);
     const int64_t q_b = scaled(extent(B, q_stride_b, T, q_stride_t, Hq * D), eb);
     if (q_b < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "%s: strides of q overlap its rows or overflow", fn);
     if (!aligned(q, eb) || !aligned(y, eb))
@@ -385,7 +385,11 @@ gdn_status gdn_kv_attention(const void *q, const void *cache, const int32_t *blo
     a.page_shift = shift_of(page);
     a.scale = scale;
     a.window = (int)window;
-    return launched(fn, gdn::launch_kv_attend(static_cast<gdn::DType>(dtype), a, reinterpret_cast<cudaStream_t>(stream)));
+    a.vec_y = aligned(y, 16);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return launched(fn, dtype == GDN_DTYPE_F32    ? gdn::launch_attend_f32(a, s)
+                        : dtype == GDN_DTYPE_BF16 ? gdn::launch_attend_bf16(a, s)
+                                                  : gdn::launch_attend_f16(a, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,17 @@
+// attend_f32.cu -- kv_attend.cuh for f32 queries.
+#include "kv_attend.cuh"
+
+namespace gdn {
+
+cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t s) { return launch_attend<float>(a, s); }
+
+int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D) {
+    int64_t rows, pairs;
+    if (__builtin_mul_overflow(T, Hq / H, &rows) || rows > INT32_MAX - 64) return -1;
+    const int NB = eights_of(rows, D);
+    if (__builtin_mul_overflow(B, (rows + 8 * NB - 1) / (8 * NB), &pairs) || pairs > INT32_MAX) return -1;
+    if (!cut(pairs, H)) return 0;
+    return ((int64_t)2 * kSms * resident(NB, (int)D, false) * partial_floats(8 * NB, (int)D) + kBaseFloats) * 4;
+}
+
+}  // namespace gdn
