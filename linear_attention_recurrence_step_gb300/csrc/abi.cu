@@ -10,6 +10,7 @@
 #include <string>
 
 #include "abi_util.h"
+#include "attend.h"
 #include "gdn.h"
 #include "launch.h"
 #include "record.cuh"
@@ -188,14 +189,16 @@ int gdn_abi_version(void) { return GDN_ABI_VERSION; }
 
 gdn_status gdn_wait_status(int *expired) {
     if (!expired) return fail(GDN_ERR_INVALID_ARGUMENT, "gdn_wait_status: expired must be non-NULL");
-    unsigned rec = 0, rep = 0, str = 0;
+    unsigned rec = 0, rep = 0, str = 0, att = 0;
     cudaError_t e = gdn::record_tc_take_wait_flag(&rec);
     if (e != cudaSuccess) return cuda_fail("gdn_wait_status", "record flag", e);
     e = gdn::replay_tc_take_wait_flag(&rep);
     if (e != cudaSuccess) return cuda_fail("gdn_wait_status", "replay flag", e);
     e = gdn::replay_stream_take_wait_flag(&str);
     if (e != cudaSuccess) return cuda_fail("gdn_wait_status", "stream replay flag", e);
-    *expired = (rec | rep | str) != 0u ? 1 : 0;
+    e = gdn::attend_tc_take_wait_flag(&att);
+    if (e != cudaSuccess) return cuda_fail("gdn_wait_status", "attention flag", e);
+    *expired = (rec | rep | str | att) != 0u ? 1 : 0;
     return ok();
 }
 

@@ -65,12 +65,17 @@ struct AttendArgs {
     int Hq, H, D, width, page_shift;
     float scale;
     int window;                         // 0: none
-    bool vec_y;                         // y is 16-byte aligned
+    bool vec_q, vec_y;                  // rows of q, y begin on 16 bytes
 };
 int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D);
 // One translation unit per element type.
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_attend_f16(const AttendArgs &a, cudaStream_t s);
+// The tcgen05 form (attend_tc.cu), for f16 and bf16 calls of many query rows;
+// its wait-expiry flag.
+bool attend_takes_tc(DType dt, const AttendArgs &a);
+cudaError_t launch_attend_tc(DType dt, const AttendArgs &a, cudaStream_t s);
+cudaError_t attend_tc_take_wait_flag(unsigned *was_set);
 
 }  // namespace gdn

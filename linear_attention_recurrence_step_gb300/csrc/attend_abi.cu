@@ -386,7 +386,11 @@ gdn_status gdn_kv_attention(const void *q, const void *cache, const int32_t *blo
     a.scale = scale;
     a.window = (int)window;
     a.vec_y = aligned(y, 16);
+    const int64_t vec = 16 / eb;
+    a.vec_q = aligned(q, 16) && (B == 1 || q_stride_b % vec == 0) && (T == 1 || q_stride_t % vec == 0);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const gdn::DType dt = static_cast<gdn::DType>(dtype);
+    if (gdn::attend_takes_tc(dt, a)) return launched(fn, gdn::launch_attend_tc(dt, a, s));
     return launched(fn, dtype == GDN_DTYPE_F32    ? gdn::launch_attend_f32(a, s)
                         : dtype == GDN_DTYPE_BF16 ? gdn::launch_attend_bf16(a, s)
                                                   : gdn::launch_attend_f16(a, s));
