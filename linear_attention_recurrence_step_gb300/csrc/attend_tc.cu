@@ -40,7 +40,7 @@ namespace {
 
 __device__ unsigned g_attend_tc_wait_flag;
 
-constexpr int kTcWarps = 13, kTcThreads = 32 * kTcWarps;  // 8 softmax (or 4 and 4 dequant), 4 dequant, 1 issuer
+constexpr int kTcThreads = 512;   // warpgroups: softmax, softmax (or dequant), dequant, issuer (one warp of it)
 constexpr int kTcTile = 128;                              // query rows of a tile
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;         // S buffers at 0 and 128, O from 256 on
 constexpr long long kDrainCycles = 2000000000ll;
@@ -85,7 +85,7 @@ __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // 32 columns of the thread's lane; 32 and 16 columns written.
-__device__ __forceinline__ void tm_ld32(uint32_t t, float (&v)[32]) {
+__device__ __forceinline__ void tm_ld32(uint32_t t, float *v) {  // (valid after tm_wait_ld)
     uint32_t r[32];
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -95,7 +95,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t t, float (&v)[32]) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(t));
-    tm_wait_ld();
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
 }
@@ -123,6 +122,13 @@ __device__ __forceinline__ uint32_t times2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ void st_shared16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void less_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
 struct TcArgs {
@@ -191,7 +197,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
 
     const bool softmax_warp = warp < 4 * L::kTiles;
     float sum = 0.f, off = -1e30f;
+    // registers where they are used: 4 x 128 at launch, as many or fewer in all
     if (softmax_warp) {
+        more_registers<192>();
         // ================================================ softmax warps
         const int t = warp >> 2, row = tid & 127, r = r0 + t * kTcTile + row;  // tile, row in it, row of the sequence
         const bool there = t * kTcTile + row < rows;
@@ -255,22 +263,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             const int tok0 = (step0 + j) * TN;
             const bool edge = tok0 < all_lo || tok0 + TN > all_hi || present != (1u << (TN / 16)) - 1u;
             const int c_lo = row_lo - tok0, c_hi = row_hi - tok0;
-            auto mask = [&](float (&v)[32], int k) {
+            float v[TN];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int col = 32 * k + e;
-                    if (col < c_lo || col >= c_hi || !((present >> (col / 16)) & 1u)) v[e] = -INFINITY;
-                }
-            };
-            float top = -INFINITY;
+            for (int k = 0; k < TN / 32; ++k) tm_ld32(s_at + 32u * k, v + 32 * k);
+            tm_wait_ld();
+            if (edge) {
 #pragma unroll
-            for (int k = 0; k < TN / 32; ++k) {
-                float v[32];
-                tm_ld32(s_at + 32u * k, v);
-                if (edge) mask(v, k);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e]);
+                for (int e = 0; e < TN; ++e)
+                    if (e < c_lo || e >= c_hi || !((present >> (e / 16)) & 1u)) v[e] = -INFINITY;
             }
+            float tops[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int e = 4; e < TN; ++e) tops[e % 4] = fmaxf(tops[e % 4], v[e]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             if (__any_sync(0xffffffffu, fmaf(top, c, -off) > kTcBoost + kTcSlack)) {
                 const float to = top == -INFINITY ? off : fmaxf(off, top * c - kTcBoost);
                 const float f = exp2f(off - to);
@@ -281,34 +286,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                     tm_after();
 #pragma unroll 1
                     for (int k = 0; k < D / 32; ++k) {
-                        float v[32];
+                        float w[32];
                         const uint32_t o_at = lanes + kTmemO + (uint32_t)(t * D + 32 * k);
-                        tm_ld32(o_at, v);
+                        tm_ld32(o_at, w);
+                        tm_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] *= f;
-                        tm_st32(o_at, v);
+                        for (int e = 0; e < 32; ++e) w[e] *= f;
+                        tm_st32(o_at, w);
                     }
                     tm_wait_st();
                 }
             }
             const float2 c2 = make_float2(c, c), off2 = make_float2(-off, -off);
-            float2 part = make_float2(0.f, 0.f);
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int k = 0; k < TN / 32; ++k) {
-                float v[32];
-                tm_ld32(s_at + 32u * k, v);
-                if (edge) mask(v, k);
                 uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float2 x = ffma2(make_float2(v[2 * e], v[2 * e + 1]), c2, off2);
+                    const float2 x = ffma2(make_float2(v[32 * k + 2 * e], v[32 * k + 2 * e + 1]), c2, off2);
                     const float2 y = make_float2(ex2f(x.x), ex2f(x.y));
-                    part = __fadd2_rn(part, y);
+                    part[e & 1] = __fadd2_rn(part[e & 1], y);
                     p[e] = pack2<__half>(y.x, y.y);
                 }
                 tm_st16(s_at + 16u * k, p);
             }
-            sum += part.x + part.y;
+            part[0] = __fadd2_rn(part[0], part[1]);
+            sum += part[0].x + part[0].y;
             tm_wait_st();
             tm_before();
             __syncwarp();
@@ -328,6 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                 float v[32];
                 if (steps > 0 && ok) {
                     tm_ld32(lanes + kTmemO + (uint32_t)(t * D + 32 * k), v);
+                    tm_wait_ld();
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
@@ -350,69 +355,72 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                 a.lse[at] = !ok ? inv : sum == 0.f ? -INFINITY : (off + log2f(sum)) * 0.693147180559945309f;
         }
     } else if (warp < 12) {
+        less_registers<D == 256 ? 120 : 88>();
         // ================================================ dequant warps
-        constexpr int LPR = D / 32, JOBS = TN * LPR / (32 * L::kDqWarps);  // lanes per token; pieces of 32 channels per thread
-        const int w = warp - 4 * L::kTiles, piece = lane % LPR, sub = lane / LPR;
-        const int panel = piece >> 1, order = D == 256 ? panel : D == 128 ? 2 * panel : 0;  // (distinct banks in 8 lanes)
-        const int64_t block_bytes = kv_block_bytes(page, D), page_bytes = a.H * block_bytes;
-        const unsigned char *cache = a.cache + h * block_bytes;
+        // A job is 32 neighbouring channels of a token: 16 bytes of codes, two
+        // scales.  D/32 lanes share a token; a warp's jobs are neighbouring tokens,
+        // those of 16 tokens in one page.
+        constexpr int LPR = D / 32, RPI = 32 / LPR, JOBS = TN / (RPI * L::kDqWarps);
+        constexpr int PAGES = JOBS * RPI >= 16 ? JOBS * RPI / 16 : 1, JPP = JOBS / PAGES;
+        const int w = warp - 4 * L::kTiles, piece = lane % LPR, sub = lane / LPR, panel = piece >> 1;
+        const int first = w * JOBS * RPI + sub;  // the token of job 0, in the step
+        // the order of a job's four words, so that eight lanes write distinct banks
+        const int order = D == 256 ? panel : D == 128 ? 2 * panel : 0;
+        const uint32_t page_bytes = (uint32_t)(a.H * kv_block_bytes(page, D));
+        const unsigned char *cache = a.cache + h * kv_block_bytes(page, D) + 16 * piece;
+        const unsigned char *scales = a.cache + h * kv_block_bytes(page, D) + page * (D / 2) + 2 * piece;
         const int values = page * (D / 2 + D / 16);
-        auto token = [&](int i) { return (w * JOBS + i) * (32 / LPR) + sub; };  // of job i, in the step
-        uint4 kq[JOBS], vq[JOBS];
-        uint32_t ks[JOBS], vs[JOBS];
-        auto load = [&](int j, int ids, bool v, uint4 (&q)[JOBS], uint32_t (&sc)[JOBS]) {
+        const uint32_t pick[2] = {order & 2 ? 0x3232u : 0x1010u, order & 2 ? 0x1010u : 0x3232u};
+        uint32_t chunk[4];
 #pragma unroll
-            for (int i = 0; i < JOBS; ++i) {
-                const int in = token(i), tok = (step0 + j) * TN + in;
-                const int id = __shfl_sync(0xffffffffu, ids, in >> 4);
-                q[i] = make_uint4(0, 0, 0, 0);
-                sc[i] = 0;
-                if (id >= 0 && tok >= lo && tok < hi) {
-                    const unsigned char *blk = cache + id * page_bytes + (v ? values : 0);
-                    const int row = tok & (page - 1);
-                    q[i] = *reinterpret_cast<const uint4 *>(blk + row * (D / 2) + 16 * piece);
-                    sc[i] = *reinterpret_cast<const uint16_t *>(blk + page * (D / 2) + row * (D / 16) + 2 * piece);
+        for (int k = 0; k < 4; ++k)
+            chunk[k] = (uint32_t)panel * (TN * 128) + first * 128 + ((((piece & 1) * 4 + (k ^ order)) ^ (first & 7)) << 4);
+        uint2 kq[JOBS][2], vq[JOBS][2];
+        uint32_t ks[JOBS], vs[JOBS];
+        auto load = [&](int j, int ids, int at, uint2 (&q)[JOBS][2], uint32_t (&sc)[JOBS]) {
+            const int t0 = (step0 + j) * TN;
+            const bool full = t0 >= lo && t0 + TN <= hi;
+#pragma unroll
+            for (int p = 0; p < PAGES; ++p) {
+                const int id = __shfl_sync(0xffffffffu, ids, (w * JOBS * RPI + 16 * p) >> 4);
+                const int in = first + 16 * p, row = (t0 + in) & (page - 1);
+                const uint64_t off = (uint64_t)(uint32_t)id * page_bytes + (uint32_t)at;
+                const unsigned char *c = cache + off + row * (D / 2), *s = scales + off + row * (D / 16);
+#pragma unroll
+                for (int i = 0; i < JPP; ++i) {
+                    const int job = p * JPP + i, tok = t0 + in + i * RPI;
+                    q[job][0] = q[job][1] = make_uint2(0, 0);
+                    sc[job] = 0;
+                    if (id >= 0 && (full || (tok >= lo && tok < hi))) {
+                        // (the halves in the order that they are written in)
+                        q[job][0] = *reinterpret_cast<const uint2 *>(c + i * RPI * (D / 2) + 4 * (order & 2));
+                        q[job][1] = *reinterpret_cast<const uint2 *>(c + i * RPI * (D / 2) + 8 - 4 * (order & 2));
+                        sc[job] = *reinterpret_cast<const uint16_t *>(s + i * RPI * (D / 16));
+                    }
                 }
             }
         };
-        auto store = [&](uint32_t dst, const uint4 (&q)[JOBS], const uint32_t (&sc)[JOBS]) {
+        auto store = [&](uint32_t dst, const uint2 (&q)[JOBS][2], const uint32_t (&sc)[JOBS]) {
 #pragma unroll
             for (int i = 0; i < JOBS; ++i) {
-                uint32_t x[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-                if (D == 256 && (order & 1)) {
-                    uint32_t t = x[0];
-                    x[0] = x[1];
-                    x[1] = t;
-                    t = x[2];
-                    x[2] = x[3];
-                    x[3] = t;
-                }
-                if (D >= 128 && (order & 2)) {
-                    uint32_t t = x[0];
-                    x[0] = x[2];
-                    x[2] = t;
-                    t = x[1];
-                    x[1] = x[3];
-                    x[3] = t;
-                }
                 const uint32_t both = e4m3x2_to_f16(sc[i]);
-                const int row = token(i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int word = k ^ order;  // of the piece
-                    const uint32_t f = __byte_perm(both, both, word & 2 ? 0x3232 : 0x1010);
+                    uint32_t x = k % 2 ? q[i][k / 2].y : q[i][k / 2].x;
+                    if (D == 256 && (order & 1)) x = k % 2 ? q[i][k / 2].x : q[i][k / 2].y;
+                    const uint32_t f = __byte_perm(both, both, pick[k / 2]);
                     uint32_t e[4];
-                    e2m1x8_to_f16(x[k], e);
-                    st_shared16(dst + (uint32_t)panel * (TN * 128) + row * 128 + ((((piece & 1) * 4 + word) ^ (row & 7)) << 4),
-                                times2(e[0], f), times2(e[1], f), times2(e[2], f), times2(e[3], f));
+                    e2m1x8_to_f16(x, e);
+                    st_shared16(dst + (chunk[k] ^ (((i * RPI) & 7) << 4)) + i * RPI * 128, times2(e[0], f), times2(e[1], f),
+                                times2(e[2], f), times2(e[3], f));
                 }
             }
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             __syncwarp();
         };
         int ids = pages_of(0), ids_next = pages_of(1);
-        load(0, ids, false, kq, ks);
-        load(0, ids, true, vq, vs);
+        load(0, ids, 0, kq, ks);
+        load(0, ids, values, vq, vs);
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
             ids = ids_next;
@@ -420,16 +428,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             if (j >= 2 && !wait(kKFree + st, (j >> 1) - 1)) break;
             store(base + L::kK + st * L::kOpBytes, kq, ks);
             if (lane == 0) mbar_arrive(bar(kKFull + st));
-            load(j + 1, ids, false, kq, ks);
+            load(j + 1, ids, 0, kq, ks);
             if (j >= 2 && !wait(kVFree + st, (j >> 1) - 1)) break;
             store(base + L::kV + st * L::kOpBytes, vq, vs);
             if (lane == 0) mbar_arrive(bar(kVFull + st));
-            load(j + 1, ids, true, vq, vs);
+            load(j + 1, ids, values, vq, vs);
         }
     } else {
+        less_registers<40>();
         // ================================================ issuer
-        named_bar_sync(1, 32 * (4 * L::kTiles + 1));
-        if (lane == 0) {
+        if (warp == 12) named_bar_sync(1, 32 * (4 * L::kTiles + 1));
+        if (warp == 12 && lane == 0) {
             const uint32_t op_s = op_desc(TN, false), op_o = op_desc(D, true);
             auto wait = [&](int i, uint32_t parity) {
                 if (ok) ok = mbar_wait_bounded(bar(i), parity & 1u, ta.wait_cycles);
