@@ -65,20 +65,30 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lbo, ui
 constexpr uint32_t op_desc(int n, bool n_major) {
     return (1u << 4) | (n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t op, uint32_t add) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(op), "r"(add)
+// One thread of the warp issues (`one`), so that the warp stays together and
+// descriptors are uniform: a branch around each product costs 100 cycles in
+// moves to uniform registers.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t op, uint32_t add) {
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(op), "r"(add), "r"(one)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t op, uint32_t add) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(op), "r"(add)
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t op, uint32_t add) {
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(op), "r"(add), "r"(one)
                  : "memory");
 }
-__device__ __forceinline__ void commit_to(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit_to(uint32_t one, uint32_t bar) {
+    asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(one)
+                 : "memory");
 }
 __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
@@ -437,37 +447,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
     } else {
         less_registers<40>();
         // ================================================ issuer
-        if (warp == 12) named_bar_sync(1, 32 * (4 * L::kTiles + 1));
-        if (warp == 12 && lane == 0) {
-            const uint32_t op_s = op_desc(TN, false), op_o = op_desc(D, true);
-            auto wait = [&](int i, uint32_t parity) {
-                if (ok) ok = mbar_wait_bounded(bar(i), parity & 1u, ta.wait_cycles);
-                return ok;
-            };
+        if (warp == 12) {
+            named_bar_sync(1, 32 * (4 * L::kTiles + 1));
+            constexpr uint32_t op_s = op_desc(TN, false), op_o = op_desc(D, true);
+            const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t sbase = __shfl_sync(0xffffffffu, base, 0);
             auto issue_s = [&](int j, int t) {
                 const int buf = tiles == 2 ? t : j & 1;
                 if (!wait(kKFull + (j & 1), j >> 1)) return;
                 tm_after();
-                const uint32_t q = base + L::kQ + t * kTcTile * 128, k = base + L::kK + (j & 1) * L::kOpBytes;
+                const uint64_t q = operand_desc(sbase + L::kQ + t * kTcTile * 128, 16, 1024);
+                const uint64_t k = operand_desc(sbase + L::kK + (j & 1) * L::kOpBytes, 16, 1024);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
-                    mma_ss(tmem + 128u * buf,
-                           operand_desc(q + (s >> 2) * (L::kRows * 128) + (s & 3) * 32, 16, 1024),
-                           operand_desc(k + (s >> 2) * (TN * 128) + (s & 3) * 32, 16, 1024), op_s, s > 0);
-                commit_to(bar(kSFull + buf));
-                if (t == tiles - 1) commit_to(bar(kKFree + (j & 1)));
+                    mma_ss(one, tm + 128u * buf, q + ((s >> 2) * (L::kRows * 128) + (s & 3) * 32) / 16,
+                           k + ((s >> 2) * (TN * 128) + (s & 3) * 32) / 16, op_s, s > 0);
+                commit_to(one, bar(kSFull + buf));
+                if (t == tiles - 1) commit_to(one, bar(kKFree + (j & 1)));
             };
             auto issue_o = [&](int j, int t) {
                 const int buf = tiles == 2 ? t : j & 1;
                 if (!wait(kVFull + (j & 1), j >> 1) || !wait(kPFull + buf, tiles == 2 ? j : j >> 1)) return;
                 tm_after();
-                const uint32_t v = base + L::kV + (j & 1) * L::kOpBytes;
+                const uint64_t v = operand_desc(sbase + L::kV + (j & 1) * L::kOpBytes, TN * 128, 1024);
 #pragma unroll
                 for (int s = 0; s < TN / 16; ++s)
-                    mma_ts(tmem + kTmemO + (uint32_t)(t * D), tmem + 128u * buf + 8u * s,
-                           operand_desc(v + s * 2048, TN * 128, 1024), op_o, j > 0 || s > 0);
-                commit_to(bar(kODone + t));
-                if (t == tiles - 1) commit_to(bar(kVFree + (j & 1)));
+                    mma_ts(one, tm + kTmemO + (uint32_t)(t * D), tm + 128u * buf + 8u * s, v + s * 2048 / 16, op_o, j > 0 || s > 0);
+                commit_to(one, bar(kODone + t));
+                if (t == tiles - 1) commit_to(one, bar(kVFree + (j & 1)));
             };
             if (steps > 0)
                 for (int t = 0; t < tiles; ++t) issue_s(0, t);
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                 }
             }
             // nothing is in flight when the tensor memory goes
-            commit_to(bar(kDrain));
+            commit_to(one, bar(kDrain));
             if (!mbar_wait_bounded(bar(kDrain), 0, kDrainCycles)) ok = false;
         }
     }
