@@ -267,12 +267,13 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
         // ------------------------------------------------ this warp's tiles
         const int n = c1 - c0, first_tok = (s.chunk0 + c0) * kChunk + warp * kTile;
         const int32_t *row_table = a.table + (int64_t)s.b * a.width;
-        // the page of half `lane` of the tiles from k on, -1: nothing of it is seen
+        // the table's entry for half `lane` of the tiles from k on, -1: nothing of it
+        // is seen
         auto pages_from = [&](int k) {
             const int kk = k + (lane >> 1), tok = first_tok + kk * kChunk + 16 * (lane & 1);
             int id = -1;
             if (kk < n && tok < s.hi && tok + 16 > s.lo) id = row_table[tok >> a.page_shift];
-            return id < a.pages ? id : -1;
+            return id;  // (checked where it is used, later: here the warp would wait for it)
         };
         int ids = pages_from(0), ids_next = pages_from(16);
         // pages divide a chunk, so a warp's tiles start at the same row of their
@@ -280,7 +281,7 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
         // keys' codes, values' codes, and the piece of scales that is its own
         constexpr int CODES = 8 * D, HALF = 9 * D;   // bytes of 16 tokens: codes; codes and scales
         constexpr int SPS = D / 16;                  // pieces of 16 tokens' scales, of keys or of values
-        const uint32_t page_bytes = (uint32_t)(a.H * block_bytes);
+        const uint32_t page_bytes = (uint32_t)(a.H * block_bytes), pool = (uint32_t)a.pages;
         const unsigned char *k_src[2], *v_src[2];
         const int values = page * (D / 2 + D / 16), row0 = first_tok & (page - 1);
 #pragma unroll
@@ -300,7 +301,9 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
         // the halves of a tile into a slot of the ring; `from` holds their pages in
         // lanes at and at + 1.  Returns which of them are there.
         auto fetch = [&](uint32_t dst, int from, int at) {
-            const int id0 = __shfl_sync(0xffffffffu, from, at & 31), id1 = __shfl_sync(0xffffffffu, from, (at + 1) & 31);
+            int id0 = __shfl_sync(0xffffffffu, from, at & 31), id1 = __shfl_sync(0xffffffffu, from, (at + 1) & 31);
+            if ((uint32_t)id0 >= pool) id0 = -1;
+            if ((uint32_t)id1 >= pool) id1 = -1;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int id = i ? id1 : id0;
