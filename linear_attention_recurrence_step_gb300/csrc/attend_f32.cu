@@ -10,8 +10,11 @@ int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int6
     if (__builtin_mul_overflow(T, Hq / H, &rows) || rows > INT32_MAX - 64) return -1;
     const int NB = eights_of(rows, D);
     if (__builtin_mul_overflow(B, (rows + 8 * NB - 1) / (8 * NB), &pairs) || pairs > INT32_MAX) return -1;
-    if (!cut(pairs, H)) return 0;
-    return ((int64_t)2 * kSms * resident(NB, (int)D, false) * partial_floats(8 * NB, (int)D) + kBaseFloats) * 4;
+    // whichever form the call takes
+    const int64_t tc = attend_tc_workspace_bytes(B, T, Hq, H, D);
+    if (!cut(pairs, H)) return tc;
+    const int64_t own = ((int64_t)2 * kSms * resident(NB, (int)D, false) * partial_floats(8 * NB, (int)D) + kBaseFloats) * 4;
+    return own > tc ? own : tc;
 }
 
 }  // namespace gdn
