@@ -389,6 +389,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             acc[0] = __fadd2_rn(acc[0], acc[1]);
             sum += acc[0].x + acc[0].y;
             tm_wait_st();
+            // (one tile's S runs ahead of its O: O's phases are followed step by step, for
+            // a phase can only be told from the one before it)
+            if (tiles == 1 && j > 0 && !wait(kODone + t, j - 1)) break;
             tm_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kPFull + buf));
@@ -671,11 +674,14 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const TcPlan p = tc_plan(a.B, a.T * (a.Hq / a.H), a.H, D);
     if (p.units * p.parts > INT32_MAX) return cudaErrorInvalidConfiguration;
-    TcArgs ta{a, p.parts, p.part_rows, static_cast<unsigned *>(flag), wait_bound_cycles(), inject_wait_expiry()};
-    e = launch_dependent(attend_tc_kernel<T, D>, (unsigned)(p.units * p.parts), kTcThreads, L::kSmem, s, ta);
-    if (e != cudaSuccess || p.parts == 1) return e;
+    // a part's first step, queries and output cost as much as six steps
+    const int64_t steps = ((int64_t)a.width << a.page_shift) / L::kTok;
+    const int parts = (int)std::max<int64_t>(std::min<int64_t>(p.parts, steps / 6), 1);
+    TcArgs ta{a, parts, p.part_rows, static_cast<unsigned *>(flag), wait_bound_cycles(), inject_wait_expiry()};
+    e = launch_dependent(attend_tc_kernel<T, D>, (unsigned)(p.units * parts), kTcThreads, L::kSmem, s, ta);
+    if (e != cudaSuccess || parts == 1) return e;
     const int groups = p.part_rows / 8;
-    return launch_dependent(attend_tc_join_kernel<T, D>, (unsigned)(p.units * groups), 256, 0, s, a, p.parts, p.part_rows, groups);
+    return launch_dependent(attend_tc_join_kernel<T, D>, (unsigned)(p.units * groups), 256, 0, s, a, parts, p.part_rows, groups);
 }
 
 template <typename T>
@@ -695,8 +701,7 @@ int64_t attend_tc_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, i
     return attend_tc_rows(rows) ? tc_plan(B, rows, H, D).workspace : 0;
 }
 
-// (up to 16 rows the other form's narrow products fit them)
-bool attend_tc_rows(int64_t rows) { return rows > 16; }
+bool attend_tc_rows(int64_t rows) { return rows > 64; }
 bool attend_takes_tc(DType dt, const AttendArgs &a) { return dt != DType::F32 && attend_tc_rows(a.T * (a.Hq / a.H)); }
 
 cudaError_t launch_attend_tc(DType dt, const AttendArgs &a, cudaStream_t s) {

@@ -1,6 +1,6 @@
 // kv_attend.cuh -- attention over the 4-bit paged cache.
 //
-// A unit is up to 8, 16 or 32 query rows (draft tokens times query heads of one
+// A unit is up to 8 or 16 query rows (draft tokens times query heads of one
 // key head) of one sequence and key head.  Each warp takes 32 tokens at a time
 // through S^T = K Q^T, the softmax, and O^T += V^T P^T on mma.sync (m16n8k16, f16
 // operands, f32 sums), and keeps its own reference, sum and O until the end of
@@ -53,12 +53,12 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 template <typename T> constexpr float kBoost = sizeof(T) == 4 ? 14.f : 6.f;
 template <typename T> constexpr float kSlack = sizeof(T) == 4 ? 1.f : 8.f;
 
-// Eights of query rows per unit, and what a block of such units takes: blocks
-// per SM by registers and shared memory.
-constexpr int eights_of(int64_t rows, int64_t D) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
+// Eights of query rows per unit (four would take 255 registers: 32 rows of 16
+// sequences of up to 8192 tokens 75 us, two units of 16 rows 70), and the blocks of
+// such units that an SM holds, by registers and shared memory.
+constexpr int eights_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
 constexpr int resident(int NB, int D, bool f32) {
-    return (NB == 1 ? (D == 64 ? 6 : D == 128 ? 5 : 3) : NB == 2 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : D == 64 ? 3 : 2) -
-           (f32 && !(NB > 1 && D > 64));
+    return (NB == 1 ? (D == 64 ? 6 : D == 128 ? 5 : 3) : D == 64 ? 4 : D == 128 ? 3 : 2) - (f32 && !(NB > 1 && D > 64));
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -783,12 +783,7 @@ cudaError_t launch_tdn(const AttendArgs &a, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_td(const AttendArgs &a, cudaStream_t s) {
-    switch (eights_of(a.T * (a.Hq / a.H), D)) {
-    case 1: return launch_tdn<T, D, 1>(a, s);
-    case 2: return launch_tdn<T, D, 2>(a, s);
-    }
-    if constexpr (D < 256) return launch_tdn<T, D, 4>(a, s);
-    return cudaErrorInvalidValue;
+    return eights_of(a.T * (a.Hq / a.H)) == 1 ? launch_tdn<T, D, 1>(a, s) : launch_tdn<T, D, 2>(a, s);
 }
 
 template <typename T>

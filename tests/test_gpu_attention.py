@@ -321,6 +321,15 @@ def test_attention_prompts(dev, dtype, D, T, Hq, H, lengths, window):
     attend_case(dev, dtype, 2, T, Hq, H, D, 32, lengths, [T, T - 3], window, seed=T)
 
 
+@pytest.mark.parametrize("D,T,Hq,H,lengths", [(128, 200, 4, 1, [200]), (128, 300, 1, 1, [900]), (64, 90, 1, 1, [1100]), (256, 140, 2, 1, [1200])])
+def test_attention_prompts_again(dev, D, T, Hq, H, lengths):
+    """Row blocks of one tile over several steps, whole and in parts, many times: the
+    same results each time."""
+    y = attend_case(dev, "f16", 1, T, Hq, H, D, 16, lengths, seed=T).clone()
+    for _ in range(15):
+        assert torch.equal(attend_case(dev, "f16", 1, T, Hq, H, D, 16, lengths, seed=T), y)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attention_sharp_scores(dev, dtype):
     """Scores of hundreds (one token takes all), tiny ones, scales of zero and below."""
