@@ -20,7 +20,7 @@ struct SlotsArgs {
     int64_t B, T;
     int width, pages, page_shift;
 };
-cudaError_t launch_page_slots(const SlotsArgs &a, int sm_count, cudaStream_t s);
+cudaError_t launch_page_slots(const SlotsArgs &a, cudaStream_t s);
 
 struct RotaryArgs {
     const void *q, *k;                  // k may be null

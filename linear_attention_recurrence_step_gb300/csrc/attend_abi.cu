@@ -113,9 +113,6 @@ gdn_status gdn_page_slots(const int32_t *lengths, const int32_t *add, const int3
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps another tensor", fn);
 
     if (take_forced_failure()) return forced_failure(fn);
-    cudaError_t e;
-    const int sms = current_sm_count(&e);
-    if (e != cudaSuccess) return cuda_fail(fn, "device query", e);
     gdn::SlotsArgs a{};
     a.lengths = lengths;
     a.add = add;
@@ -134,7 +131,7 @@ gdn_status gdn_page_slots(const int32_t *lengths, const int32_t *add, const int3
     a.width = (int)width;
     a.pages = (int)pages;
     a.page_shift = shift_of(page);
-    return launched(fn, gdn::launch_page_slots(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return launched(fn, gdn::launch_page_slots(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_rotary(const void *q, const void *k, const int32_t *positions, const float *inv_freq, void *q_out,

@@ -6,7 +6,8 @@
 // where its remainder says on which side of it the exact one lies.
 //
 // Bound by memory (a read or write of 16 elements and one of 9 bytes); one
-// thread per group, neighbouring threads on neighbouring groups.
+// thread per group, neighbouring threads on neighbouring groups, whose scales go out
+// four to a word.
 #include "attend.h"
 #include "fp4.cuh"
 #include "pieces.cuh"
@@ -33,13 +34,19 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(int64_t i, int H, int groups) {
     Place p;
-    const int per = 2 * H * groups;
-    p.token = i / per;
-    int r = (int)(i - p.token * per);
-    p.value = r >= H * groups;
-    if (p.value) r -= H * groups;
-    p.head = r / groups;
-    p.group = r - p.head * groups;
+    const unsigned half = (unsigned)(H * groups), per = 2 * half;
+    unsigned r;
+    if (i <= UINT32_MAX) {  // (a quarter of the cost of the other division)
+        p.token = (unsigned)i / per;
+        r = (unsigned)i - (unsigned)p.token * per;
+    } else {
+        p.token = i / per;
+        r = (unsigned)(i - p.token * per);
+    }
+    p.value = r >= half;
+    if (p.value) r -= half;
+    p.head = (int)(r / (unsigned)groups);
+    p.group = (int)(r - (unsigned)p.head * (unsigned)groups);
     return p;
 }
 // The group's codes and scale in the cache (the slot is valid).
@@ -57,52 +64,74 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvArgs a, i
     pdl_trigger();
     pdl_wait();
     const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-    if (i >= total) return;
-    const Place p = place_of(i, a.H, a.D / 16);
-    const int slot = a.slots[p.token];
-    if (slot < 0 || (slot >> a.page_shift) >= a.pages) return;
-    const int64_t b = p.token / a.T, t = p.token - b * a.T;
-    const T *src = static_cast<const T *>(p.value ? a.v_in : a.k_in) + b * (p.value ? a.v_sb : a.k_sb) +
-                   t * (p.value ? a.v_st : a.k_st) + (int64_t)p.head * a.D + p.group * 16;
-    constexpr int VEC = VECTOR ? 16 / (int)sizeof(T) : 1;
-    float u[16];
-#pragma unroll
-    for (int e = 0; e < 16; e += VEC) {
-        float v[VEC];
-        load_piece<T, VEC>(v, src + e);
-#pragma unroll
-        for (int f = 0; f < VEC; ++f) u[e + f] = v[f];
+    Place p{};
+    int slot = -1;
+    if (i < total) {
+        p = place_of(i, a.H, a.D / 16);
+        slot = a.slots[p.token];
+        if ((slot >> a.page_shift) >= a.pages) slot = -1;
     }
-    const float *hs = p.value ? a.v_scale : a.k_scale;
-    const float g = hs ? hs[p.head] : 1.f;
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        u[e] = hs ? u[e] / g : u[e];
-        // finite from here on: a NaN is a zero, infinities are the largest value
-        u[e] = u[e] == u[e] ? fminf(fmaxf(u[e], -3.4e38f), 3.4e38f) : 0.f;
-        top = fmaxf(top, fabsf(u[e]));
-    }
-    const uint32_t sb = f32_to_e4m3(beside(top / 6.f, top, 6.f));
-    const float s = f16_lo(e4m3x2_to_f16(sb));
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    uint32_t word[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 16; e += 2) {
-        float q[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const float m = fabsf(u[e + f]);
-            float x = m * inv;
-            x = fmaf(fmaf(-x, s, m), inv, x);  // the quotient's nearest float
-            if (s > 0.f && sizeof(T) == 4) x = beside(x, m, s);
-            q[f] = copysignf(x, u[e + f]);
+    uint32_t sb = 0u;
+    unsigned char *scale = nullptr;
+    if (slot >= 0) {
+        int64_t b = 0, t = p.token;
+        if (a.B > 1) {
+            b = p.token <= INT32_MAX && a.T <= INT32_MAX ? (unsigned)p.token / (unsigned)a.T : p.token / a.T;
+            t -= b * a.T;
         }
-        word[e / 8] |= f32_to_e2m1x2(q[0], q[1]) << (4 * (e % 8));
+        const T *src = static_cast<const T *>(p.value ? a.v_in : a.k_in) + b * (p.value ? a.v_sb : a.k_sb) +
+                       t * (p.value ? a.v_st : a.k_st) + (int64_t)p.head * a.D + p.group * 16;
+        constexpr int VEC = VECTOR ? 16 / (int)sizeof(T) : 1;
+        float u[16];
+#pragma unroll
+        for (int e = 0; e < 16; e += VEC) {
+            float v[VEC];
+            load_piece<T, VEC>(v, src + e);
+#pragma unroll
+            for (int f = 0; f < VEC; ++f) u[e + f] = v[f];
+        }
+        const float *hs = p.value ? a.v_scale : a.k_scale;
+        if (hs) {
+            // a power of two divides exactly by its reciprocal, any other number by division
+            const float g = hs[p.head], r = 1.f / g;
+            if ((__float_as_uint(g) & 0x007fffffu) == 0 && r >= 0x1p-126f && r <= 0x1p126f) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] *= r;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] /= g;
+            }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            // finite from here on: a NaN is a zero, infinities are the largest value
+            u[e] = u[e] == u[e] ? fminf(fmaxf(u[e], -3.4e38f), 3.4e38f) : 0.f;
+            top = fmaxf(top, fabsf(u[e]));
+        }
+        sb = f32_to_e4m3(beside(top / 6.f, top, 6.f));
+        const float s = f16_lo(e4m3x2_to_f16(sb));
+        const float inv = s > 0.f ? 1.f / s : 0.f;
+        uint32_t word[2] = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+            float q[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const float m = fabsf(u[e + f]);
+                float x = m * inv;
+                x = fmaf(fmaf(-x, s, m), inv, x);  // the quotient's nearest float
+                if (s > 0.f && sizeof(T) == 4) x = beside(x, m, s);
+                q[f] = copysignf(x, u[e + f]);
+            }
+            word[e / 8] |= f32_to_e2m1x2(q[0], q[1]) << (4 * (e % 8));
+        }
+        *reinterpret_cast<uint2 *>(codes_of(a, slot, p, &scale)) = make_uint2(word[0], word[1]);
     }
-    unsigned char *scale, *codes = codes_of(a, slot, p, &scale);
-    *reinterpret_cast<uint2 *>(codes) = make_uint2(word[0], word[1]);
-    *scale = (unsigned char)sb;
+    // (groups of four are of one token and head: D/16 is a multiple of four)
+    sb |= __shfl_down_sync(0xffffffffu, sb, 1) << 8;
+    sb |= __shfl_down_sync(0xffffffffu, sb, 2) << 16;
+    if (slot >= 0 && p.group % 4 == 0) *reinterpret_cast<uint32_t *>(scale) = sb;
 }
 
 template <typename T, bool VECTOR>

@@ -53,6 +53,7 @@ __device__ __forceinline__ void put_token(const SlotsArgs &a, int64_t b, int64_t
 
 __global__ void __launch_bounds__(kSlotsThreads) slots_plan_kernel(const SlotsArgs a, bool tokens) {
     __shared__ Pair part[32];
+    __shared__ int run[kSlotsThreads], run_at[kSlotsThreads], run_ring[kSlotsThreads];  // pages taken (or given back), where
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,24 +103,30 @@ __global__ void __launch_bounds__(kSlotsThreads) slots_plan_kernel(const SlotsAr
             a.lengths_out[b] = ends ? 0 : len + granted;
             a.held_out[b] = ends ? 0 : held + more;
         }
-        // short runs by their own thread, long ones by the warp
+        // a sequence's page by its own thread, longer runs by a warp each
         int32_t *row = a.table + b * a.width;
-        if (more > 0 && more <= 2)
-            for (int i = 0; i < more; ++i) row[held + i] = a.ring[ring_place(head + from + i, a.pages)];
-        for (unsigned m = __ballot_sync(0xffffffffu, more > 2); m; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int n = __shfl_sync(0xffffffffu, more, src), h = __shfl_sync(0xffffffffu, held, src);
-            const int64_t f = __shfl_sync(0xffffffffu, from, src);
-            int32_t *r = a.table + (b - lane + src) * a.width + h;
-            for (int i = lane; i < n; i += 32) r[i] = a.ring[ring_place(head + f + i, a.pages)];
-        }
-        for (unsigned m = __ballot_sync(0xffffffffu, back > 0); m; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int n = __shfl_sync(0xffffffffu, back, src);
-            const int64_t f = __shfl_sync(0xffffffffu, to, src);
-            const int32_t *r = a.table + (b - lane + src) * a.width;
+        const bool runs = more > 1 || back > 0;
+        if (more == 1) row[held] = a.ring[ring_place(head + from, a.pages)];
+        if (runs) {
+            run[tid] = more > 1 ? more : -back;
+            run_at[tid] = more > 1 ? held : 0;
+            run_ring[tid] = ring_place(head + (more > 1 ? from : to), a.pages);
             // (a ring that is full already takes no more)
-            for (int i = lane; i < n && f + i < a.pages; i += 32) a.ring[ring_place(head + f + i, a.pages)] = r[i];
+            if (back > 0) run[tid] = -(int)max(min((int64_t)back, a.pages - to), (int64_t)0);
+        } else {
+            run[tid] = 0;
+        }
+        if (__syncthreads_or(runs)) {
+            const int warps = (int)blockDim.x / 32, mine = run[warp + warps * lane];
+            for (unsigned m = __ballot_sync(0xffffffffu, mine != 0); m; m &= m - 1) {
+                const int q = warp + warps * (__ffs(m) - 1), n = run[q];
+                int32_t *r = a.table + (b0 + q) * a.width + run_at[q];
+                for (int i = lane; i < (n < 0 ? -n : n); i += 32) {
+                    const int at = run_ring[q] + i, place = at < a.pages ? at : at - a.pages;
+                    if (n > 0) r[i] = a.ring[place];
+                    else a.ring[place] = r[i];
+                }
+            }
         }
         // the pages taken so far: the sum up to the last sequence that took one
         int64_t mine = more > 0 ? sum.need : 0;
@@ -144,27 +151,54 @@ __global__ void __launch_bounds__(kSlotsThreads) slots_plan_kernel(const SlotsAr
         }
 }
 
-__global__ void __launch_bounds__(256) slots_tokens_kernel(const SlotsArgs a) {
+// Four neighbouring tokens per thread; VECTOR: rows of whole int4.
+template <bool VECTOR>
+__global__ void __launch_bounds__(256) slots_tokens_kernel(const SlotsArgs a, int per_row) {
     pdl_trigger();
     pdl_wait();
-    const int64_t n = a.B * a.T;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t b = i / a.T;
-        const int granted = a.granted[b];
-        put_token(a, b, i - b * a.T, a.lengths_out[b] - granted, granted);
+    const int64_t b = blockIdx.x / per_row, t0 = ((int64_t)(blockIdx.x - b * per_row) * 256 + threadIdx.x) * 4;
+    if (t0 >= a.T) return;
+    const int granted = a.granted[b], first = a.lengths_out[b] - granted;
+    int slot[4], pos[4], page = -1, entry = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        slot[i] = pos[i] = -1;
+        if (t0 + i < granted) {
+            pos[i] = first + (int)t0 + i;
+            if (pos[i] >> a.page_shift != page) {
+                page = pos[i] >> a.page_shift;
+                entry = a.table[b * a.width + page];
+            }
+            if (entry >= 0 && entry < a.pages) slot[i] = (entry << a.page_shift) + (pos[i] & ((1 << a.page_shift) - 1));
+        }
+    }
+    const int64_t at = b * a.T + t0;
+    if (VECTOR) {
+        *reinterpret_cast<int4 *>(a.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *reinterpret_cast<int4 *>(a.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t0 + i < a.T) {
+                a.slots[at + i] = slot[i];
+                a.positions[at + i] = pos[i];
+            }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_page_slots(const SlotsArgs &a, int sm_count, cudaStream_t s) {
+cudaError_t launch_page_slots(const SlotsArgs &a, cudaStream_t s) {
     const int64_t n = a.B * a.T;
     const bool one = n <= kSlotsOneBlock;
     const unsigned threads = a.B <= 256 && n <= 256 ? 256 : kSlotsThreads;
     cudaError_t e = launch_dependent(slots_plan_kernel, 1, threads, 0, s, a, one);
     if (e != cudaSuccess || one) return e;
-    const int64_t blocks = (n + 255) / 256, most = (int64_t)(sm_count > 0 ? sm_count : 152) * 8;
-    return launch_dependent(slots_tokens_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, s, a);
+    const int64_t per_row = (a.T + 1023) / 1024, blocks = a.B * per_row;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const bool vec = a.T % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+    return vec ? launch_dependent(slots_tokens_kernel<true>, (unsigned)blocks, 256, 0, s, a, (int)per_row)
+               : launch_dependent(slots_tokens_kernel<false>, (unsigned)blocks, 256, 0, s, a, (int)per_row);
 }
 
 }  // namespace gdn
