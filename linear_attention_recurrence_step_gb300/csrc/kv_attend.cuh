@@ -135,11 +135,15 @@ template <int N> __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// First index of block c's part of a line of W chunks; the block of index x.
-__device__ __forceinline__ int64_t part_begin(int64_t c, int64_t W, int64_t N) { return c * W / N; }
-__device__ __forceinline__ int64_t part_of(int64_t x, int64_t W, int64_t N) { return ((x + 1) * N - 1) / W; }
-
-__device__ __forceinline__ int64_t parts_of(int64_t W, int64_t blocks) { return W < blocks ? W : blocks; }
+// A line of W chunks is cut in as many parts as there are blocks (a constant: the
+// quotient is a product), or in chunks if there are fewer: the first index of block
+// c's part; the block of index x.
+template <int BLOCKS> __device__ __forceinline__ int64_t part_begin(int c, int64_t W) {
+    return W < BLOCKS ? min((int64_t)c, W) : (int64_t)((uint64_t)c * (uint64_t)W / BLOCKS);
+}
+template <int BLOCKS> __device__ __forceinline__ int part_of(int64_t x, int64_t W) {
+    return W < BLOCKS ? (int)x : (int)(((x + 1) * BLOCKS - 1) / W);
+}
 
 // The workspace: where each pair begins in the line, then two partial results
 // per block (O, the reference and the sum of each row).
@@ -197,7 +201,7 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
     const unsigned char *ring = smem + S::kQ + warp * NS * S::kTileBytes;
     const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
 
-    int64_t at, end, W = 0;
+    int64_t at, end;
     if (!whole) {
         int64_t carry = 0;
         for (int p0 = 0; p0 < pairs; p0 += kThreads) {
@@ -219,10 +223,10 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
             __syncthreads();
         }
         if (tid == 0) base[pairs] = carry;
-        W = carry;
-        const int64_t N = parts_of(W, gridDim.x);
-        at = blockIdx.x < N ? part_begin(blockIdx.x, W, N) : W;
-        end = blockIdx.x < N ? part_begin(blockIdx.x + 1, W, N) : W;
+        const int64_t W = carry;
+        constexpr int BLOCKS = kSms * resident(NB, D, sizeof(T) == 4);
+        at = part_begin<BLOCKS>((int)blockIdx.x, W);
+        end = part_begin<BLOCKS>((int)blockIdx.x + 1, W);
         __syncthreads();
         // where the pairs begin, for the kernel that joins
         if (blockIdx.x == 0)
@@ -699,10 +703,10 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
 // Joins the parts of a unit that several blocks worked on: a block per query
 // row, each of its warps every eighth part.
 constexpr int kJoinWarps = 8;
-template <typename T, int D>
+template <typename T, int D, int NB>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int unit_rows, int rows, int blocks) {
-    constexpr int PER = D / 32;
+attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int rows) {
+    constexpr int PER = D / 32, unit_rows = 8 * NB, BLOCKS = kSms * resident(NB, D, sizeof(T) == 4);
     __shared__ float sm[kJoinWarps], sl[kJoinWarps], so[kJoinWarps][D];
     pdl_trigger();
     pdl_wait();
@@ -712,13 +716,12 @@ attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int unit_rows,
     const int64_t *base = reinterpret_cast<const int64_t *>(a.workspace);
     const int64_t begin = base[p], chunks = (base[p + 1] - begin) / a.H, W = base[pairs];
     if (chunks == 0) return;
-    const int64_t N = parts_of(W, blocks);
     const int64_t x0 = begin + h * chunks, x1 = x0 + chunks;
-    const int b0 = (int)part_of(x0, W, N), b1 = (int)part_of(x1 - 1, W, N);
+    const int b0 = part_of<BLOCKS>(x0, W), b1 = part_of<BLOCKS>(x1 - 1, W);
     if (b0 == b1) return;  // written whole
     const Span s = span_of(a, p, row_blocks, unit_rows);
     if (row >= s.rows) return;
-    const int later = part_begin(b0, W, N) < x0;  // the unit is not the first of block b0
+    const int later = part_begin<BLOCKS>(b0, W) < x0;  // the unit is not the first of block b0
     float m = -1e30f, l = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
@@ -777,8 +780,8 @@ cudaError_t launch_tdn(const AttendArgs &a, cudaStream_t s) {
     e = launch_dependent(attend_kernel<T, D, NB>, (unsigned)blocks, kThreads, smem, s, a, (int)pairs, (int)rb, false);
     if (e != cudaSuccess) return e;
     const int rows = (int)std::min<int64_t>(all, ROWS);
-    return launch_dependent(attend_join_kernel<T, D>, (unsigned)(units * rows), 32 * kJoinWarps, 0, s, a, (int)pairs,
-                            (int)rb, ROWS, rows, blocks);
+    return launch_dependent(attend_join_kernel<T, D, NB>, (unsigned)(units * rows), 32 * kJoinWarps, 0, s, a, (int)pairs,
+                            (int)rb, rows);
 }
 
 template <typename T, int D>

@@ -26,6 +26,13 @@ __device__ __forceinline__ float beside(float q, float a, float b) {
                    : r < 0.f ? __uint_as_float(__float_as_uint(q) - 1u) : q;
 }
 
+// The larger one, a NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // Where a (token, kv, head, group) of the flat index lies.
 struct Place {
     int64_t token;
@@ -91,6 +98,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvArgs a, i
             for (int f = 0; f < VEC; ++f) u[e + f] = v[f];
         }
         const float *hs = p.value ? a.v_scale : a.k_scale;
+        bool any = sizeof(T) == 4;  // u may be any float
         if (hs) {
             // a power of two divides exactly by its reciprocal, any other number by division
             const float g = hs[p.head], r = 1.f / g;
@@ -98,16 +106,21 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvArgs a, i
 #pragma unroll
                 for (int e = 0; e < 16; ++e) u[e] *= r;
             } else {
+                any = true;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) u[e] /= g;
             }
         }
         float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            // finite from here on: a NaN is a zero, infinities are the largest value
-            u[e] = u[e] == u[e] ? fminf(fmaxf(u[e], -3.4e38f), 3.4e38f) : 0.f;
-            top = fmaxf(top, fabsf(u[e]));
+        for (int e = 0; e < 16; ++e) top = max_nan(top, fabsf(u[e]));
+        if (!(top < INFINITY)) {  // a NaN is written as zero, an infinity as the largest value
+            top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                u[e] = u[e] == u[e] ? fminf(fmaxf(u[e], -3.4e38f), 3.4e38f) : 0.f;
+                top = fmaxf(top, fabsf(u[e]));
+            }
         }
         sb = f32_to_e4m3(beside(top / 6.f, top, 6.f));
         const float s = f16_lo(e4m3x2_to_f16(sb));
@@ -118,11 +131,12 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const KvArgs a, i
             float q[2];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                const float m = fabsf(u[e + f]);
-                float x = m * inv;
-                x = fmaf(fmaf(-x, s, m), inv, x);  // the quotient's nearest float
-                if (s > 0.f && sizeof(T) == 4) x = beside(x, m, s);
-                q[f] = copysignf(x, u[e + f]);
+                // the quotient's nearest float; of 16-bit values' none but a border itself
+                // is one
+                float x = u[e + f] * inv;
+                x = fmaf(fmaf(-x, s, u[e + f]), inv, x);
+                if (any && s > 0.f) x = copysignf(beside(fabsf(x), fabsf(u[e + f]), s), u[e + f]);
+                q[f] = x;
             }
             word[e / 8] |= f32_to_e2m1x2(q[0], q[1]) << (4 * (e % 8));
         }
