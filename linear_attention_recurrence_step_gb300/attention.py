@@ -25,6 +25,8 @@ from collections import namedtuple
 
 import torch
 
+import linear_attention_recurrence_step_gb300 as _pkg
+
 from . import DTYPE_CODES, _check, _empty, _need, _need_workspace, load
 from .layer import _dense, _device_of, _lib, _shape, _stream, _strided
 
@@ -45,7 +47,6 @@ def _int_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected a CUDA device")
     dev = t.get_device()
-    import linear_attention_recurrence_step_gb300 as _pkg
     if not (_pkg._one_device or _pkg._is_current(dev)):
         raise _pkg._other_device(dev)
     return dev

@@ -38,6 +38,9 @@ int shift_of(int64_t page) {
 bool page_ok(int64_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 bool head_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
+// Tokens of a sequence: places counted in tiles do not pass 31 bits.
+constexpr int64_t kMaxRow = INT32_MAX - 4096;
+
 // The sizes of a cache that slots of int32 can name, in bytes, or -1.
 int64_t cache_bytes(int64_t pages, int64_t H, int64_t page, int64_t D) {
     int64_t slots;
@@ -96,7 +99,7 @@ gdn_status gdn_page_slots(const int32_t *lengths, const int32_t *add, const int3
     const int64_t b_b = nbytes({B}, 4), bt_b = nbytes({B, T}, 4), table_b = nbytes({B, width}, 4);
     int64_t slots_all, row_all;
     if (b_b < 0 || bt_b < 0 || table_b < 0 || !mul_ok(pages, page, &slots_all) || slots_all > INT32_MAX ||
-        !mul_ok(width, page, &row_all) || row_all > INT32_MAX || T > INT32_MAX || B > INT32_MAX)
+        !mul_ok(width, page, &row_all) || row_all > kMaxRow || T > kMaxRow || B > INT32_MAX)
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: sizes overflow (pages * page and width * page fit int32)", fn);
     const int64_t ring_b = pages * 4;
     if (!apart_or_same(lengths_out, lengths, b_b) || !apart_or_same(held_out, held, b_b) ||
@@ -335,7 +338,7 @@ gdn_status gdn_kv_attention(const void *q, const void *cache, const int32_t *blo
     const int64_t y_b = nbytes({B, T, Hq, D}, eb), l_b = nbytes({B, T, Hq}, 4), t_b = nbytes({B, width}, 4);
     const int64_t c_b = cache_bytes(pages, H, page, D);
     int64_t row_all;
-    if (y_b < 0 || l_b < 0 || t_b < 0 || c_b < 0 || !mul_ok(width, page, &row_all) || row_all > INT32_MAX ||
+    if (y_b < 0 || l_b < 0 || t_b < 0 || c_b < 0 || !mul_ok(width, page, &row_all) || row_all > kMaxRow ||
         B > INT32_MAX || gdn::attend_workspace_bytes(B, T, Hq, H, D) < 0)
         return fail(GDN_ERR_INVALID_ARGUMENT,
                     "%s: sizes overflow (pages * page, width * page and the query rows fit int32, H 16 bits)", fn);
