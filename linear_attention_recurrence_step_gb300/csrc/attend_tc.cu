@@ -13,16 +13,24 @@
 //   issuer         S of a tile into tensor memory; then, when its probabilities
 //                  are there, O += P V with P from tensor memory.  While one
 //                  tile's softmax runs, the other tile's products do.
-//   softmax warps  thread r owns row r of its tile: S from tensor memory, once for
-//                  the maximum and once for 2^(x - reference); P as f16 over the
-//                  columns of S already read.  O is rescaled, by the row's thread,
-//                  only when the maximum is 2^8 above the reference.
+//   softmax warps  thread r owns row r of its tile: a step's scores from tensor
+//                  memory to registers, their maximum, 2^(x - reference) as f16
+//                  over the columns of S.  O is rescaled, by the row's thread, only
+//                  when a probability would pass 2^14.
 // With one tile S has two buffers instead, and S of the next step is issued
 // before O += P V of this one.
 //
 // Per 128 x 128 x 128 step of a tile: 2 x 512 cycles of products, 16384
 // exponentials and 64 KB through shared memory by the products (512 + 256
-// cycles), 32 KB of operands written (256 cycles, no bank conflicts).
+// cycles), 32 KB of operands written (256 cycles, no bank conflicts).  Measured:
+// 2048 tokens over 8192, 32 heads of 128 on 4 of the cache, in 190 us (1.27
+// PFLOP/s of products, 0.66 of a library product's rate), 369 over 16384: 1.4 us a
+// step of two tiles, and 9 us a unit for its queries, first step and output.  The
+// products and the dequant warps share the shared memory, which is what bounds
+// the steps.
+//
+// Registers: 192 for a softmax thread, so that a step's 128 scores stay in them.
+// Spills there cost most of all (106 bytes of them: 249 us for 193).
 //
 // Operands and softmax are those of kv_attend.cuh; sums stay in tensor memory
 // in float32.  Every wait is bounded; when one runs out, the unit's rows are
@@ -46,11 +54,10 @@ constexpr int kTcTile = 128;                              // query rows of a til
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;         // S buffers at 0 and 128, O from 256 on
 constexpr int kTcSms = 152;
 constexpr long long kDrainCycles = 2000000000ll;
-// A row's largest probability when its reference is set is 2^6, or, the wider the
-// scores spread, down to 2^0; the reference moves when one passes 2^14.  f16 steps
-// end at 2^-24: weights are off by 2^-12 of themselves, or by 2^-31 of the row's
-// largest (2^-25 if the scores spread over 24 bits or more).
-constexpr float kTcBoost = 6.f, kTcRoom = 6.f, kTcMost = 14.f;
+// A row's largest probability when its reference is set is 2^6; the reference
+// moves when one passes 2^14.  f16 steps end at 2^-24: weights are off by 2^-12 of
+// themselves, or by 2^-31 of the row's largest.
+constexpr float kTcBoost = 6.f, kTcMost = 14.f;
 
 template <int D> struct Tc {
     static constexpr int kTiles = D == 256 ? 1 : 2;
@@ -348,9 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
 #pragma unroll
             for (int e = 4; e < TN; ++e) tops[e % 4] = fmaxf(tops[e % 4], v[e]);
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            // The reference moves (and sum and O with it) only when a probability would
-            // pass 2^14; then above the maximum, the more the wider the scores spread:
-            // later ones rise higher, and small probabilities matter less.
+            // the reference moves, and sum and O with it
             if (__any_sync(0xffffffffu, fmaf(top, c, -off) > kTcMost)) {
                 const float to = top == -INFINITY ? off : fmaxf(off, top * c - kTcBoost);
                 const float f = exp2f(off - to);
@@ -657,7 +662,8 @@ TcPlan tc_plan(int64_t B, int64_t rows, int64_t H, int64_t D) {
     TcPlan p{B * ((rows + unit_rows - 1) / unit_rows) * H, 0, 1, (int)((std::min(rows, unit_rows) + 7) / 8 * 8)};
     // Units of 1.5 times the SMs on are left whole: cut, they would be dealt out
     // little more evenly (256 over 152 SMs: 112 steps instead of 118), and have to
-    // be joined.
+    // be joined.  Fewer are cut, into two parts an SM, or four of few rows: 256 rows of
+    // one sequence of 8192 tokens and 8 heads 54 us whole, 23 cut.
     if (2 * p.units < 3 * kTcSms) p.parts = (int)std::min<int64_t>((p.part_rows > 64 ? 2 : 4) * kTcSms / p.units, 64);
     if (p.parts > 1) p.workspace = p.units * p.parts * (D + 2) * p.part_rows * 4;
     else p.parts = 1;
