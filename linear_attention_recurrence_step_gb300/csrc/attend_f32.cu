@@ -7,7 +7,7 @@ cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t s) { return laun
 
 int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D) {
     int64_t rows, pairs;
-    if (__builtin_mul_overflow(T, Hq / H, &rows) || rows > INT32_MAX - 64) return -1;
+    if (H > 65535 || __builtin_mul_overflow(T, Hq / H, &rows) || rows > INT32_MAX - 64) return -1;
     const int NB = eights_of(rows);
     if (__builtin_mul_overflow(B, (rows + 8 * NB - 1) / (8 * NB), &pairs) || pairs > INT32_MAX) return -1;
     // whichever form the call takes

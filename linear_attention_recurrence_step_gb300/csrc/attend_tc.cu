@@ -1,8 +1,8 @@
 // attend_tc.cu -- attention of many query rows over the 4-bit paged cache
 // (prompts), on tcgen05.
 //
-// A unit is up to 256 query rows (two tiles of 128; one tile for heads of 256) of
-// one sequence and key head.  A CTA takes a unit, or, where there are few, an equal
+// A unit is up to 256 query rows (two tiles of 128; one tile for heads of 256, and
+// where a sequence has no more rows) of one sequence and key head.  A CTA takes a unit, or, where there are few, an equal
 // part of its tokens (a second kernel joins the parts, in order), TN = 128 tokens
 // (64 for heads of 256) at a time.  Roles:
 //   dequant warps  codes from global memory, a step ahead in registers, to exact
@@ -59,11 +59,11 @@ constexpr long long kDrainCycles = 2000000000ll;
 // themselves, or by 2^-31 of the row's largest.
 constexpr float kTcBoost = 6.f, kTcMost = 14.f;
 
-template <int D> struct Tc {
-    static constexpr int kTiles = D == 256 ? 1 : 2;
+template <int D, int TILES> struct Tc {
+    static constexpr int kTiles = TILES;
     static constexpr int kRows = kTiles * kTcTile;
     static constexpr int kTok = D == 256 ? 64 : 128;       // tokens per step
-    static constexpr int kDqWarps = D == 256 ? 8 : 4;
+    static constexpr int kDqWarps = 12 - 4 * TILES;
     static constexpr uint32_t kQBytes = kRows * D * 2, kOpBytes = kTok * D * 2;  // K or V of a step
     static constexpr uint32_t kQ = 0, kK = kQBytes, kV = kK + 2 * kOpBytes, kBars = kV + 2 * kOpBytes;
     static constexpr size_t kSmem = kBars + 256 + 1024;    // (1024: alignment)
@@ -184,8 +184,8 @@ struct TcArgs {
 struct TcSpan {
     int r0, rows, n, len, lo, hi, step0, steps;
 };
-template <int D> __device__ __forceinline__ TcSpan tc_span(const AttendArgs &a, int b, int rb) {
-    using L = Tc<D>;
+template <int D, int TILES> __device__ __forceinline__ TcSpan tc_span(const AttendArgs &a, int b, int rb) {
+    using L = Tc<D, TILES>;
     TcSpan s;
     const int G = a.Hq / a.H;
     s.n = a.fresh ? min(max(a.fresh[b], 0), (int)a.T) : (int)a.T;
@@ -200,9 +200,9 @@ template <int D> __device__ __forceinline__ TcSpan tc_span(const AttendArgs &a, 
     return s;
 }
 
-template <typename T, int D>
+template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs ta) {
-    using L = Tc<D>;
+    using L = Tc<D, TILES>;
     constexpr int TN = L::kTok;
     const AttendArgs &a = ta.a;
     extern __shared__ unsigned char smem_raw[];
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
     // later row blocks see more tokens: those first
     const int ordered = (int)(gridDim.x - 1 - blockIdx.x), u = ordered / ta.parts, part = ordered - u * ta.parts;
     const int h = u % a.H, b = u / a.H % (int)a.B, rb = u / a.H / (int)a.B;
-    const TcSpan span = tc_span<D>(a, b, rb);
+    const TcSpan span = tc_span<D, TILES>(a, b, rb);
     const int n = span.n, len = span.len, r0 = span.r0, rows = span.rows, lo = span.lo, hi = span.hi;
     const int tiles = rows > kTcTile ? 2 : 1;
     const int j0 = (int)((int64_t)part * span.steps / ta.parts);
@@ -331,6 +331,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             const unsigned present = __ballot_sync(0xffffffffu, (uint32_t)ids < pool);  // bit i: tokens 16 i on
             ids = pages_of(j + 1);
             if (!wait(kSFull + buf, tiles == 2 ? j : j >> 1)) break;
+            if (t * kTcTile + (row & ~31) >= rows) {  // none of the warp's rows: what S holds is no one's P
+                if (lane == 0) mbar_arrive(bar(kPFull + buf));
+                continue;
+            }
             tm_after();
             const int tok0 = (step0 + j) * TN;
             const bool edge = tok0 < all_lo || tok0 + TN > all_hi || present != (1u << (TN / 16)) - 1u;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
         }
 
         // ------------------------------------------------ the row's output
-        if (t < tiles && rows > 0) {
+        if (t < tiles && t * kTcTile + (row & ~31) < rows) {
             if (steps > 0) wait(kODone + t, steps - 1);
             tm_after();
             const bool there = t * kTcTile + row < rows;
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                     a.lse[((int64_t)b * a.T + qt) * a.Hq + h * G + r - qt * G] =
                         !ok ? bad : sum == 0.f ? -INFINITY : (off + log2f(sum)) * 0.693147180559945309f;
                 }
-            } else if (t * kTcTile + (row & ~31) < rows) {
+            } else {
                 // (channel d of row i at [d][i], so that a warp's stores are whole lines)
                 float *ws = a.workspace + ((int64_t)u * ta.parts + part) * ((D + 2) * (int64_t)ta.part_rows);
                 const int i = t * kTcTile + row;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             }
         }
     } else if (warp < 12) {
-        less_registers<D == 256 ? 120 : 88>();
+        less_registers<TILES == 1 ? 120 : 88>();
         // ================================================ dequant warps
         // A job is 32 neighbouring channels of a token: 16 bytes of codes, two
         // scales.  D/32 lanes share a token; a warp's jobs are neighbouring tokens,
@@ -495,8 +499,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             chunk[k] = (uint32_t)panel * (TN * 128) + first * 128 + ((((piece & 1) * 4 + (k ^ order)) ^ (first & 7)) << 4);
-        uint2 kq[JOBS][2], vq[JOBS][2];
-        uint32_t ks[JOBS], vs[JOBS];
+        // steps read ahead: two where a warp's share of one is few registers
+        constexpr int AHEAD = JOBS <= 2 ? 2 : 1;
+        uint2 kq[AHEAD][JOBS][2], vq[AHEAD][JOBS][2];
+        uint32_t ks[AHEAD][JOBS], vs[AHEAD][JOBS];
         auto load = [&](int j, int ids, int at, uint2 (&q)[JOBS][2], uint32_t (&sc)[JOBS]) {
             const int t0 = (step0 + j) * TN;
             const bool full = t0 >= lo && t0 + TN <= hi;
@@ -538,21 +544,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
             asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
             __syncwarp();
         };
-        int ids = pages_of(0), ids_next = pages_of(1);
-        load(0, ids, 0, kq, ks);
-        load(0, ids, values, vq, vs);
-        for (int j = 0; j < steps; ++j) {
-            const int st = j & 1;
-            ids = ids_next;
-            ids_next = pages_of(j + 2);
-            if (j >= 2 && !wait(kKFree + st, (j >> 1) - 1)) break;
-            store(base + L::kK + st * L::kOpBytes, kq, ks);
-            if (lane == 0) mbar_arrive(bar(kKFull + st));
-            load(j + 1, ids, 0, kq, ks);
-            if (j >= 2 && !wait(kVFree + st, (j >> 1) - 1)) break;
-            store(base + L::kV + st * L::kOpBytes, vq, vs);
-            if (lane == 0) mbar_arrive(bar(kVFull + st));
-            load(j + 1, ids, values, vq, vs);
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p) {
+            const int ids = pages_of(p);
+            load(p, ids, 0, kq[p], ks[p]);
+            load(p, ids, values, vq[p], vs[p]);
+        }
+        int ids_next = pages_of(AHEAD);
+        for (int j0 = 0; j0 < steps && ok; j0 += AHEAD) {
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p) {
+                const int j = j0 + p, st = j & 1, ids = ids_next;
+                if (j >= steps) break;
+                ids_next = pages_of(j + AHEAD + 1);
+                if (j >= 2 && !wait(kKFree + st, (j >> 1) - 1)) break;
+                store(base + L::kK + st * L::kOpBytes, kq[p], ks[p]);
+                if (lane == 0) mbar_arrive(bar(kKFull + st));
+                load(j + AHEAD, ids, 0, kq[p], ks[p]);
+                if (j >= 2 && !wait(kVFree + st, (j >> 1) - 1)) break;
+                store(base + L::kV + st * L::kOpBytes, vq[p], vs[p]);
+                if (lane == 0) mbar_arrive(bar(kVFull + st));
+                load(j + AHEAD, ids, values, vq[p], vs[p]);
+            }
         }
     } else {
         less_registers<40>();
@@ -609,14 +622,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
 }
 
 // Joins a unit's parts: a block per eight of its rows.
-template <typename T, int D>
+template <typename T, int D, int TILES>
 __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a, int parts, int part_rows, int groups) {
     __shared__ float so[D][9];
     pdl_trigger();
     pdl_wait();
     const int u = blockIdx.x / groups, i0 = (blockIdx.x - u * groups) * 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = u % a.H, b = u / a.H % (int)a.B, rb = u / a.H / (int)a.B, G = a.Hq / a.H;
-    const TcSpan s = tc_span<D>(a, b, rb);
+    const TcSpan s = tc_span<D, TILES>(a, b, rb);
     if (i0 >= s.rows) return;
     // eight neighbouring rows of a channel are 32 bytes: the lane of channel
     // lane / 8 of the warp's four and row lane % 8 adds them up
@@ -652,31 +665,36 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a,
     }
 }
 
+// Tiles of a unit: one where a sequence has no more rows (the second tile's warps
+// then help to dequantise).
+int tc_tiles(int64_t rows, int64_t D) { return D == 256 || rows <= kTcTile ? 1 : 2; }
 // How a call is laid out: units, and in how many parts each is cut.
 struct TcPlan {
     int64_t units, workspace;
     int parts, part_rows;
 };
 TcPlan tc_plan(int64_t B, int64_t rows, int64_t H, int64_t D) {
-    const int64_t unit_rows = D == 256 ? kTcTile : 2 * kTcTile;
+    const int64_t unit_rows = tc_tiles(rows, D) * kTcTile;
     TcPlan p{B * ((rows + unit_rows - 1) / unit_rows) * H, 0, 1, (int)((std::min(rows, unit_rows) + 7) / 8 * 8)};
     // Units of 1.5 times the SMs on are left whole: cut, they would be dealt out
     // little more evenly (256 over 152 SMs: 112 steps instead of 118), and have to
-    // be joined.  Fewer are cut, into two parts an SM, or four of few rows: 256 rows of
-    // one sequence of 8192 tokens and 8 heads 54 us whole, 23 cut.
-    if (2 * p.units < 3 * kTcSms) p.parts = (int)std::min<int64_t>((p.part_rows > 64 ? 2 : 4) * kTcSms / p.units, 64);
+    // be joined.  Fewer are cut, into one part an SM in all, or two of two tiles: 256
+    // rows of one sequence of 8192 tokens and 8 heads 54 us whole, 23 cut; 32 to 128
+    // rows of 16 sequences of up to 8192 tokens 79 us whole, 81 in two parts each and
+    // 88 in four.
+    if (2 * p.units < 3 * kTcSms) p.parts = (int)std::min<int64_t>(tc_tiles(rows, D) * kTcSms / p.units, 64);
     if (p.parts > 1) p.workspace = p.units * p.parts * (D + 2) * p.part_rows * 4;
     else p.parts = 1;
     return p;
 }
 
-template <typename T, int D>
+template <typename T, int D, int TILES>
 cudaError_t launch_tc(const AttendArgs &a, cudaStream_t s) {
-    using L = Tc<D>;
+    using L = Tc<D, TILES>;
     void *flag = nullptr;
     cudaError_t e = cudaGetSymbolAddress(&flag, g_attend_tc_wait_flag);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attend_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+    e = cudaFuncSetAttribute(attend_tc_kernel<T, D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
     if (e != cudaSuccess) return e;
     const TcPlan p = tc_plan(a.B, a.T * (a.Hq / a.H), a.H, D);
     if (p.units * p.parts > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -684,18 +702,19 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t s) {
     const int64_t steps = ((int64_t)a.width << a.page_shift) / L::kTok;
     const int parts = (int)std::max<int64_t>(std::min<int64_t>(p.parts, steps / 6), 1);
     TcArgs ta{a, parts, p.part_rows, static_cast<unsigned *>(flag), wait_bound_cycles(), inject_wait_expiry()};
-    e = launch_dependent(attend_tc_kernel<T, D>, (unsigned)(p.units * parts), kTcThreads, L::kSmem, s, ta);
+    e = launch_dependent(attend_tc_kernel<T, D, TILES>, (unsigned)(p.units * parts), kTcThreads, L::kSmem, s, ta);
     if (e != cudaSuccess || parts == 1) return e;
     const int groups = p.part_rows / 8;
-    return launch_dependent(attend_tc_join_kernel<T, D>, (unsigned)(p.units * groups), 256, 0, s, a, parts, p.part_rows, groups);
+    return launch_dependent(attend_tc_join_kernel<T, D, TILES>, (unsigned)(p.units * groups), 256, 0, s, a, parts, p.part_rows, groups);
 }
 
 template <typename T>
 cudaError_t launch_t(const AttendArgs &a, cudaStream_t s) {
+    const bool one = tc_tiles(a.T * (a.Hq / a.H), a.D) == 1;
     switch (a.D) {
-    case 64: return launch_tc<T, 64>(a, s);
-    case 128: return launch_tc<T, 128>(a, s);
-    case 256: return launch_tc<T, 256>(a, s);
+    case 64: return one ? launch_tc<T, 64, 1>(a, s) : launch_tc<T, 64, 2>(a, s);
+    case 128: return one ? launch_tc<T, 128, 1>(a, s) : launch_tc<T, 128, 2>(a, s);
+    case 256: return launch_tc<T, 256, 1>(a, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -704,11 +723,16 @@ cudaError_t launch_t(const AttendArgs &a, cudaStream_t s) {
 
 int64_t attend_tc_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D) {
     const int64_t rows = T * (Hq / H);
-    return attend_tc_rows(rows) ? tc_plan(B, rows, H, D).workspace : 0;
+    return attend_tc_rows(B * H, rows) ? tc_plan(B, rows, H, D).workspace : 0;
 }
 
-bool attend_tc_rows(int64_t rows) { return rows > 64; }
-bool attend_takes_tc(DType dt, const AttendArgs &a) { return dt != DType::F32 && attend_tc_rows(a.T * (a.Hq / a.H)); }
+// The rows of a (sequence, key head) from which they go here and not to
+// kv_attend.cuh's kernel: 16 sequences of up to 8192 tokens and 8 heads take 79 us
+// here with 32 to 128 rows, there 72 (32 rows), 78 (48), 108 (64) and 172 (128); one
+// sequence, which has to be joined here, 22 to 23 us here, there 14 (64 rows), 22
+// (128 and 256).
+bool attend_tc_rows(int64_t units, int64_t rows) { return rows > (2 * units >= kTcSms ? 48 : 64); }
+bool attend_takes_tc(DType dt, const AttendArgs &a) { return dt != DType::F32 && attend_tc_rows(a.B * a.H, a.T * (a.Hq / a.H)); }
 
 cudaError_t launch_attend_tc(DType dt, const AttendArgs &a, cudaStream_t s) {
     return dt == DType::BF16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<__half>(a, s);
