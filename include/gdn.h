@@ -605,7 +605,7 @@ gdn_status gdn_sample(const void *logits, const float *noise,
  *                   its input's own buffer.  With other buffers a repeated call
  *                   gives the same results.
  * Counts that are negative or too large act as the nearest that is possible.
- * One kernel, two for more than 8192 slots.
+ * One kernel, two for more than 2048 slots.
  */
 gdn_status gdn_page_slots(const int32_t *lengths, const int32_t *add,
                           const int32_t *held, const int32_t *ring_state,
@@ -739,10 +739,11 @@ int gdn_abi_version(void);
  *
  * The pipelined paths (the tcgen05 record kernel behind gdn_step_record and
  * gdn_step_record_mapped, the persistent replay behind gdn_state_replay and
- * gdn_state_replay_per_seq, and gdn_chunk_replay) run stages that wait on
+ * gdn_state_replay_per_seq, gdn_chunk_replay, and gdn_kv_attention's kernel for
+ * many query rows) run stages that wait on
  * each other through mbarriers.  Every such wait gives up after a
  * bound (about a second of GPU clock by default) instead of hanging; the
- * kernel then writes NaN to the state rows it could not finish, lets its
+ * kernel then writes NaN to the state or output rows it could not finish, lets its
  * copies and products in flight land, and raises a device-side flag.  The
  * call that launched it still returned GDN_OK (it only enqueues work), so a
  * caller that wants to know reads the flag here: *expired is set to 1 if any

@@ -12,8 +12,9 @@ int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int6
     if (__builtin_mul_overflow(B, (rows + 8 * NB - 1) / (8 * NB), &pairs) || pairs > INT32_MAX) return -1;
     // whichever form the call takes
     const int64_t tc = attend_tc_workspace_bytes(B, T, Hq, H, D);
-    if (!cut(pairs, H)) return tc;
-    const int64_t own = ((int64_t)2 * kSms * resident(NB, (int)D, false) * partial_floats(8 * NB, (int)D) + kBaseFloats) * 4;
+    const int blocks = kSms * resident(NB, (int)D, false);  // (no fewer than for f32)
+    if (!cut(pairs, H, blocks)) return tc;
+    const int64_t own = ((int64_t)2 * blocks * partial_floats(8 * NB, (int)D) + kBaseFloats) * 4;
     return own > tc ? own : tc;
 }
 

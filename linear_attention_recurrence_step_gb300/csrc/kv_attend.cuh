@@ -761,9 +761,11 @@ attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int rows) {
     }
 }
 
-// A call is cut along its tokens while its units would not fill the GPU by
-// themselves several times over.
-bool cut(int64_t pairs, int64_t H) { return pairs <= kMaxPairs && pairs * H < 24 * kSms; }
+// A call is cut along its tokens while its units do not fill the GPU by themselves:
+// then equal parts are worth the second kernel.  Tokens of up to 4096, 8 key heads:
+// 512 units of 8 rows 57 us cut, 64 whole; 1024 100 and 97; 2048 180 and 157; 384 units
+// of 16 rows 90 and 101; 512 94 and 78; 1024 161 and 127.
+bool cut(int64_t pairs, int64_t H, int blocks) { return pairs <= kMaxPairs && pairs * H < blocks; }
 
 template <typename T, int D, int NB>
 cudaError_t launch_tdn(const AttendArgs &a, cudaStream_t s) {
@@ -773,11 +775,11 @@ cudaError_t launch_tdn(const AttendArgs &a, cudaStream_t s) {
     constexpr size_t smem = S::kBytes;
     cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    if (!cut(pairs, a.H)) {
+    const int blocks = kSms * resident(NB, D, sizeof(T) == 4);
+    if (!cut(pairs, a.H, blocks)) {
         if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
         return launch_dependent(attend_kernel<T, D, NB>, (unsigned)units, kThreads, smem, s, a, (int)pairs, (int)rb, true);
     }
-    const int blocks = kSms * resident(NB, D, sizeof(T) == 4);
     e = launch_dependent(attend_kernel<T, D, NB>, (unsigned)blocks, kThreads, smem, s, a, (int)pairs, (int)rb, false);
     if (e != cudaSuccess) return e;
     const int rows = (int)std::min<int64_t>(all, ROWS);

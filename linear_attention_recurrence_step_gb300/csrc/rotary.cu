@@ -7,11 +7,11 @@
 // whole turns by itself, and the upper 32 bits are the fraction, off by 2^-32
 // of a turn and 2^-53 of inv_freq per step at most.
 //
-// Bound by memory: every element is read once and written once.  A block makes
-// the sines of its tokens once, in shared memory, and uses them for all heads of q
-// and k; a thread takes the same piece of all of the block's tokens, so that where
-// it lies in a token is worked out once and four loads are in flight (4096 tokens
-// of 40 heads of 128: 26.8 us with a token's pieces one after the other).
+// Bound by memory: every element is read once and written once (84 MB of 4096
+// tokens of 40 heads of 128: 15.3 us from and to L2, 25.7 with cold caches).  A block
+// makes the sines of its tokens once, in shared memory, and uses them for all heads of
+// q and k; a thread takes the same piece of all of the block's tokens, so that where
+// it lies in a token is worked out once and their loads are in flight together.
 #include "attend.h"
 #include "pieces.cuh"
 
@@ -123,11 +123,13 @@ cudaError_t launch_tb(const RotaryArgs &a, cudaStream_t s) {
                   : launch_dependent(rotary_kernel<T, VEC, false, TB>, (unsigned)blocks, kRotThreads, smem, s, a);
 }
 
-// Several tokens per block once there are enough of them to fill the SMs (and
-// their sines fit the shared memory that needs no asking).
+// Four tokens per block once blocks of one fill the SMs some four times over (and
+// their sines fit the shared memory that needs no asking).  40 heads of 128: 2048
+// tokens 8.8 us with one per block, 10.2 with four; 4096 15.3 and 16.7; 8192 34.6 and
+// 30.2; 16384 64.2 and 55.7.
 template <typename T, int VEC>
 cudaError_t launch_t(const RotaryArgs &a, int sm_count, cudaStream_t s) {
-    const bool many = a.B * a.T > (int64_t)(sm_count > 0 ? sm_count : 152) * 8 && a.R <= 2048;
+    const bool many = a.B * a.T > (int64_t)(sm_count > 0 ? sm_count : 152) * 32 && a.R <= 2048;
     return many ? launch_tb<T, VEC, 4>(a, s) : launch_tb<T, VEC, 1>(a, s);
 }
 

@@ -82,3 +82,53 @@ def test_nonfinite_rows_of_tiles(dev, T, L):  # noqa: F811
     bad = torch.zeros(1, T, 8, dtype=torch.bool)
     bad[0, 1, 2] = bad[0, T - 1, 7] = True
     assert torch.equal(o.y.isnan().all(-1).cpu(), bad) and torch.equal(o.y.isnan().any(-1).cpu(), bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,T,Hq,window", [(64, 1, 32, 0), (128, 3, 64, 0), (256, 2, 32, 30)])
+def test_many_units(dev, dtype, D, T, Hq, window):  # noqa: F811
+    """Units that fill the GPU by themselves are not cut: of 8 rows and of 16, some of
+    sequences without tokens."""
+    B = 62
+    attend_case(dev, dtype, B, T, Hq, 16, D, 16, [(53 * i) % 170 for i in range(B)], [(i + 1) % (T + 2) for i in range(B)],
+                window, seed=D)
+
+
+@pytest.mark.parametrize("tokens", [4864, 4865])
+def test_rotary_of_many_tokens(dev, tokens):  # noqa: F811
+    """One token per block and four: the same bits."""
+    g = torch.Generator(device=dev).manual_seed(3)
+    q = torch.randn(1, tokens, 2, 64, generator=g, device=dev).bfloat16()
+    pos = torch.randint(-1, 1 << 20, (1, tokens), generator=g, device=dev, dtype=torch.int32)
+    inv, scale = gdn.rotary_frequencies(32, device=dev)
+    y = torch.full_like(q, 7.0)
+    gdn.gdn_rotary(q, pos, inv, q_out=y, scale=scale)
+    for at in range(0, tokens, 1000):
+        piece = torch.full_like(q[:, at:at + 1000], 7.0)
+        gdn.gdn_rotary(q[:, at:at + 1000].contiguous(), pos[:, at:at + 1000].contiguous(), inv, q_out=piece, scale=scale)
+        assert torch.equal(piece, y[:, at:at + 1000])
+
+
+@pytest.mark.parametrize("B,T", [(8, 256), (3, 682), (64, 30)])
+def test_slots_by_one_kernel_and_two(dev, B, T):  # noqa: F811
+    """Tokens of a call of few slots (one kernel) and of a call of many (two): the same."""
+    g = torch.Generator().manual_seed(B)
+    page, width = 16, T // 16 + 20
+    lengths = torch.randint(0, 300, (B,), generator=g).int().to(dev)
+    held = (lengths + page - 1) // page
+    pages = B * width
+    ring = torch.randperm(pages, generator=g).int().to(dev)
+    used, outs = int(held.sum()), []
+    table = torch.zeros(B, width, dtype=torch.int32, device=dev)
+    at = 0
+    for b in range(B):
+        table[b, :int(held[b])] = ring[at:at + int(held[b])]
+        at += int(held[b])
+    add = torch.randint(0, 20, (B,), generator=g).int().to(dev)
+    for wide in (T, 4 * T):
+        tab, rg = table.clone(), ring.clone()
+        s = gdn.gdn_page_slots(lengths, add, held, ints([used, pages - used], dev), tab, rg, T=wide, page=page)
+        assert bool((s.slots[:, T:] == -1).all()) and torch.equal(s.granted, add)
+        outs.append((s.slots[:, :20].clone(), s.positions[:, :20].clone(), tab, rg, s.lengths_out, s.held_out, s.ring_state_out))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
