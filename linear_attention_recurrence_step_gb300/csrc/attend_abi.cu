@@ -30,6 +30,18 @@ bool clash(std::initializer_list<Tensor> outputs, std::initializer_list<Tensor> 
 // An output on its input: the same buffer or apart from it.
 bool apart_or_same(const void *o, const void *i, int64_t bytes) { return o == i || !over(o, bytes, i, bytes); }
 
+// Whether two [B,T,row] tensors of elements of `eb` bytes are slices of the same wider
+// rows, apart from one another: same strides, and a row of both, one behind the other,
+// still does not reach the next one.
+bool slices(const void *p, int64_t sb_p, int64_t st_p, int64_t row_p, const void *q, int64_t sb_q, int64_t st_q,
+            int64_t row_q, int64_t B, int64_t T, int eb) {
+    if ((B > 1 && sb_p != sb_q) || (T > 1 && st_p != st_q)) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q), d = a < b ? b - a : a - b;
+    const int64_t apart = (int64_t)(d / eb), first = a < b ? row_p : row_q, second = a < b ? row_q : row_p;
+    return d % eb == 0 && apart >= first && apart <= INT64_MAX - second &&
+           extent(B, sb_p, T, st_p, apart + second) >= 0;
+}
+
 int shift_of(int64_t page) {
     int s = 0;
     while (((int64_t)1 << s) < page) ++s;
@@ -174,13 +186,14 @@ gdn_status gdn_rotary(const void *q, const void *k, const int32_t *positions, co
         if (!aligned(p, eb)) return fail(GDN_ERR_MISALIGNED, "%s: a tensor is not aligned to its element size", fn);
     if (!aligned(positions, 4) || !aligned(inv_freq, 4))
         return fail(GDN_ERR_MISALIGNED, "%s: positions and inv_freq must be 4-byte aligned", fn);
-    // in place is the input's own rows; q and k may be slices of the same rows,
-    // so that their extents interlace
+    // in place is the input's own rows; q and k, or q_out and k_out, may be slices of
+    // the same rows, so that their extents interlace
     const bool q_in = q_out == q && st.q_out_b == st.q_b && st.q_out_t == st.q_t;
     const bool k_in = k && k_out == k && st.k_out_b == st.k_b && st.k_out_t == st.k_t;
     if ((!q_in && (over(q_out, qo_b, q, q_b) || over(q_out, qo_b, k, k_b))) ||
         (!k_in && (over(k_out, ko_b, k, k_b) || over(k_out, ko_b, q, q_b))) ||
-        (!(q_in && k_in) && over(q_out, qo_b, k_out, ko_b)))
+        (over(q_out, qo_b, k_out, ko_b) &&
+         !slices(q_out, st.q_out_b, st.q_out_t, qd, k_out, st.k_out_b, st.k_out_t, kd, B, T, eb)))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps another tensor without being in place", fn);
     for (const auto &[o, o_b] : {std::pair<const void *, int64_t>(q_out, qo_b), {k_out, ko_b}})
         if (over(o, o_b, positions, bt_b) || over(o, o_b, inv_freq, R * 2))

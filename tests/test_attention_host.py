@@ -202,3 +202,24 @@ def test_rotary_frequencies():
                   dict(R=8, scaling="linear", factor=0.5)):
         with pytest.raises(ValueError):
             gdn.rotary_frequencies(**wrong)
+
+
+def test_outputs_of_the_same_rows(lib):
+    """q_out and k_out may be slices of one wider row (in either order), not of each other."""
+    good = (dict(q_out=P(4), k_out=P(4) + 512, strides=(768, 256, 384, 128, 1152, 384, 1152, 384)),
+            dict(q_out=P(4) + 256, k_out=P(4), strides=(768, 256, 384, 128, 1152, 384, 1152, 384)),
+            dict(q_out=P(4), k_out=P(4) + 512, strides=(768, 256, 384, 128, 400, 800, 400, 800)))
+    bad = (dict(q_out=P(4), k_out=P(4) + 510, strides=(768, 256, 384, 128, 1152, 384, 1152, 384)),
+           dict(q_out=P(4), k_out=P(4) + 514, strides=(768, 256, 384, 128, 1152, 384, 1152, 384)),
+           dict(q_out=P(4), k_out=P(4) + 512, strides=(768, 256, 384, 128, 1152, 384, 1155, 385)),
+           # in place, but k lies on q
+           dict(q=P(0), k=P(0), q_out=P(0), k_out=P(0), strides=(1152, 384, 1152, 384, 1152, 384, 1152, 384)),
+           dict(q=P(0), k=P(0) + 256, q_out=P(0), k_out=P(0) + 256, strides=(1152, 384, 1152, 384, 1152, 384, 1152, 384)))
+    gdn.force_launch_failures(1000)
+    try:
+        for change in good:
+            assert rotary(lib, **change) == CUDA, lib.gdn_last_error()
+        for change in bad:
+            assert rotary(lib, **change) == INVALID, change
+    finally:
+        gdn.force_launch_failures(0)

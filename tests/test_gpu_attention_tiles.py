@@ -132,3 +132,17 @@ def test_slots_by_one_kernel_and_two(dev, B, T):  # noqa: F811
         outs.append((s.slots[:, :20].clone(), s.positions[:, :20].clone(), tab, rg, s.lengths_out, s.held_out, s.ring_state_out))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_into_slices(dev, layout):  # noqa: F811
+    """Both outputs in one wider buffer, whose other channels stay."""
+    g = torch.Generator(device=dev).manual_seed(4)
+    q, k = (torch.randn(2, 9, h, 64, generator=g, device=dev).half() for h in (4, 2))
+    pos = torch.randint(0, 9000, (2, 9), generator=g, device=dev, dtype=torch.int32)
+    inv, scale = gdn.rotary_frequencies(64, device=dev)
+    plain = gdn.gdn_rotary(q, pos, inv, k=k, layout=layout, scale=scale)
+    wide = torch.full((2, 9, 7, 64), 7.0, device=dev).half()
+    gdn.gdn_rotary(q, pos, inv, k=k, layout=layout, scale=scale, q_out=wide[:, :, :4], k_out=wide[:, :, 4:6])
+    assert torch.equal(wide[:, :, :4], plain.q) and torch.equal(wide[:, :, 4:6], plain.k)
+    assert bool((wide[:, :, 6] == 7.0).all())
