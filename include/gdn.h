@@ -641,7 +641,9 @@ typedef struct gdn_rotary_strides {
  *              GDN_ERR_UNSUPPORTED); frequencies stretched for long contexts
  *              are simply others, with their factor as `scale`
  *   q_out, k_out  like q and k; each may be its input's own rows (same pointer
- *              and strides), and the two may be slices of the same wider rows
+ *              and strides), and the two may be slices of the same wider rows.
+ *              Where one is in place, the other input is apart from it or
+ *              another slice of the same rows
  *   strides    of the four, or NULL (dense)
  * An angle's fraction of a turn is exact to 2^-32 and 2^-53 of inv_freq per
  * step for every position; sines and products are float32, rounded once.  One

@@ -186,12 +186,17 @@ gdn_status gdn_rotary(const void *q, const void *k, const int32_t *positions, co
         if (!aligned(p, eb)) return fail(GDN_ERR_MISALIGNED, "%s: a tensor is not aligned to its element size", fn);
     if (!aligned(positions, 4) || !aligned(inv_freq, 4))
         return fail(GDN_ERR_MISALIGNED, "%s: positions and inv_freq must be 4-byte aligned", fn);
-    // in place is the input's own rows; q and k, or q_out and k_out, may be slices of
-    // the same rows, so that their extents interlace
+    // An output lies on its input's own rows (in place) or apart from it; on the other
+    // input only where it is in place and the two are slices of the same rows (a block
+    // writes its rows of the one while others read theirs of the other); on the other
+    // output as slices of the same rows.
     const bool q_in = q_out == q && st.q_out_b == st.q_b && st.q_out_t == st.q_t;
     const bool k_in = k && k_out == k && st.k_out_b == st.k_b && st.k_out_t == st.k_t;
-    if ((!q_in && (over(q_out, qo_b, q, q_b) || over(q_out, qo_b, k, k_b))) ||
-        (!k_in && (over(k_out, ko_b, k, k_b) || over(k_out, ko_b, q, q_b))) ||
+    if ((!q_in && over(q_out, qo_b, q, q_b)) || (!k_in && over(k_out, ko_b, k, k_b)) ||
+        (over(q_out, qo_b, k, k_b) &&
+         !(q_in && slices(q, st.q_b, st.q_t, qd, k, st.k_b, st.k_t, kd, B, T, eb))) ||
+        (over(k_out, ko_b, q, q_b) &&
+         !(k_in && slices(k, st.k_b, st.k_t, kd, q, st.q_b, st.q_t, qd, B, T, eb))) ||
         (over(q_out, qo_b, k_out, ko_b) &&
          !slices(q_out, st.q_out_b, st.q_out_t, qd, k_out, st.k_out_b, st.k_out_t, kd, B, T, eb)))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s: an output overlaps another tensor without being in place", fn);

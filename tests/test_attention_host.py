@@ -223,3 +223,45 @@ def test_outputs_of_the_same_rows(lib):
             assert rotary(lib, **change) == INVALID, change
     finally:
         gdn.force_launch_failures(0)
+
+
+# wider rows [q | k | rest] of 4 + 2 heads of 64 and 64 more, and their slices' strides
+ROWS = (3 * 448, 448)
+
+
+@pytest.mark.parametrize("change", [
+    # q in place, the keys on its rows or partly on them, k_out apart
+    dict(q=P(0), k=P(0), q_out=P(0), strides=(768, 256, 384, 128, 768, 256, 384, 128)),
+    dict(q=P(0), k=P(0) + 256, q_out=P(0), strides=(768, 256, 768, 256, 768, 256, 384, 128)),
+    dict(q=P(0), k=P(0) + 510, q_out=P(0), strides=ROWS * 3 + (384, 128)),
+    dict(q=P(0), k=P(0) - 254, q_out=P(0), strides=ROWS * 3 + (384, 128)),
+    # keys between the queries' rows, whose rows do not keep to the gaps
+    dict(q=P(0), k=P(0) + 512, q_out=P(0), strides=ROWS + (3 * 500, 500) + ROWS + (384, 128)),
+    # and the other way round: k in place, the queries on its rows, q_out apart
+    dict(k=P(1), q=P(1), k_out=P(1), strides=(768, 256, 768, 256, 768, 256, 768, 256)),
+    dict(k=P(1), q=P(1) - 256, k_out=P(1), strides=(768, 256, 768, 256, 768, 256, 768, 256)),
+    dict(k=P(1), q=P(1) + 254, k_out=P(1), strides=ROWS * 2 + (768, 256) + ROWS),
+    dict(k=P(1), q=P(1) + 256, k_out=P(1), strides=(3 * 500, 500) + ROWS + (768, 256) + ROWS),
+])
+def test_one_in_place_on_the_other_input(lib, change):
+    """Of q and k the one that is turned in place may not lie on the other one, which
+    is read at the same time."""
+    gdn.force_launch_failures(1)
+    try:
+        assert rotary(lib, **change) == INVALID
+    finally:
+        gdn.force_launch_failures(0)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=P(0), k=P(0) + 512, q_out=P(0), strides=ROWS * 3 + (384, 128)),
+    dict(q=P(0) + 256, k=P(0), q_out=P(0) + 256, strides=ROWS * 3 + (384, 128)),
+    dict(k=P(1) + 512, q=P(1), k_out=P(1) + 512, strides=ROWS * 2 + (768, 256) + ROWS),
+    dict(k=P(1), q=P(1) + 256, k_out=P(1), strides=ROWS * 2 + (768, 256) + ROWS),
+])
+def test_one_in_place_of_slices_of_the_same_rows(lib, change):
+    gdn.force_launch_failures(1)
+    try:
+        assert rotary(lib, **change) == CUDA, lib.gdn_last_error()
+    finally:
+        gdn.force_launch_failures(0)
