@@ -305,8 +305,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
 #pragma unroll
                     for (int d = 1; d < LR; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const int e2 = top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 10;
-                    const float up = copysignf(__uint_as_float((uint32_t)(127 + 10 - e2) << 23), a.scale);
+                    // (an infinite row is made NaN: scores of -inf would count as masked ones)
+                    const bool finite = top < INFINITY;
+                    const int e2 = finite ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 10;
+                    const float up = copysignf(__uint_as_float(finite ? (uint32_t)(127 + 10 - e2) << 23 : 0x7fc00000u), a.scale);
                     st_shared16(place(warp_row + (i0 + i) * RI + lane / LR), pack2<__half>(v[0] * up, v[1] * up),
                                 pack2<__half>(v[2] * up, v[3] * up), pack2<__half>(v[4] * up, v[5] * up),
                                 pack2<__half>(v[6] * up, v[7] * up));

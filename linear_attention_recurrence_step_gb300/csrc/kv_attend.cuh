@@ -362,9 +362,11 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
 #pragma unroll
             for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             // the power of two that brings the largest into [2^10, 2^11), with the
-            // scale's sign
-            const int e = top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 10;
-            const float up = copysignf(__uint_as_float((uint32_t)(127 + 10 - e) << 23), a.scale);
+            // scale's sign; a NaN if it is infinite, for scores of -inf would count as
+            // masked ones (NaNs are passed on as they are)
+            const bool finite = top < INFINITY;
+            const int e = finite ? max((int)(__float_as_uint(top) >> 23) - 127, -100) : 10;
+            const float up = copysignf(__uint_as_float(finite ? (uint32_t)(127 + 10 - e) << 23 : 0x7fc00000u), a.scale);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const float x = v[i] * up;

@@ -28,3 +28,52 @@ def test_rotary_with_one_in_place(dev, layout):  # noqa: F811
         assert torch.equal(o.q, plain.q) and torch.equal(o.k, plain.k)
         other = parts(w)[1 - which]
         assert torch.equal(other, parts(wide)[1 - which]) and torch.equal(w[:, :, 6], wide[:, :, 6])
+
+
+def filled(dev, pages, H, page, D, seed, dtype=torch.bfloat16):  # noqa: F811
+    """A cache of `pages` pages of normal values, and as it stands its keys and values."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    cache = gdn.gdn_kv_cache(pages, H, page, D, device=dev)
+    kv = torch.randn(1, pages * page, 2, H, D, generator=g, device=dev).to(dtype)
+    kv[:, :, 0, :, 5] = -kv[:, :, 0, :, 5].abs() - 1  # (one channel of the keys has one sign)
+    gdn.gdn_kv_append(kv[:, :, 0], kv[:, :, 1], torch.arange(pages * page, device=dev, dtype=torch.int32)[None], cache)
+    return cache, g
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,L", [(1, 1), (1, 2), (2, 2), (1, 300), (70, 70), (70, 71), (150, 150), (150, 2000)])
+@pytest.mark.parametrize("scale,window", [(0.1, 0), (-0.1, 1), (0.0, 2)])
+def test_infinite_queries_of_few_tokens(dev, dtype, D, T, L, scale, window):  # noqa: F811
+    """A row that holds an infinity is NaN whatever the scores' sign, when it sees one
+    token or many; the others are what they were, and one that sees nothing stays 0.
+
+    Rows of a warp move their softmax reference together, so without one of them the
+    others' weights may be rounded elsewhere.  Their scores keep their bits: per call a
+    weight is off by 2^-12 (f16; float32 calls 2^-23), by 2^-18 from the difference to
+    the reference and its power, and L/16 sums by 2^-23 each, together 2^-16: below
+    2^-11.5 (float32: 2^-15) of the largest value, which is at most 6 of normal ones.
+    Twice that, and a rounding of each y; log-sum-exps below 2^6 twice by 2^-17."""
+    H, G, page = 2, 2, 16
+    cache, g = filled(dev, -(-L // page), H, page, D, T)
+    q = torch.randn(1, T, H * G, D, generator=g, device=dev).to(dtype)
+    table = torch.arange(-(-L // page), device=dev, dtype=torch.int32)[None]
+
+    def call(q, n):
+        return gdn.gdn_kv_attention(q, cache, table, torch.tensor([n], device=dev, dtype=torch.int32), scale=scale,
+                                    window=window, return_lse=True)
+
+    clean = call(q, L)
+    assert not bool(clean.y.isnan().any())
+    bad = torch.zeros(1, T, H * G, dtype=torch.bool, device=dev)
+    for i, t in enumerate({0, min(1, T - 1), T - 1}):
+        for h, x in ((i, float("inf")), (3, -float("inf"))):
+            q[0, t, h, 5], bad[0, t, h] = x, True
+    o = call(q, L)
+    assert bool(o.y[bad].isnan().all()) and bool(o.lse[bad].isnan().all())
+    by = 6 * 2.0 ** (-14 if dtype == torch.float32 else -10.5) + torch.finfo(dtype).eps * clean.y.double().abs()
+    assert bool(((o.y.double() - clean.y.double()).abs() <= by)[~bad].all())
+    assert bool(((o.lse - clean.lse).abs() <= 2.0 ** -16)[~bad].all())
+    if T > 1:  # one token less: the first row sees none
+        o = call(q, T - 1)
+        assert bool((o.y[0, 0] == 0).all()) and bool((o.lse[0, 0] == -float("inf")).all())
