@@ -77,3 +77,24 @@ def test_infinite_queries_of_few_tokens(dev, dtype, D, T, L, scale, window):  # 
     if T > 1:  # one token less: the first row sees none
         o = call(q, T - 1)
         assert bool((o.y[0, 0] == 0).all()) and bool((o.lse[0, 0] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 1 << 30])
+@pytest.mark.parametrize("T,lengths", [(9, [4, 0, 9, 300, 5]), (70, [2, 0, 70, 69, 1000]), (300, [2, 299, 700, 1, 0])])
+def test_largest_windows(dev, dtype, window, T, lengths):  # noqa: F811
+    """A window past every token is none, also for sequences with fewer tokens than
+    queries, whose first ones stand before the first token."""
+    H, G, page, D = 2, 2, 32, 64
+    width = 32
+    cache, g = filled(dev, width, H, page, D, T)
+    B = len(lengths)
+    q = torch.randn(B, T, H * G, D, generator=g, device=dev).to(dtype)
+    table = torch.arange(width, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    at = torch.tensor(lengths, device=dev, dtype=torch.int32)
+    want = gdn.gdn_kv_attention(q, cache, table, at, return_lse=True)
+    got = gdn.gdn_kv_attention(q, cache, table, at, window=window, return_lse=True)
+    assert torch.equal(got.y, want.y) and torch.equal(got.lse, want.lse)
+    for b, n in enumerate(lengths):  # rows that see a token are not empty
+        seen = torch.arange(T, device=dev) >= T - n
+        assert torch.equal(got.lse[b].isfinite().all(-1), seen) and torch.equal((got.y[b] != 0).flatten(1).any(-1), seen)
