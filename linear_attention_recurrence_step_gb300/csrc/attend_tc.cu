@@ -178,6 +178,12 @@ struct TcArgs {
     int inject_expiry;
 };
 
+// The first token that a query at position pos sees.  (Positions before the first
+// token count as -1: that less a window of up to 2^31 - 1 stays in 32 bits.)
+__device__ __forceinline__ int first_seen(const AttendArgs &a, int pos) {
+    return a.window > 0 ? max(max(pos, -1) - a.window + 1, 0) : 0;
+}
+
 // Row block rb of sequence b: the tokens [lo, hi) that any of its rows sees, and the
 // steps over them (one at least where there are rows: those that see nothing are
 // written too).
@@ -192,11 +198,9 @@ template <int D, int TILES> __device__ __forceinline__ TcSpan tc_span(const Atte
     s.len = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.width << a.page_shift);
     s.r0 = rb * L::kRows;
     s.rows = min(max(s.n * G - s.r0, 0), L::kRows);
-    // (a position before the first token sees nothing, wherever; -1 less a window of up
-    // to 2^31 - 1 stays in 32 bits)
-    const int first = max(s.len - s.n + s.r0 / G, -1), last = max(s.len - s.n + (s.r0 + max(s.rows, 1) - 1) / G, -1);
-    s.hi = last + 1;
-    s.lo = a.window > 0 ? max(first - a.window + 1, 0) : 0;
+    const int first = s.len - s.n + s.r0 / G, last = s.len - s.n + (s.r0 + max(s.rows, 1) - 1) / G;
+    s.hi = max(last + 1, 0);
+    s.lo = first_seen(a, first);
     s.step0 = s.lo / L::kTok;
     s.steps = s.rows == 0 ? 0 : max((s.hi + L::kTok - 1) / L::kTok - s.step0, 1);
     return s;
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
         // ================================================ softmax warps
         const int t = warp >> 2, row = tid & 127, r = r0 + t * kTcTile + row;  // tile, row in it, row of the sequence
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-        const int pos = max(len - n + r / G, -1);
+        const int pos = len - n + r / G;
         // D/8 lanes share a row of q or y, eight channels each
         constexpr int LR = D / 8, RI = 32 / LR;
         const int piece = lane % LR, warp_row = t * kTcTile + (row & ~31);
@@ -324,11 +328,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
         named_bar_sync(1, 32 * (4 * L::kTiles + 1));  // with the issuer: the queries are there
 
         // visible tokens of the row: [row_lo, row_hi)
-        const int row_hi = min(pos + 1, hi), row_lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        const int row_hi = min(pos + 1, hi), row_lo = first_seen(a, pos);
         // tokens that every row of the tile sees
         const int tr0 = r0 + t * kTcTile, tr1 = r0 + min(rows, (t + 1) * kTcTile) - 1;
-        const int all_hi = len - n + tr0 / G + 1;
-        const int all_lo = a.window > 0 ? max(max(len - n + tr1 / G, -1) - a.window + 1, 0) : 0;
+        const int all_hi = len - n + tr0 / G + 1, all_lo = first_seen(a, len - n + tr1 / G);
         int ids = t < tiles ? pages_of(0) : -1;
         for (int j = 0; j < steps && t < tiles; ++j) {
             const int buf = tiles == 2 ? t : j & 1;

@@ -103,14 +103,13 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int p, int row_bloc
     s.rows = min(max(s.n * G - r0, 0), unit_rows);
     s.lo = s.hi = s.lo_all = s.hi_all = s.chunk0 = s.chunks = 0;
     if (s.rows == 0) return s;
-    // (a position before the first token sees nothing, wherever; -1 less a window of up
-    // to 2^31 - 1 stays in 32 bits)
-    const int pos0 = max(s.len - s.n + r0 / G, -1), pos1 = max(s.len - s.n + (r0 + s.rows - 1) / G, -1);
-    s.hi = pos1 + 1;
-    s.hi_all = pos0 + 1;
+    const int pos0 = s.len - s.n + r0 / G, pos1 = s.len - s.n + (r0 + s.rows - 1) / G;
+    s.hi = max(pos1 + 1, 0);
+    s.hi_all = max(pos0 + 1, 0);
     if (a.window > 0) {
-        s.lo = max(pos0 - a.window + 1, 0);
-        s.lo_all = max(pos1 - a.window + 1, 0);
+        // (positions before the first token are below 0: no difference that leaves 32 bits)
+        s.lo = pos0 >= a.window ? pos0 - a.window + 1 : 0;
+        s.lo_all = pos1 >= a.window ? pos1 - a.window + 1 : 0;
     }
     s.chunk0 = s.lo / kChunk;
     s.chunks = max((s.hi + kChunk - 1) / kChunk - s.chunk0, 1);  // (a row that sees nothing is written too)
@@ -415,7 +414,7 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * b + 2 * t4 + e;
                 cr[b][e] = sc[row];
-                pos[b][e] = max(s.len - s.n + (s.rb * ROWS + row) / G, -1);
+                pos[b][e] = s.len - s.n + (s.rb * ROWS + row) / G;
                 off[b][e] = -1e30f;
                 sum[b][e] = 0.f;
             }
