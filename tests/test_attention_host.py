@@ -265,3 +265,67 @@ def test_one_in_place_of_slices_of_the_same_rows(lib, change):
         assert rotary(lib, **change) == CUDA, lib.gdn_last_error()
     finally:
         gdn.force_launch_failures(0)
+
+
+def neighbours(values):
+    """The values, every midpoint between neighbours, and one float32 step on either side
+    of all of them (at least 0), with the index of the nearest value: of a midpoint the
+    even one."""
+    x, want = [], []
+    for i, v in enumerate(values):
+        x.append(v)
+        want.append(i)
+        if i + 1 < len(values):
+            x.append((v + values[i + 1]) / 2)
+            want.append(i if i % 2 == 0 else i + 1)
+    x, want = torch.tensor(x, dtype=torch.float64), torch.tensor(want)
+    exact = x.float()
+    assert torch.equal(exact.double(), x)
+    up, down = (torch.nextafter(exact, torch.full_like(exact, s)) for s in (math.inf, 0.0))
+    i = torch.arange(len(x)) // 2
+    return torch.cat([exact, up, down]), torch.cat([want, torch.where(torch.arange(len(x)) % 2 == 1, i + 1, i), i])
+
+
+def test_reference_of_scales():
+    """The tests' quantiser gives each scale byte where its value, a midpoint or a float
+    beside one says so, as torch's own e4m3 does."""
+    import attention_reference as ref
+    assert torch.equal(torch.tensor(ref.E4M3), torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float())
+    top, want = neighbours([6 * v for v in ref.E4M3])  # a group's largest, whose sixth the scale is
+    u = torch.zeros(len(top), 1, 16)
+    u[:, 0, 3] = top
+    byte = ref.quantise(u, None)[1][:, 0, 0]
+    assert torch.equal(byte, want)
+    sixth = (top.double() / 6).float()
+    exact = sixth.double() * 6 == top.double()
+    assert int(exact.sum()) >= 2 * 127 - 1
+    assert torch.equal(byte[exact].to(torch.uint8), sixth[exact].to(torch.float8_e4m3fn).view(torch.uint8))
+    assert int(ref.quantise(torch.full((1, 1, 16), 1e9), None)[1]) == 126  # the largest scale, no further
+
+
+@pytest.mark.parametrize("byte", [1, 8, 56, 61, 126])
+def test_reference_of_codes(byte):
+    """... and each code, of both signs, under scales that are subnormal, one, odd and the largest."""
+    import attention_reference as ref
+    s = ref.E4M3[byte]
+    table = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+    x, want = neighbours([v * s for v in table])
+    keep = x <= 6 * s
+    x, want = x[keep], want[keep]
+    u = torch.zeros(2, len(x), 1, 16)
+    u[..., 0] = 6 * s  # fixes the group's scale
+    u[0, :, 0, 5], u[1, :, 0, 5] = x, -x
+    code, sb = ref.quantise(u, None)
+    assert bool((sb == byte).all())
+    code = code[..., 0, 5]
+    assert torch.equal(code[0], want) and torch.equal(code[1] % 8, want) and bool((code[1] >= 8)[x > 0].all())
+    assert torch.equal(ref.values(ref.quantise(u, None)[0], sb, None)[0, :, 0, 5],
+                       torch.tensor(table, dtype=torch.float64)[want] * s)
+
+
+def test_reference_of_infinities():
+    """A NaN is held as zero, an infinity as the largest value of the largest scale."""
+    import attention_reference as ref
+    u = torch.tensor([math.nan, math.inf, -math.inf, 1.0] + [0.0] * 12).view(1, 1, 16)
+    code, byte = ref.quantise(u, None)
+    assert code[0, 0, :4].tolist() == [0, 7, 15, 0] and int(byte) == 126

@@ -98,3 +98,38 @@ def test_largest_windows(dev, dtype, window, T, lengths):  # noqa: F811
     for b, n in enumerate(lengths):  # rows that see a token are not empty
         seen = torch.arange(T, device=dev) >= T - n
         assert torch.equal(got.lse[b].isfinite().all(-1), seen) and torch.equal((got.y[b] != 0).flatten(1).any(-1), seen)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,T,G,H,L", [
+    (2, 1, 4, 2, 500), (2, 3, 5, 2, 500), (120, 1, 3, 8, 60), (70, 5, 2, 8, 60),   # few rows: cut, whole
+    (2, 70, 1, 2, 500), (2, 99, 2, 2, 500), (2, 67, 1, 2, 4000), (1, 150, 2, 1, 4000)])  # tiles: whole, cut
+def test_rows_at_odd_addresses(dev, dtype, D, B, T, G, H, L):  # noqa: F811
+    """Queries whose rows begin at odd elements, and outputs that do, give the bits of
+    dense ones; nothing beside the outputs is written."""
+    page = 64
+    width = -(-L // page)
+    cache, g = filled(dev, width, H, page, D, L)
+    q = torch.randn(B, T, H * G, D, generator=g, device=dev).to(dtype)
+    table = torch.arange(width, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    lengths = torch.randint(1, L + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    lengths[0] = L
+    new = torch.randint(0, T + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    new[0] = T
+    on = torch.arange(T, device=dev) < new[:, None]
+    want = gdn.gdn_kv_attention(q, cache, table, lengths, new=new, y=torch.full_like(q, 7.0))
+    n = q.numel()
+    # a slice that begins one element into rows with odd strides; a y one element behind a boundary
+    wide = torch.full((B, T + 1, H * G * D + 33), float("nan"), device=dev, dtype=dtype)
+    odd = wide[:, :T, 1:H * G * D + 1].unflatten(-1, (H * G, D))
+    odd.copy_(q)
+    assert odd.data_ptr() % 16 != 0 and odd.stride(1) % 2 == 1
+    for x in (q, odd):
+        flat = torch.full((n + 18,), 7.0, device=dev, dtype=dtype)
+        y = flat[1:1 + n].view(q.shape)
+        assert y.data_ptr() % 16 != 0
+        gdn.gdn_kv_attention(x, cache, table, lengths, new=new, y=y)
+        assert torch.equal(y, want.y) and bool((y[~on] == 7.0).all())
+        assert bool((flat[:1] == 7.0).all()) and bool((flat[1 + n:] == 7.0).all())
+    assert torch.equal(gdn.gdn_kv_attention(odd, cache, table, lengths, new=new, y=torch.full_like(q, 7.0)).y, want.y)
