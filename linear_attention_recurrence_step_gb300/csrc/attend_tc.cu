@@ -58,6 +58,10 @@ constexpr long long kDrainCycles = 2000000000ll;
 // moves when one passes 2^14.  f16 steps end at 2^-24: weights are off by 2^-12 of
 // themselves, or by 2^-31 of the row's largest.
 constexpr float kTcBoost = 6.f, kTcMost = 14.f;
+constexpr float kTcNoScore = -FLT_MAX;  // the reference of a row that has seen nothing
+// Whether scores of a factor can reach 2^26 in powers of two: they are rounded then before
+// the reference is taken off (kv_attend.cuh).
+__device__ __forceinline__ bool far_scores(float factor, int D) { return factor * (float)D >= 0x1p26f / (2048.f * 2688.f); }
 
 template <int D, int TILES> struct Tc {
     static constexpr int kTiles = TILES;
@@ -66,7 +70,8 @@ template <int D, int TILES> struct Tc {
     static constexpr int kDqWarps = 12 - 4 * TILES;
     static constexpr uint32_t kQBytes = kRows * D * 2, kOpBytes = kTok * D * 2;  // K or V of a step
     static constexpr uint32_t kQ = 0, kK = kQBytes, kV = kK + 2 * kOpBytes, kBars = kV + 2 * kOpBytes;
-    static constexpr size_t kSmem = kBars + 256 + 1024;    // (1024: alignment)
+    static constexpr uint32_t kFactors = kBars + 256;      // f32 per row, where scores are rounded
+    static constexpr size_t kSmem = kFactors + 4 * kRows + 1024;  // (1024: alignment)
 };
 enum Bar { kKFull = 0, kVFull = 2, kKFree = 4, kVFree = 6, kSFull = 8, kPFull = 10, kODone = 12, kDrain = 14, kNever = 15, kBarCount = 16 };
 
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
     if (ta.inject_expiry) wait(kNever, 0);
 
     const bool softmax_warp = warp < 4 * L::kTiles;
-    float sum = 0.f, off = -1e30f;
+    float sum = 0.f, off = kTcNoScore;
     // registers where they are used: 4 x 128 at launch, as many or fewer in all
     if (softmax_warp) {
         more_registers<192>();  // (192 + 192 + 88 + 40, or 192 + 120 + 120 + 40)
@@ -333,6 +338,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
         const int tr0 = r0 + t * kTcTile, tr1 = r0 + min(rows, (t + 1) * kTcTile) - 1;
         const int all_hi = len - n + tr0 / G + 1, all_lo = first_seen(a, len - n + tr1 / G);
         int ids = t < tiles ? pages_of(0) : -1;
+        // the warp's scores are rounded: their factor is 1 then, which is far itself
+        auto factor_at = [&]() { return base + L::kFactors + 4u * threadIdx.x; };
+        if (__any_sync(0xffffffffu, far_scores(c, D))) {
+            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(factor_at()), "f"(c) : "memory");
+            c = 1.f;
+        }
         for (int j = 0; j < steps && t < tiles; ++j) {
             const int buf = tiles == 2 ? t : j & 1;
             const uint32_t s_at = lanes + 128u * (uint32_t)buf;
@@ -362,6 +373,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const TcArgs t
                     for (int i = 0; i < 32; ++i)
                         if (!((seen >> i) & 1u)) v[32 * q + i] = -INFINITY;
                 }
+            }
+            if (c == 1.f) {
+                float f;
+                asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(f) : "r"(factor_at()));
+#pragma unroll
+                for (int e = 0; e < TN; ++e) v[e] = __fmul_rn(v[e], f);
             }
             float tops[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -643,7 +660,7 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a,
     // lane / 8 of the warp's four and row lane % 8 adds them up
     const int i = i0 + lane % 8;
     const bool there = i < s.rows;
-    float ref = -1e30f, sum = 0.f, acc[D / 32];
+    float ref = kTcNoScore, sum = 0.f, acc[D / 32];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
 #pragma unroll 2

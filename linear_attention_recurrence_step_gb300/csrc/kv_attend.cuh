@@ -17,6 +17,9 @@
 // Softmax.  2^(x - reference) needs no maximum as long as the reference is near:
 // it moves (and sum and O with it) only when some x is 2^slack above it, which
 // one vote per tile finds, so most tiles take no reduction over tokens at all.
+// x - reference is one operation on a score and its factor.  Where x can reach 2^26, and
+// a float32 reference can be off by more than the slack, a warp rounds scores to x
+// first, as the reference is.
 //
 // Layout.  The order of the contracted index is free as long as both operands
 // use it: a lane's four elements of a k-step are neighbours in its row of the
@@ -57,6 +60,10 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // f16 (whose steps end at 2^-24); boost + slack stay below f16's 2^16.
 template <typename T> constexpr float kBoost = sizeof(T) == 4 ? 14.f : 6.f;
 template <typename T> constexpr float kSlack = sizeof(T) == 4 ? 1.f : 8.f;
+constexpr float kNoScore = -FLT_MAX;         // the reference of a row that has seen nothing
+// Whether scores of a factor can reach 2^26 in powers of two: products of queries below
+// 2^11 and keys of up to 2688, times D.
+__device__ __forceinline__ bool far_scores(float factor, int D) { return factor * (float)D >= 0x1p26f / (2048.f * 2688.f); }
 
 // Eights of query rows per unit (four would take 255 registers: 32 rows of 16
 // sequences of up to 8192 tokens 75 us, two units of 16 rows 70), and the blocks of
@@ -406,6 +413,7 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
         // of the lane's query rows 8b + 2 t4 + e: the score's factor, the last
         // token seen, the reference less the boost, the sum
         float2 cr[NB][2];
+        bool rounded = false;  // the warp's scores are: their factor is 1 then, which is far itself
         int pos[NB][2];
         float off[NB][2], sum[NB][2];
 #pragma unroll
@@ -414,10 +422,16 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * b + 2 * t4 + e;
                 cr[b][e] = sc[row];
+                rounded = rounded || far_scores(cr[b][e].x, D);
                 pos[b][e] = s.len - s.n + (s.rb * ROWS + row) / G;
-                off[b][e] = -1e30f;
+                off[b][e] = kNoScore;
                 sum[b][e] = 0.f;
             }
+        rounded = __any_sync(0xffffffffu, rounded);
+        if (rounded) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) cr[b][0] = cr[b][1] = make_float2(1.f, 0.f);
+        }
         float o[NB][MT][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -516,6 +530,17 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
                             if (!(i ? in1 : in0) || tok > pos[b][e & 1] ||
                                 (a.window > 0 && tok <= pos[b][e & 1] - a.window))
                                 x[i][b][e] = -INFINITY;
+                    }
+            }
+            if (cr[0][0].x == 1.f) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = sc[8 * b + 2 * t4 + (e & 1)];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (x[i][b][e] != -INFINITY) x[i][b][e] = fmaf(x[i][b][e], f.x, x[i][b][e] * f.y);
                     }
             }
             auto power = [&](float v, int b, int e) {
@@ -731,7 +756,7 @@ attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int rows) {
     const Span s = span_of(a, p, row_blocks, unit_rows);
     if (row >= s.rows) return;
     const int later = part_begin<BLOCKS>(b0, W) < x0;  // the unit is not the first of block b0
-    float m = -1e30f, l = 0.f, acc[PER];
+    float m = kNoScore, l = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
     for (int q = b0 + warp; q <= b1; q += kJoinWarps) {

@@ -133,3 +133,44 @@ def test_rows_at_odd_addresses(dev, dtype, D, B, T, G, H, L):  # noqa: F811
         assert torch.equal(y, want.y) and bool((y[~on] == 7.0).all())
         assert bool((flat[:1] == 7.0).all()) and bool((flat[1 + n:] == 7.0).all())
     assert torch.equal(gdn.gdn_kv_attention(odd, cache, table, lengths, new=new, y=torch.full_like(q, 7.0)).y, want.y)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("B,T,G,L", [(2, 1, 7, 4000), (2, 2, 7, 1500), (120, 1, 7, 150), (2, 11, 7, 700), (2, 20, 7, 4000),
+                                     (1, 30, 7, 4000)])
+def test_scores_of_any_size(dev, dtype, D, sign, B, T, G, L):  # noqa: F811
+    """Rows whose scores reach from ones to 1e37 side by side, the best ones below 0 and
+    above, on three tokens far apart: the softmax of the exact scores.
+
+    A row's scores are one size times 1, 2, 4 or 8, so from 1e3 on all but the best weigh
+    nothing and a score's own error moves nothing.  Weights are off by 2^-12 (f16) or 2^-23, and
+    at scores of at most 8 by twice 8 40 2^-23 + 2^-20 < 2^-13; values are at most 6.
+    Log-sum-exps are off by a few roundings of the score."""
+    H, page, at = 8 if B > 2 else 2, 32, torch.tensor([3, L // 2, L - T - 5])
+    g = torch.Generator().manual_seed(D + L)
+    k, v = torch.zeros(1, L, H, D), torch.randn(1, L, H, D, generator=g)
+    best, other = ((-1, (-2, -4)), (-8, (-2, -4)))[sign < 0]
+    k[0, :, :, 5] = torch.tensor(other)[torch.randint(0, 2, (L, H), generator=g)].float()
+    k[0, at, :, 5] = float(best)
+    width = -(-L // page)
+    cache = gdn.gdn_kv_cache(width, H, page, D, device=dev)
+    slots = torch.arange(L, device=dev, dtype=torch.int32)
+    gdn.gdn_kv_append(k.to(dev), v.to(dev), slots[None], cache)
+    kr, vr = (t.double().cpu() for t in gdn.gdn_kv_read(cache, slots, dtype=torch.float32))
+    sizes = torch.tensor([1.0, 1e3, 1e6, 1e9, 1e20, 1e30, 1e37])
+    q = torch.zeros(B, T, H * G, D)
+    q[..., 5] = sign * sizes.repeat(H)
+    q = q.to(dtype)
+    table = torch.arange(width, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    o = gdn.gdn_kv_attention(q.to(dev), cache, table, torch.full((B,), L, device=dev, dtype=torch.int32), scale=1.0,
+                             return_lse=True)
+    b = B - 1
+    assert torch.equal(o.y, o.y[:1].expand_as(o.y)) or B <= 2
+    x = torch.einsum("thgd,lhd->thgl", q[b].double().unflatten(1, (H, G)), kr)
+    x = x.masked_fill((torch.arange(L) > L - T + torch.arange(T)[:, None])[:, None, None], -float("inf"))
+    want, lse = torch.einsum("thgl,lhd->thgd", x.softmax(-1), vr).flatten(1, 2), x.logsumexp(-1).flatten(1, 2)
+    by = 6 * (2.0 ** -11 if dtype != torch.float32 else 0.0) + 6 * 2.0 ** -13 + torch.finfo(dtype).eps * want.abs()
+    assert bool(((o.y[b].cpu().double() - want).abs() <= by).all()), float((o.y[b].cpu().double() - want).abs().max())
+    assert bool(((o.lse[b].cpu().double() - lse).abs() <= lse.abs() * 2.0 ** -20 + 2.0 ** -12).all())
