@@ -72,12 +72,15 @@ int64_t attend_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int6
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t s);
 cudaError_t launch_attend_f16(const AttendArgs &a, cudaStream_t s);
-// The tcgen05 form (attend_tc.cu), for f16 and bf16 calls of many query rows;
-// its wait-expiry flag.
+// The tcgen05 form (attend_tc.cuh, a translation unit per type), for f16 and bf16 calls
+// of many query rows; its wait-expiry flag.
 bool attend_tc_rows(int64_t units, int64_t rows);
 bool attend_takes_tc(DType dt, const AttendArgs &a);
 int64_t attend_tc_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D);
 cudaError_t launch_attend_tc(DType dt, const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_tc_bf16(const AttendArgs &a, cudaStream_t s);
+cudaError_t launch_attend_tc_f16(const AttendArgs &a, cudaStream_t s);
+cudaError_t attend_tc_wait_flag(unsigned **flag);
 cudaError_t attend_tc_take_wait_flag(unsigned *was_set);
 
 }  // namespace gdn

@@ -174,3 +174,85 @@ def test_scores_of_any_size(dev, dtype, D, sign, B, T, G, L):  # noqa: F811
     by = 6 * (2.0 ** -11 if dtype != torch.float32 else 0.0) + 6 * 2.0 ** -13 + torch.finfo(dtype).eps * want.abs()
     assert bool(((o.y[b].cpu().double() - want).abs() <= by).all()), float((o.y[b].cpu().double() - want).abs().max())
     assert bool(((o.lse[b].cpu().double() - lse).abs() <= lse.abs() * 2.0 ** -20 + 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D,B,T,G,H", [(128, 16, 17, 4, 8), (128, 29, 64, 4, 8), (256, 16, 17, 4, 8), (64, 29, 50, 4, 8),
+                                       (128, 25, 64, 4, 4)])  # whole units, and parts of 43690 tokens
+@pytest.mark.parametrize("drift", [0.0, 12.0])
+def test_sums_over_long_contexts(dev, dtype, D, B, T, G, H, drift):  # noqa: F811
+    """131072 tokens whose values have one sign: sums that only grow, where every unit cut
+    off is seen.
+
+    Beside the weights' 2^-12 and twice the scores' 40 2^-23 of sum |q k| and 2^-20 (as in
+    attention_bounds), a sum is off by 2^-23 at each addition to it since it was last set
+    down: 16384/16 and 16 more, below 2^-13 + 2^-19.  The outputs' rounding goes either
+    way: in the mean over 8704 and more of them it leaves 2^-16 at most (five standard
+    deviations of 2^-11 / sqrt(3 8704))."""
+    L, page = 131072, 128
+    g = torch.Generator(device=dev).manual_seed(D + B)
+    cache = gdn.gdn_kv_cache(L // page, H, page, D, device=dev)
+    at = torch.arange(L, device=dev, dtype=torch.int32)
+    for i in range(0, L, 16384):
+        k, v = (torch.randn(1, 16384, H, D, generator=g, device=dev) for _ in range(2))
+        k[0, :, :, 5] += drift * at[i:i + 16384, None] / L  # (later tokens weigh more: the reference moves)
+        gdn.gdn_kv_append(k, v.abs() + 1, at[None, i:i + 16384], cache)
+    q = (0.05 * torch.randn(B, T, H * G, D, generator=g, device=dev))
+    q[..., 5] = 1.0
+    q = q.to(dtype)
+    table = torch.arange(L // page, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    lengths = torch.full((B,), L, device=dev, dtype=torch.int32)
+    flat = torch.full((q.numel() + 8,), 7.0, device=dev, dtype=dtype)
+    o = gdn.gdn_kv_attention(q, cache, table, lengths, scale=1.0, return_lse=True)
+    for b, h in ((0, 0), (B - 1, H - 1)):
+        keys, vals = (t[:, h].double() for t in gdn.gdn_kv_read(cache, at, dtype=torch.float32))
+        rows = q[b, :, h * G:(h + 1) * G].double().reshape(-1, D)
+        x = rows @ keys.T
+        pos = L - T + torch.arange(T, device=dev).repeat_interleave(G)
+        x = x.masked_fill(torch.arange(L, device=dev) > pos[:, None], -float("inf"))
+        want, lse = x.softmax(-1) @ vals, x.logsumexp(-1)
+        size = rows.norm(dim=-1).max() * keys.norm(dim=-1).max()
+        ds = float(size) * 40 * 2.0 ** -23 + 2.0 ** -20
+        err = o.y[b, :, h * G:(h + 1) * G].double().reshape(-1, D) - want
+        by = want * (2.0 ** -12 + 2.0 ** -13 + 2.0 ** -19 + 2 * ds + torch.finfo(dtype).eps / 2) + vals.sum(0) * 2.0 ** -31
+        assert bool((err.abs() <= by).all()), float((err.abs() - by).max())
+        if dtype == torch.float16:
+            assert abs(float((err / want).mean())) <= 2.0 ** -13 + 2.0 ** -19 + 2.0 ** -16 + 2.0 ** -20
+        assert bool(((o.lse[b, :, h * G:(h + 1) * G].double().reshape(-1) - lse).abs() <= ds + lse.abs() * 2.0 ** -22).all())
+    # y at an odd address: the same bits, nothing beside it
+    y = flat[1:1 + q.numel()].view(q.shape)
+    gdn.gdn_kv_attention(q, cache, table, lengths, scale=1.0, y=y)
+    assert torch.equal(y, o.y) and bool((flat[:1] == 7.0).all()) and bool((flat[1 + q.numel():] == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [17, 50])
+def test_rows_of_long_contexts(dev, T):  # noqa: F811
+    """Over 40000 tokens: a row with an infinity, rows that are not there, a window that
+    ends before the last sums are set down, sequences of other lengths."""
+    H, G, D, page, B, L = 8, 4, 128, 128, 29, 40000
+    width = -(-L // page)
+    cache, g = filled(dev, width, H, page, D, T)
+    q = torch.randn(B, T, H * G, D, generator=g, device=dev).half()
+    q[1, 2, 3, 7], q[2, T - 1, 0, 0] = float("inf"), float("nan")
+    table = torch.arange(width, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    lengths = torch.randint(0, L + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    new = torch.randint(0, T + 1, (B,), generator=g, device=dev, dtype=torch.int32)
+    lengths[:4], new[:4] = L, T
+    new[3] = T - 3
+    for window in (0, 20000):
+        y = torch.full_like(q, 7.0)
+        o = gdn.gdn_kv_attention(q, cache, table, lengths, new=new, window=window, y=y, return_lse=True)
+        bad = torch.zeros(B, T, H * G, dtype=torch.bool, device=dev)
+        bad[1, 2, 3] = bad[2, T - 1, 0] = True
+        assert torch.equal(y.isnan().all(-1), bad) and torch.equal(y.isnan().any(-1), bad)
+        on = torch.arange(T, device=dev) < new[:, None]
+        assert bool((y[~on] == 7.0).all())
+        # rows in calls of 16 tokens' worth of few rows: the other kernel
+        for b, t in ((0, 0), (0, T - 1), (3, T - 4), (1, 5)):
+            n = lengths[b:b + 1] - new[b] + t + 1
+            one = gdn.gdn_kv_attention(q[b:b + 1, t:t + 1], cache, table[b:b + 1], n.int(), window=window, return_lse=True)
+            # values of at most 6, two calls each off by 2^-12 of the weights, 2^-13 of the sums
+            # and 2^-13 of the scores, and rounded
+            by = 6 * 2 * (2.0 ** -12 + 2.0 ** -12) + 2.0 ** -10 * one.y.float().abs()
+            assert bool(((one.y.float() - y[b:b + 1, t:t + 1].float()).abs() <= by).all())
+            assert bool(((one.lse - o.lse[b:b + 1, t:t + 1]).abs() <= 2.0 ** -12).all())
