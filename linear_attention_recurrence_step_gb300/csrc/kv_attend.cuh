@@ -60,6 +60,13 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // f16 (whose steps end at 2^-24); boost + slack stay below f16's 2^16.
 template <typename T> constexpr float kBoost = sizeof(T) == 4 ? 14.f : 6.f;
 template <typename T> constexpr float kSlack = sizeof(T) == 4 ? 1.f : 8.f;
+// The tensor cores cut a sum off where they add to it, so sums of terms of one sign fall
+// short by half a unit of their last place per 16 tokens of a warp: by 1.6e-4 of them over
+// 131072 tokens of a block.  Where a block can have more (of f16 calls; of bf16 calls 8
+// times as many), that would pass half of y's rounding, and products are added outside
+// (LONG).
+template <typename T> constexpr int64_t kLongTokens = 131072;
+template <> constexpr int64_t kLongTokens<__nv_bfloat16> = 1048576;
 constexpr float kNoScore = -FLT_MAX;         // the reference of a row that has seen nothing
 // Whether scores of a factor can reach 2^26 in powers of two: products of queries below
 // 2^11 and keys of up to 2688, times D.
@@ -189,7 +196,7 @@ __device__ __forceinline__ void write_row(const AttendArgs &a, const Span &s, in
     if (d0 == 0 && a.lse) a.lse[tok * a.Hq + hq] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
-template <typename T, int D, int NB>
+template <typename T, int D, int NB, bool LONG>
 __global__ void __launch_bounds__(kThreads, resident(NB, D, sizeof(T) == 4))
 attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
     using S = Smem<T, D, NB>;
@@ -656,11 +663,11 @@ attend_kernel(const AttendArgs a, int pairs, int row_blocks, bool whole) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             float (&acc)[4] = o[b][4 * v8 + q];
-                            if constexpr (TERMS == 1) {
+                            if constexpr (TERMS == 1 && !LONG) {
                                 mma_f16(acc, af, pb[0][i][b][0], pb[0][i][b][1]);
                             } else {
                                 float y[4] = {};
-                                mma_f16(y, af, pb[TERMS - 1][i][b][0], pb[TERMS - 1][i][b][1]);
+                                if (TERMS == 2) mma_f16(y, af, pb[TERMS - 1][i][b][0], pb[TERMS - 1][i][b][1]);
                                 mma_f16(y, af, pb[0][i][b][0], pb[0][i][b][1]);
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) acc[c] += y[c];
@@ -806,14 +813,20 @@ cudaError_t launch_tdn(const AttendArgs &a, cudaStream_t s) {
     constexpr int ROWS = S::kRows;
     const int64_t all = a.T * (a.Hq / a.H), rb = (all + ROWS - 1) / ROWS, pairs = a.B * rb, units = pairs * a.H;
     constexpr size_t smem = S::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     const int blocks = kSms * resident(NB, D, sizeof(T) == 4);
-    if (!cut(pairs, a.H, blocks)) {
+    const bool whole = !cut(pairs, a.H, blocks);
+    // the most tokens of a unit that a block can have, of a part where units are cut (in the
+    // mean over the blocks, which have equal parts)
+    const int64_t row = (int64_t)a.width << a.page_shift;
+    const int64_t tokens = whole ? row : std::min<int64_t>(row, units * (row / kChunk + 1) / blocks * kChunk);
+    const auto kernel = sizeof(T) == 2 && tokens > kLongTokens<T> ? attend_kernel<T, D, NB, sizeof(T) == 2> : attend_kernel<T, D, NB, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (whole) {
         if (units > INT32_MAX) return cudaErrorInvalidConfiguration;
-        return launch_dependent(attend_kernel<T, D, NB>, (unsigned)units, kThreads, smem, s, a, (int)pairs, (int)rb, true);
+        return launch_dependent(kernel, (unsigned)units, kThreads, smem, s, a, (int)pairs, (int)rb, true);
     }
-    e = launch_dependent(attend_kernel<T, D, NB>, (unsigned)blocks, kThreads, smem, s, a, (int)pairs, (int)rb, false);
+    e = launch_dependent(kernel, (unsigned)blocks, kThreads, smem, s, a, (int)pairs, (int)rb, false);
     if (e != cudaSuccess) return e;
     const int rows = (int)std::min<int64_t>(all, ROWS);
     return launch_dependent(attend_join_kernel<T, D, NB>, (unsigned)(units * rows), 32 * kJoinWarps, 0, s, a, (int)pairs,

@@ -256,3 +256,40 @@ def test_rows_of_long_contexts(dev, T):  # noqa: F811
             by = 6 * 2 * (2.0 ** -12 + 2.0 ** -12) + 2.0 ** -10 * one.y.float().abs()
             assert bool(((one.y.float() - y[b:b + 1, t:t + 1].float()).abs() <= by).all())
             assert bool(((one.lse - o.lse[b:b + 1, t:t + 1]).abs() <= 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("dtype,L", [(torch.float16, 262144), (torch.bfloat16, 2 ** 21)])
+@pytest.mark.parametrize("D,B,G,H", [(64, 120, 4, 8), (128, 95, 4, 8), (256, 60, 4, 8), (64, 77, 12, 8), (128, 58, 12, 8),
+                                     (256, 39, 12, 8), (128, 90, 4, 8)])  # units that are whole, and one call that is cut
+def test_sums_of_few_rows(dev, dtype, L, D, B, G, H):  # noqa: F811
+    """Values of one sign over more tokens than the tensor cores' own sums are good for.
+
+    As in test_sums_over_long_contexts, with sums that are added outside: L/64 terms to a
+    warp, each time by half a unit, 2^-24, either way, so 2^-24 sqrt(L/64 / 3) in the mean
+    and five times that at most, below 2^-14.  The pages repeat, so the softmax is that over
+    the first ones."""
+    n, page = 8192, 128
+    g = torch.Generator(device=dev).manual_seed(D + B)
+    cache = gdn.gdn_kv_cache(n // page, H, page, D, device=dev)
+    at = torch.arange(n, device=dev, dtype=torch.int32)
+    k, v = (torch.randn(1, n, H, D, generator=g, device=dev) for _ in range(2))
+    gdn.gdn_kv_append(k, v.abs() + 1, at[None], cache)
+    q = (0.05 * torch.randn(B, 1, H * G, D, generator=g, device=dev)).to(dtype)
+    table = (torch.arange(L // page, device=dev, dtype=torch.int32) % (n // page)).expand(B, -1).contiguous()
+    lengths = torch.full((B,), L, device=dev, dtype=torch.int32)
+    o = gdn.gdn_kv_attention(q, cache, table, lengths, scale=1.0, return_lse=True)
+    mean = []
+    for b, h in ((0, 0), (B // 2, 3), (B - 1, H - 1)):
+        keys, vals = (t[:, h].double() for t in gdn.gdn_kv_read(cache, at, dtype=torch.float32))
+        rows = q[b, 0, h * G:(h + 1) * G].double()
+        x = rows @ keys.T
+        want, lse = x.softmax(-1) @ vals, x.logsumexp(-1) + torch.log(torch.tensor(L / n, dtype=torch.float64))
+        ds = float(rows.norm(dim=-1).max() * keys.norm(dim=-1).max()) * 40 * 2.0 ** -23 + 2.0 ** -20
+        err = o.y[b, 0, h * G:(h + 1) * G].double() - want
+        by = want * (2.0 ** -12 + 2.0 ** -14 + 2 * ds + torch.finfo(dtype).eps / 2) + vals.sum(0) * (L / n) * 2.0 ** -31
+        assert bool((err.abs() <= by).all()), float((err.abs() - by).max())
+        assert bool(((o.lse[b, 0, h * G:(h + 1) * G].double() - lse).abs() <= ds + lse.abs() * 2.0 ** -22).all())
+        mean.append((err / want).flatten())
+    mean = torch.cat(mean)
+    # the outputs' rounding: five standard deviations of their mean
+    assert abs(float(mean.mean())) <= 2.0 ** -14 + 5 * torch.finfo(dtype).eps / 2 / (3 * mean.numel()) ** 0.5
