@@ -678,8 +678,8 @@ gdn_status gdn_kv_append(const void *k, const void *v, const int32_t *slots,
 
 /*
  * gdn_kv_read -- the keys and values of N slots ([N] int32), as dense [N,H,D]
- * dtype, rounded to nearest-even.  The rows of a slot that is none are not
- * written.  One kernel.
+ * dtype: the float32 product, rounded to nearest-even.  The rows of a slot that is
+ * none are not written.  One kernel.
  */
 gdn_status gdn_kv_read(const void *cache, const int32_t *slots,
                        const float *k_scale, const float *v_scale, void *k,

@@ -109,6 +109,8 @@ def rotary_frequencies(R: int, base: float = 10000.0, *, scaling: str | None = N
         raise ValueError('scaling must be None, "linear", "base", "parts" or "parts_scaled"')
     if not factor >= 1.0:
         raise ValueError("factor must be at least 1")
+    if not base > (1.0 if scaling == "parts_scaled" else 0.0):
+        raise ValueError('base must be above 0, and above 1 for "parts_scaled"')
     i = torch.arange(0, R, 2, dtype=torch.float64)
     scale = 1.0
     if scaling == "base" and R > 2:
@@ -117,7 +119,7 @@ def rotary_frequencies(R: int, base: float = 10000.0, *, scaling: str | None = N
     if scaling == "linear":
         f = f / factor
     if scaling in ("parts", "parts_scaled"):
-        if not trained or not 0 < low < high:
+        if not trained or trained < 0 or not 0 < low < high:
             raise ValueError('"parts" needs trained > 0 and 0 < low < high')
         if scaling == "parts":
             keep = (trained * f / (2 * math.pi) - low) / (high - low)

@@ -329,3 +329,12 @@ def test_reference_of_infinities():
     u = torch.tensor([math.nan, math.inf, -math.inf, 1.0] + [0.0] * 12).view(1, 1, 16)
     code, byte = ref.quantise(u, None)
     assert code[0, 0, :4].tolist() == [0, 7, 15, 0] and int(byte) == 126
+
+
+@pytest.mark.parametrize("wrong", [
+    dict(base=0.0), dict(base=-2.0), dict(base=math.nan), dict(base=1.0, scaling="parts_scaled", factor=2.0, trained=100),
+    dict(scaling="parts", factor=2.0, trained=-5), dict(scaling="parts_scaled", factor=2.0, trained=-5),
+    dict(scaling="parts", factor=2.0, trained=100, low=4.0, high=2.0), dict(scaling="linear", factor=math.nan)])
+def test_rotary_frequencies_refuse(wrong):
+    with pytest.raises(ValueError, match="must be|needs"):
+        gdn.rotary_frequencies(64, **wrong)
