@@ -18,10 +18,13 @@ int64_t attend_tc_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t H, i
 }
 
 // The rows of a (sequence, key head) from which they go here and not to
-// kv_attend.cuh's kernel: 16 sequences of up to 8192 tokens and 8 heads take 79 us
-// here with 32 to 128 rows, there 72 (32 rows), 78 (48), 108 (64) and 172 (128); one
-// sequence, which has to be joined here, 22 to 23 us here, there 14 (64 rows), 22
-// (128 and 256).
+// kv_attend.cuh's kernel.  16 sequences of 2048 to 8192 tokens, 8 heads of 128: here 79 to
+// 82 us with 32 to 128 rows; there 72 (32 rows), 78 (48), 108 (64) and 172 (128) where
+// sequences bring half of their rows in the mean, 83, 116, 146 and 242 where they bring
+// all.  Heads of 64: here 65, there 52, 74, 91 and 142; of 256: here 152, there 179, 233,
+// 291 and 532.  One sequence of 8192, which has to be joined here, heads of 64, 128 and
+// 256: here 20, 27 and 43 us with 32 to 128 rows; there 19, 28 and 55 (64 rows), 29, 38 and
+// 86 (128).
 bool attend_tc_rows(int64_t units, int64_t rows) { return rows > (2 * units >= kTcSms ? 48 : 64); }
 bool attend_takes_tc(DType dt, const AttendArgs &a) { return dt != DType::F32 && attend_tc_rows(a.B * a.H, a.T * (a.Hq / a.H)); }
 

@@ -2,9 +2,9 @@
 // (prompts), on tcgen05.
 //
 // A unit is up to 256 query rows (two tiles of 128; one tile for heads of 256, and
-// where a sequence has no more rows) of one sequence and key head.  A CTA takes a unit, or, where there are few, an equal
-// part of its tokens (a second kernel joins the parts, in order), TN = 128 tokens
-// (64 for heads of 256) at a time.  Roles:
+// where a sequence has no more rows) of one sequence and key head.  A CTA takes a unit,
+// or, where there are few, an equal part of its tokens (a second kernel joins the parts,
+// in order), TN = 128 tokens (64 for heads of 256) at a time.  Roles:
 //   dequant warps  codes from global memory, a step ahead in registers, to exact
 //                  f16 (code times scale, fp4.cuh) in shared memory: K and V as
 //                  panels of 64 channels x TN tokens, 128-byte rows, 128-byte
@@ -23,11 +23,11 @@
 // Per 128 x 128 x 128 step of a tile: 2 x 512 cycles of products, 16384
 // exponentials and 64 KB through shared memory by the products (512 + 256
 // cycles), 32 KB of operands written (256 cycles, no bank conflicts).  Measured:
-// 2048 tokens over 8192, 32 heads of 128 on 4 of the cache, in 190 us (1.27
-// PFLOP/s of products, 0.66 of a library product's rate), 369 over 16384: 1.4 us a
-// step of two tiles, and 9 us a unit for its queries, first step and output.  The
-// products and the dequant warps share the shared memory, which is what bounds
-// the steps.
+// 2048 tokens over 8192, 32 heads of 128 on 8 of the cache, in 191 us (1.26
+// PFLOP/s of products, 0.66 of a library product's rate), 197 with cold caches, 369 over
+// 16384: 1.4 us a step of two tiles, and 9 us a unit for its queries, first step and
+// output.  The products and the dequant warps share the shared memory, which is what
+// bounds the steps.
 //
 // Registers: 192 for a softmax thread, so that a step's 128 scores stay in them.
 // Spills there cost most of all (106 bytes of them: 249 us for 193).
@@ -802,7 +802,10 @@ TcPlan tc_plan(int64_t B, int64_t rows, int64_t H, int64_t D) {
     TcPlan p{B * ((rows + unit_rows - 1) / unit_rows) * H, 0, 1, (int)((std::min(rows, unit_rows) + 7) / 8 * 8)};
     // Units of 1.5 times the SMs on are left whole: cut, they would be dealt out
     // little more evenly (256 over 152 SMs: 112 steps instead of 118), and have to
-    // be joined.  Fewer are cut, into one part an SM in all, or two of two tiles: 256
+    // be joined.  (So for lengths that differ by four times or so; whole units take as long
+    // as the longest: 64 rows of 15 sequences of 1000 tokens and of one of 131072 1165 us,
+    // of 3 and one, which are cut, 224.)  Fewer are cut, into one part an SM in all, or two
+    // of two tiles: 256
     // rows of one sequence of 8192 tokens and 8 heads 54 us whole, 23 cut; 32 to 128
     // rows of 16 sequences of up to 8192 tokens 79 us whole, 81 in two parts each and
     // 88 in four.

@@ -34,9 +34,10 @@
 // to run.  Units that fill the GPU by themselves are taken whole, one by a block.
 //
 // Bound by issue (62 % of the slots; half of the instructions dequantise), then by
-// memory: one token of 8 sequences of 131072 (8 key heads of 128, 1.2 GB) 222 us, 5.4
-// TB/s; of 32 sequences of up to 8192 (189 MB) 54 us.  With query rows on the wide
-// side of the products, as usual, the first took 371 us.
+// memory: one token of 8 sequences of 131072 (8 key heads of 128, 1.2 GB) 223 us, 5.4
+// TB/s; of 32 sequences of up to 8192 (189 MB) 51 us, 52 with cold caches; float32 calls
+// 321 and 69.  With query rows on the wide side of the products, as usual, the first took
+// 371 us.
 #pragma once
 
 #include <algorithm>
@@ -72,8 +73,8 @@ constexpr float kNoScore = -FLT_MAX;         // the reference of a row that has 
 // 2^11 and keys of up to 2688, times D.
 __device__ __forceinline__ bool far_scores(float factor, int D) { return factor * (float)D >= 0x1p26f / (2048.f * 2688.f); }
 
-// Eights of query rows per unit (four would take 255 registers: 32 rows of 16
-// sequences of up to 8192 tokens 75 us, two units of 16 rows 70), and the blocks of
+// Eights of query rows per unit (four would take 255 registers: 32 rows, heads of 128, of
+// 16 sequences of up to 8192 tokens 75 us, two units of 16 rows 70), and the blocks of
 // such units that an SM holds, by registers and shared memory.
 constexpr int eights_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
 constexpr int resident(int NB, int D, bool f32) {
@@ -802,7 +803,10 @@ attend_join_kernel(const AttendArgs a, int pairs, int row_blocks, int rows) {
 }
 
 // A call is cut along its tokens while its units do not fill the GPU by themselves:
-// then equal parts are worth the second kernel.  Tokens of up to 4096, 8 key heads:
+// then equal parts are worth the second kernel.  That is so for lengths that differ by
+// four times or so; a call that is not cut takes as long as its longest unit: 94 sequences
+// of 1000 tokens and one of 131072, one new token each, 850 us, and 76 with one sequence
+// less, which is cut.  Tokens of 1024 to 4096, 8 key heads of 128:
 // 512 units of 8 rows 57 us cut, 64 whole; 1024 100 and 97; 2048 180 and 157; 384 units
 // of 16 rows 90 and 101; 512 94 and 78; 1024 161 and 127.
 bool cut(int64_t pairs, int64_t H, int blocks) { return pairs <= kMaxPairs && pairs * H < blocks; }

@@ -7,11 +7,12 @@
 // whole turns by itself, and the upper 32 bits are the fraction, off by 2^-32
 // of a turn and 2^-53 of inv_freq per step at most.
 //
-// Bound by memory: every element is read once and written once (84 MB of 4096
-// tokens of 40 heads of 128: 15.3 us from and to L2, 25.7 with cold caches).  A block
-// makes the sines of its tokens once, in shared memory, and uses them for all heads of
-// q and k; a thread takes the same piece of all of the block's tokens, so that where
-// it lies in a token is worked out once and their loads are in flight together.
+// Every element is read once and written once: 84 MB of 4096 tokens of 40 heads of 128
+// in 15.6 us from and to L2, 20.8 with cold caches (4.0 TB/s; 12.4 by the bytes), bound by
+// waits for a token's position and sines in front of its loads.  A block makes the sines
+// of its tokens once, in shared memory, and uses them for all heads of q and k; a thread
+// takes the same piece of all of the block's tokens, so that where it lies in a token is
+// worked out once and their loads are in flight together.
 #include "attend.h"
 #include "pieces.cuh"
 
@@ -126,7 +127,8 @@ cudaError_t launch_tb(const RotaryArgs &a, cudaStream_t s) {
 // Four tokens per block once blocks of one fill the SMs some four times over (and
 // their sines fit the shared memory that needs no asking).  40 heads of 128: 2048
 // tokens 8.8 us with one per block, 10.2 with four; 4096 15.3 and 16.7; 8192 34.6 and
-// 30.2; 16384 64.2 and 55.7.
+// 30.2; 16384 64.2 and 55.7.  Measured on such wide tokens: of 5 heads, which leave most
+// of a block idle, 4864 tokens take 12.1 us with one per block and 4865 7.6 with four.
 template <typename T, int VEC>
 cudaError_t launch_t(const RotaryArgs &a, int sm_count, cudaStream_t s) {
     const bool many = a.B * a.T > (int64_t)(sm_count > 0 ? sm_count : 152) * 32 && a.R <= 2048;
