@@ -705,15 +705,15 @@ gdn_status gdn_kv_read(const void *cache, const int32_t *slots,
  *   workspace    at least gdn_kv_attention_workspace_size bytes, 16-byte
  *                aligned, one per call in flight; not looked at when that call
  *                gives 16
- * Scores (of less than 2^127), sums, maxima and outputs are float32, rounded
- * once (where a tensor core cuts a sum off instead, less than half of that
- * rounding of sum p |v| in all); the products take the cache's values exactly, the
- * queries to 2^-23 of their row's largest channel (if that is 2^-100 at least) and
- * the probabilities rounded to f16 (two f16 terms for float32 calls).  A query
- * row that holds an infinity or a NaN has NaN for y and lse if it sees a token.
- * What stands in places that no token sees does not matter.  Results do not
- * change from run to run.  One kernel, or two where a call's tokens are shared out
- * among blocks.
+ * Scores (of less than 2^127), maxima and sums are float32, outputs are rounded
+ * once.  What tensor cores cut off sums is at most 2^-12 of sum p |v| in f16
+ * calls, 2^-9 in bf16 and 2^-22 in float32 calls, however many tokens there are.
+ * The products take the cache's values exactly, the queries to 2^-23 of their
+ * row's largest channel (if that is 2^-100 at least) and the probabilities
+ * rounded to f16 (two f16 terms for float32 calls).  A query row that holds an
+ * infinity or a NaN has NaN for y and lse if it sees a token.  What stands in
+ * places that no token sees does not matter.  Results do not change from run to
+ * run.  One kernel, or two where a call's tokens are shared out among blocks.
  */
 size_t gdn_kv_attention_workspace_size(int64_t B, int64_t T, int64_t Hq,
                                        int64_t H, int64_t D);

@@ -293,3 +293,29 @@ def test_sums_of_few_rows(dev, dtype, L, D, B, G, H):  # noqa: F811
     mean = torch.cat(mean)
     # the outputs' rounding: five standard deviations of their mean
     assert abs(float(mean.mean())) <= 2.0 ** -14 + 5 * torch.finfo(dtype).eps / 2 / (3 * mean.numel()) ** 0.5
+
+
+@pytest.mark.parametrize("B,H", [(29, 8), (25, 4)])  # whole units, parts
+def test_waits_of_long_contexts(dev, B, H):  # noqa: F811
+    """Waits that run out where sums are set down: NaN, the flag, and the next call runs."""
+    T, G, D, page, L = 50, 4, 64, 128, 65536
+    cache, g = filled(dev, L // page, H, page, D, 1)
+    q = torch.randn(B, T, H * G, D, generator=g, device=dev).half()
+    table = torch.arange(L // page, device=dev, dtype=torch.int32).expand(B, -1).contiguous()
+    lengths = torch.full((B,), L, device=dev, dtype=torch.int32)
+    call = lambda: gdn.gdn_kv_attention(q, cache, table, lengths, return_lse=True)  # noqa: E731
+    clean = call()
+    torch.cuda.synchronize()
+    assert not gdn.wait_status()
+    gdn.set_wait_bound(1)
+    gdn.inject_wait_expiry(True)
+    try:
+        bad = call()
+        torch.cuda.synchronize()
+    finally:
+        gdn.inject_wait_expiry(False)
+        gdn.set_wait_bound(0)
+    assert gdn.wait_status() and not gdn.wait_status()
+    assert bool(bad.y.isnan().all()) and bool(bad.lse.isnan().all())
+    again = call()
+    assert torch.equal(again.y, clean.y) and torch.equal(again.lse, clean.lse) and bool(again.y.isfinite().all())
